@@ -55,7 +55,7 @@ typedef struct ihipStream_t* hipStream_t; /* HIP's own stream handle type */
 enum skgemm_status {
   SKGEMM_OK = 0,
   SKGEMM_EINVAL = -1, /* null pointer, negative size, split_k not in {1,2,4,8} */
-  SKGEMM_EALIGN = -2, /* a pointer is not 16-byte aligned                      */
+  SKGEMM_EALIGN = -2, /* a pointer or a stride is not aligned as stated        */
   SKGEMM_ESHAPE = -3, /* N % 16, K % (32*split_k) (bf16) or K % (128*split_k)
                          (MXFP4) non-zero, or a size above the limits below   */
   SKGEMM_ENOMEM = -4, /* split-K workspace could not be allocated, or it would
@@ -212,6 +212,41 @@ SKGEMM_API int skgemm_mxfp8_batched(const void* Wq8, const void* Wscale, const v
                                     int T, int N, int K, int split_k, int L, size_t wq8_stride,
                                     size_t wscale_stride, size_t x_stride, size_t c_stride,
                                     hipStream_t stream);
+
+/*
+ * The operators around the quantised layers and the language-model head.
+ * Rows may be further apart than their length: *_stride is the distance of two
+ * rows in BYTES. Sizes of zero enqueue nothing and succeed.
+ */
+enum skgemm_format {
+  SKGEMM_BF16 = 0,
+  SKGEMM_I8 = 1,   /* two's complement codes in -127..127, one FP32 scale a row */
+  SKGEMM_E4M3 = 2, /* OCP E4M3FN codes, one FP32 scale a row                    */
+  SKGEMM_F32 = 3
+};
+#define SKGEMM_MAX_H (1 << 15) /* skgemm_rmsnorm */
+
+/*
+ * skgemm_rmsnorm: h = X + R (in FP32, from here on unrounded), R_out = bf16(h),
+ *   y = h / sqrt(mean(h^2) + eps) * G over the H elements of a row,
+ *   Y = bf16(y), or the codes of y / y_scale[t] with y_scale[t] = max|y| / 127
+ *   (I8, rounded to nearest even) or max|y| / 448 (E4M3).
+ *   X, R, R_out  bf16 [T, H]; R null: h = X; R_out null: not stored. R_out may
+ *                be X or R (same stride); other overlaps are not supported.
+ *   G            bf16 [H], null for ones.
+ *   Y            bf16, int8 or uint8 [T, H]; y_scale float [T] (8-bit formats).
+ *   H % 8 == 0, H <= SKGEMM_MAX_H (SKGEMM_ESHAPE); 1e-30 <= eps < inf.
+ *   Pointers are 16-byte aligned (y_scale 4), bf16 strides multiples of 16 and
+ *   8-bit Y strides multiples of 8 (SKGEMM_EALIGN).
+ * A row of zeros has scale 0 and codes 0. A row that holds an infinity or a NaN
+ * (in h) has NaN outputs: bf16 NaN, or a NaN scale whose codes mean nothing.
+ * Finite rows of any size are right: the sum of squares is rescaled where
+ * FP32 would overflow.
+ */
+SKGEMM_API int skgemm_rmsnorm(const void* X, const void* R, const void* G, void* R_out, void* Y,
+                              float* y_scale, int T, int H, float eps, int out_format,
+                              size_t x_stride, size_t r_stride, size_t r_out_stride,
+                              size_t y_stride, hipStream_t stream);
 
 /*
  * skgemm_reserve: make sure the workspace of (current device, stream) can

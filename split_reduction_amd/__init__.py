@@ -31,6 +31,9 @@ SKGEMM_ESCRATCH = -6
 KNOBS = {"kind": 0, "stream": 1, "shape": 2, "fold": 3, "cluster_c": 4, "wg_per_cu": 5,
          "pdefer": 6, "owner_wait": 7, "handoff": 8}
 
+# Element formats (include/skgemm.h, enum skgemm_format)
+FORMATS = {"bf16": 0, "i8": 1, "e4m3": 2, "f32": 3}
+
 _lib = None
 
 
@@ -66,6 +69,7 @@ def _declare(lib):
         "skgemm_bf16_noalloc": [vp, vp, vp, i, i, i, i, st],
         "skgemm_bf16_e4m3": [vp, vp, vp, ctypes.c_float, i, i, i, i, st],
         "skgemm_bf16_chain": [vp, vp, vp, vp, i, i, i, st],
+        "skgemm_rmsnorm": [vp, vp, vp, vp, vp, vp, i, i, ctypes.c_float, i, sz, sz, sz, sz, st],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -132,6 +136,48 @@ def _ptr(a, nbytes: int = 0, what: str = "argument") -> int:
     if have < nbytes:
         raise SkgemmError(SKGEMM_EINVAL, f"{what}: holds {have} bytes, the call needs {nbytes}")
     return a.data_ptr()
+
+
+def _rows(a, rows: int, row_bytes: int, stride, what: str, esize: int = 0):
+    """(address, row stride in bytes) of a matrix whose rows are `row_bytes` long
+    and contiguous, `stride` bytes apart (None: as the tensor's own rows are, or
+    dense for an address). The tensor must be on the GPU, hold elements of
+    `esize` bytes (0: any) and reach to the end of the last row."""
+    if a is None or isinstance(a, int):
+        return a or 0, row_bytes if stride is None else stride
+    if a.device.type != "cuda":
+        raise SkgemmError(SKGEMM_EINVAL, f"{what}: a tensor on {a.device}, not on the GPU")
+    size = a.element_size()
+    if esize and size != esize:
+        raise SkgemmError(SKGEMM_EINVAL, f"{what}: elements of {size} bytes, the call's have {esize}")
+    n = a.numel() * size
+    if a.is_contiguous():
+        if stride is None:
+            stride = a.stride(0) * size if a.dim() == 2 and rows > 1 and a.stride(0) * size >= row_bytes else row_bytes
+    elif a.dim() == 2 and (a.stride(1) == 1 or a.shape[1] == 1) and a.stride(0) >= 0:
+        own = a.stride(0) * size
+        if stride is None:
+            stride = own
+        elif stride != own and rows > 1:
+            raise SkgemmError(SKGEMM_EINVAL, f"{what}: rows {own} bytes apart, not {stride}")
+        if n:
+            n = (a.shape[0] - 1) * own + a.shape[1] * size
+        if a.shape[1] * size < row_bytes and rows > 0:
+            raise SkgemmError(SKGEMM_EINVAL, f"{what}: rows of {a.shape[1] * size} bytes, the call needs {row_bytes}")
+    else:
+        raise SkgemmError(SKGEMM_EINVAL, f"{what}: rows are not contiguous")
+    need = (rows - 1) * max(stride, 0) + row_bytes if rows > 0 and row_bytes > 0 else 0
+    if n < need:
+        raise SkgemmError(SKGEMM_EINVAL, f"{what}: holds {n} bytes, the call needs {need}")
+    return a.data_ptr(), stride
+
+
+def _format(name) -> int:
+    if isinstance(name, str):
+        if name not in FORMATS:
+            raise SkgemmError(SKGEMM_EINVAL, f"unknown format {name!r}, one of {sorted(FORMATS)}")
+        return FORMATS[name]
+    return int(name)
 
 
 def _n(*dims) -> int:
@@ -244,6 +290,21 @@ def skgemm_mxfp8_batched(Wq8, Wscale, X, C, T: int, N: int, K: int, split_k: int
                                       T, N, K, split_k, L, wq8_stride, wscale_stride, x_stride, c_stride,
                                       _stream(stream))
     _check(code, "skgemm_mxfp8_batched")
+
+
+def skgemm_rmsnorm(X, R, G, R_out, Y, y_scale, T: int, H: int, eps: float, out_format="bf16", x_stride=None,
+                   r_stride=None, r_out_stride=None, y_stride=None, stream=None) -> None:
+    """Y = (X + R) / rms(X + R) * G as bf16, or as "i8" / "e4m3" codes with a
+    scale for each row; R_out = bf16(X + R). R, G and R_out may be None."""
+    f = _format(out_format)
+    ysize = 2 if f == 0 else 1
+    x, xs = _rows(X, T, 2 * H, x_stride, "X", 2)
+    r, rs = _rows(R, T, 2 * H, r_stride, "R", 2)
+    ro, ros = _rows(R_out, T, 2 * H, r_out_stride, "R_out", 2)
+    y, ys = _rows(Y, T, ysize * H, y_stride, "Y", ysize)
+    code = lib().skgemm_rmsnorm(x, r, _ptr(G, 2 * _n(H), "G"), ro, y, _ptr(y_scale, 4 * _n(T), "y_scale"), T, H, eps, f,
+                                xs, rs, ros, ys, _stream(stream))
+    _check(code, "skgemm_rmsnorm")
 
 
 def skgemm_mxfp8_dequant(Wq8, Wscale, W_out, N: int, K: int, stream=None) -> None:

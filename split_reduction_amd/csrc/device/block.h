@@ -1,0 +1,53 @@
+// Reductions over a wavefront and over a workgroup, in a fixed order.
+#pragma once
+
+#include "wave.h"
+
+namespace skg {
+
+template <int OFF>
+__device__ __forceinline__ float xred_max(float v) {
+  if constexpr (OFF >= 16) {
+    int x = __float_as_int(v);
+    auto p = (OFF == 32) ? __builtin_amdgcn_permlane32_swap(x, x, false, false)
+                         : __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    return fmaxf(__int_as_float(p[0]), __int_as_float(p[1]));
+  } else {
+    return fmaxf(v, __int_as_float(xshfl_dpp<OFF>(__float_as_int(v))));
+  }
+}
+
+// The largest of a wave's 64 values, in every lane (NaN is passed over).
+__device__ __forceinline__ float butterfly_max(float v) {
+  v = xred_max<32>(v);
+  v = xred_max<16>(v);
+  v = xred_max<8>(v);
+  v = xred_max<4>(v);
+  v = xred_max<2>(v);
+  v = xred_max<1>(v);
+  return v;
+}
+
+// The sum of `a` and the largest `b` over a workgroup of up to 16 waves, in
+// every thread. `part` holds 32 floats of LDS that nobody else uses until the
+// next barrier after this call.
+__device__ __forceinline__ void block_sum_max(float& a, float& b, float* part) {
+  a = butterfly_sum(a);
+  b = butterfly_max(b);
+  const int waves = (int)(blockDim.x >> 6);
+  if (waves == 1) return;
+  const int wave = (int)(threadIdx.x >> 6);
+  if ((threadIdx.x & 63) == 0) {
+    part[wave] = a;
+    part[16 + wave] = b;
+  }
+  __syncthreads();
+  a = part[0];
+  b = part[16];
+  for (int i = 1; i < waves; ++i) {
+    a += part[i];
+    b = fmaxf(b, part[16 + i]);
+  }
+}
+
+}  // namespace skg

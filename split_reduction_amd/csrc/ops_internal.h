@@ -1,0 +1,31 @@
+// Internal interface between the C-ABI layer (ops_api.hip) and the kernels of
+// the operators around the layers and the head.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace skg {
+
+struct NormParams {
+  const uint8_t* x;      // bf16 [T, H]
+  const uint8_t* r;      // bf16 [T, H] or null
+  const uint8_t* g;      // bf16 [H] or null
+  uint8_t* r_out;        // bf16 [T, H] or null
+  uint8_t* y;            // bf16 or 8-bit codes [T, H]
+  float* y_scale;        // [T] (8-bit codes)
+  size_t x_stride, r_stride, r_out_stride, y_stride;  // bytes
+  int T, H;
+  float eps;
+};
+
+hipError_t launch_rmsnorm(const NormParams& p, int out_format, hipStream_t s);
+
+// hip_fail and the retained error live with the other entry points (api.hip).
+int hip_fail(hipError_t e);
+// Frees the workspaces of ops_api.hip; part of skgemm_release.
+int release_ops_workspaces();
+int device_cus();
+
+}  // namespace skg

@@ -1,0 +1,190 @@
+// Root-mean-square norm with the residual's addition and a bf16 or 8-bit
+// output (skgemm_rmsnorm).
+//
+//   h = x + r,  y = h * rstd * g,  rstd = 1 / sqrt(mean(h^2) + eps)
+//
+// One pass: a row stays in the registers of one workgroup between its loads
+// and its stores, so each input is read once and each output written once.
+// The codes need max|y|, which would be a second reduction after rstd; but
+// rstd > 0 is common to the row, so max|y| = rstd * max|h g| and the codes are
+//   y / (max|y| / 127) = h g * (127 / max|h g|),
+// free of rstd: sum(h^2) and max|h g| meet in one reduction behind one barrier.
+//
+// Bound by memory: 7 bytes an element (x, r, R_out, codes) and about 10 vector
+// operations.
+
+#include "device/block.h"
+#include "device/pack.h"
+#include "ops_internal.h"
+#include "skgemm.h"
+
+namespace skg {
+
+namespace {
+
+// The low byte of x + 1.5 * 2^23 is x rounded to the nearest even integer in
+// two's complement (|x| < 2^22): one addition, no conversion.
+__device__ __forceinline__ uint32_t i8_pack4(float a, float b, float c, float d) {
+  constexpr float kMagic = 12582912.0f;
+  const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(b + kMagic), __float_as_uint(a + kMagic), 0x0C0C0400u);
+  const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(d + kMagic), __float_as_uint(c + kMagic), 0x0C0C0400u);
+  return lo | (hi << 16);
+}
+
+template <int OUT>
+constexpr float top_code() {
+  return OUT == SKGEMM_I8 ? 127.0f : 448.0f;
+}
+
+// VPT: vectors of 8 elements a thread holds; thread i takes vectors i,
+// i + blockDim, ... so that a wave's loads and stores are contiguous.
+template <int VPT, int OUT>
+__global__ __launch_bounds__(1024) void rmsnorm_kernel(NormParams p) {
+  __shared__ float part[32];
+  const size_t t = blockIdx.x;
+  const int nv = p.H >> 3;
+  const u32x4* x = reinterpret_cast<const u32x4*>(p.x + t * p.x_stride);
+  const u32x4* r = p.r != nullptr ? reinterpret_cast<const u32x4*>(p.r + t * p.r_stride) : nullptr;
+  const u32x4* g = reinterpret_cast<const u32x4*>(p.g);
+  u32x4* ro = p.r_out != nullptr ? reinterpret_cast<u32x4*>(p.r_out + t * p.r_out_stride) : nullptr;
+
+  u32x4 xv[VPT], rv[VPT], gv[VPT];
+  const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = (int)threadIdx.x + i * (int)blockDim.x;
+    const bool ok = v < nv;
+    xv[i] = ok ? x[v] : u32x4{0, 0, 0, 0};
+    rv[i] = (ok && r != nullptr) ? r[v] : u32x4{0, 0, 0, 0};
+    gv[i] = (ok && g != nullptr) ? g[v] : ones;
+  }
+  float h[VPT * 8], hg[VPT * 8];
+  float ss = 0.0f, top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      // No residual: zeros are added, which changes nothing but -0.
+      const float a = bf16_lo(xv[i][e]) + bf16_lo(rv[i][e]), b = bf16_hi(xv[i][e]) + bf16_hi(rv[i][e]);
+      h[8 * i + 2 * e] = a;
+      h[8 * i + 2 * e + 1] = b;
+      ss = fmaf(a, a, ss);
+      ss = fmaf(b, b, ss);
+    }
+    if (ro != nullptr) {
+      const int v = (int)threadIdx.x + i * (int)blockDim.x;
+      u32x4 w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = bf16_pair(h[8 * i + 2 * e], h[8 * i + 2 * e + 1]);
+      if (v < nv) ro[v] = w;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      hg[8 * i + 2 * e] = h[8 * i + 2 * e] * bf16_lo(gv[i][e]);
+      hg[8 * i + 2 * e + 1] = h[8 * i + 2 * e + 1] * bf16_hi(gv[i][e]);
+      top = fmaxf(top, fmaxf(fabsf(hg[8 * i + 2 * e]), fabsf(hg[8 * i + 2 * e + 1])));
+    }
+  block_sum_max(ss, top, part);
+  float eps = p.eps;
+  constexpr float kInf = __builtin_inff();
+  // ss or top out of FP32's range though h may be finite: take the row by a
+  // power of two and reduce again (uniform over the workgroup, rare).
+  // A NaN in ss stays: the row holds one.
+  if (ss == kInf || (top == kInf && ss == ss)) {
+    float m = 0.0f, none = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT * 8; ++i) m = fmaxf(m, fabsf(h[i]));
+    __syncthreads();
+    block_sum_max(none, m, part);
+    if (m == kInf) {
+      ss = __builtin_nanf("");
+    } else {
+      const float f = __uint_as_float((255u - (__float_as_uint(m) >> 23)) << 23);  // m * f lies in 2..4
+      eps *= f;
+      eps *= f;
+      ss = 0.0f;
+      top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float a = h[8 * i + e] * f;
+          const uint32_t w = gv[i][e >> 1];
+          hg[8 * i + e] = a * ((e & 1) ? bf16_hi(w) : bf16_lo(w));
+          ss = fmaf(a, a, ss);
+          top = fmaxf(top, fabsf(hg[8 * i + e]));
+        }
+      __syncthreads();
+      block_sum_max(ss, top, part);
+    }
+  }
+  const float rstd = 1.0f / sqrtf(ss / (float)p.H + eps);  // NaN where the row holds a NaN or infinity
+  float mul = rstd;
+  if constexpr (OUT != SKGEMM_BF16) {
+    const float scale = rstd * top / top_code<OUT>();  // in this order: top alone may be near FP32's smallest
+    if (threadIdx.x == 0) p.y_scale[t] = scale;
+    // 127 / top would pass FP32's range for a tiny top: such a row is lifted
+    // by a power of two first (exact). Zero rows get zero codes.
+    if (top < 1e-30f) {
+#pragma unroll
+      for (int i = 0; i < VPT * 8; ++i) hg[i] *= 0x1p96f;
+      top *= 0x1p96f;
+    }
+    mul = top > 0.0f && scale == scale ? top_code<OUT>() / top : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = (int)threadIdx.x + i * (int)blockDim.x;
+    float* y = hg + 8 * i;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] *= mul;
+    if (v >= nv) continue;
+    if constexpr (OUT == SKGEMM_BF16) {
+      u32x4 w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = bf16_pair(y[2 * e], y[2 * e + 1]);
+      reinterpret_cast<u32x4*>(p.y + t * p.y_stride)[v] = w;
+    } else {
+      u32x2 w;
+      if constexpr (OUT == SKGEMM_I8) {
+        w.x = i8_pack4(y[0], y[1], y[2], y[3]);
+        w.y = i8_pack4(y[4], y[5], y[6], y[7]);
+      } else {
+        w.x = e4m3_pack4(y[0], y[1], y[2], y[3]);
+        w.y = e4m3_pack4(y[4], y[5], y[6], y[7]);
+      }
+      reinterpret_cast<u32x2*>(p.y + t * p.y_stride)[v] = w;
+    }
+  }
+}
+
+template <int VPT>
+void launch_vpt(const NormParams& p, int out_format, unsigned threads, hipStream_t s) {
+  const dim3 grid((unsigned)p.T), block(threads);
+  if (out_format == SKGEMM_BF16)
+    hipLaunchKernelGGL((rmsnorm_kernel<VPT, SKGEMM_BF16>), grid, block, 0, s, p);
+  else if (out_format == SKGEMM_I8)
+    hipLaunchKernelGGL((rmsnorm_kernel<VPT, SKGEMM_I8>), grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL((rmsnorm_kernel<VPT, SKGEMM_E4M3>), grid, block, 0, s, p);
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm(const NormParams& p, int out_format, hipStream_t s) {
+  const int nv = p.H / 8;
+  int vpt = 1;
+  while (nv > vpt * 1024) vpt *= 2;  // H <= 32768: at most 4
+  const unsigned threads = (unsigned)((((nv + vpt - 1) / vpt) + 63) / 64 * 64);
+  switch (vpt) {
+    case 1: launch_vpt<1>(p, out_format, threads, s); break;
+    case 2: launch_vpt<2>(p, out_format, threads, s); break;
+    default: launch_vpt<4>(p, out_format, threads, s); break;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace skg
