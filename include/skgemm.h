@@ -224,7 +224,9 @@ enum skgemm_format {
   SKGEMM_E4M3 = 2, /* OCP E4M3FN codes, one FP32 scale a row                    */
   SKGEMM_F32 = 3
 };
-#define SKGEMM_MAX_H (1 << 15) /* skgemm_rmsnorm */
+#define SKGEMM_MAX_H (1 << 15)  /* skgemm_rmsnorm */
+#define SKGEMM_MAX_K_I8 131056  /* skgemm_i8: 2^14 K stays below 2^31 */
+#define SKGEMM_MAX_ROW_STRIDE ((size_t)1 << 22) /* skgemm_i8: W and X, bytes */
 
 /*
  * skgemm_rmsnorm: h = X + R (in FP32, from here on unrounded), R_out = bf16(h),
@@ -247,6 +249,24 @@ SKGEMM_API int skgemm_rmsnorm(const void* X, const void* R, const void* G, void*
                               float* y_scale, int T, int H, float eps, int out_format,
                               size_t x_stride, size_t r_stride, size_t r_out_stride,
                               size_t y_stride, hipStream_t stream);
+
+/*
+ * skgemm_i8: C[t, n] = x_scale[t] * w_scale[n] * sum_k Xq[t, k] * Wq[n, k].
+ *   Wq int8 [N, K], Xq int8 [T, K], w_scale float [N], x_scale float [T],
+ *   C  bf16 or float [T, N] (out_format SKGEMM_BF16 or SKGEMM_F32).
+ *   The sum is exact in 32-bit integers, so the library splits K as it likes
+ *   (no split_k argument) and every split gives the same bits; the sum is
+ *   rounded to FP32, multiplied by x_scale[t], then by w_scale[n], and rounded
+ *   once more to bf16.
+ *   K % 16 == 0, K <= SKGEMM_MAX_K_I8, N <= SKGEMM_MAX_N (SKGEMM_ESHAPE); any
+ *   N and T >= 0. K == 0 stores zeros. Wq and Xq are 16-byte aligned with
+ *   strides that are multiples of 16, at least K and at most
+ *   SKGEMM_MAX_ROW_STRIDE; C is 16-byte aligned, its stride a multiple of its
+ *   element's size and at least a row.
+ */
+SKGEMM_API int skgemm_i8(const void* Wq, const float* w_scale, const void* Xq, const float* x_scale,
+                         void* C, int T, int N, int K, int out_format, size_t w_stride,
+                         size_t x_stride, size_t c_stride, hipStream_t stream);
 
 /*
  * skgemm_reserve: make sure the workspace of (current device, stream) can

@@ -31,3 +31,9 @@ def rmsnorm_ref(x, r, g, eps):
 def row_scale(y, fmt):
     """The scale of each row's codes: the largest magnitude over the largest code."""
     return np.abs(y).max(axis=1) / TOP_CODE[fmt]
+
+
+def i8_ref(xq, x_scale, wq, w_scale):
+    """(sums, C): the exact integer products (int64) and their scaled values."""
+    s = (xq.astype(np.float64) @ wq.astype(np.float64).T)  # below 2^53: exact
+    return s.astype(np.int64), s * x_scale.astype(np.float64)[:, None] * w_scale.astype(np.float64)

@@ -69,6 +69,7 @@ def _declare(lib):
         "skgemm_bf16_noalloc": [vp, vp, vp, i, i, i, i, st],
         "skgemm_bf16_e4m3": [vp, vp, vp, ctypes.c_float, i, i, i, i, st],
         "skgemm_bf16_chain": [vp, vp, vp, vp, i, i, i, st],
+        "skgemm_i8": [vp, vp, vp, vp, vp, i, i, i, i, sz, sz, sz, st],
         "skgemm_rmsnorm": [vp, vp, vp, vp, vp, vp, i, i, ctypes.c_float, i, sz, sz, sz, sz, st],
     }
     for name, args in sig.items():
@@ -305,6 +306,23 @@ def skgemm_rmsnorm(X, R, G, R_out, Y, y_scale, T: int, H: int, eps: float, out_f
     code = lib().skgemm_rmsnorm(x, r, _ptr(G, 2 * _n(H), "G"), ro, y, _ptr(y_scale, 4 * _n(T), "y_scale"), T, H, eps, f,
                                 xs, rs, ros, ys, _stream(stream))
     _check(code, "skgemm_rmsnorm")
+
+
+def skgemm_i8(Wq, w_scale, Xq, x_scale, C, T: int, N: int, K: int, out_format=None, w_stride=None, x_stride=None,
+              c_stride=None, stream=None) -> None:
+    """C[t, n] = x_scale[t] * w_scale[n] * (Xq . Wq^T)[t, n] with exact integer
+    sums; C is bf16 or float (out_format "bf16" / "f32"; None: as C's elements
+    are, bf16 for an address)."""
+    if out_format is None:
+        out_format = 3 if not isinstance(C, int) and C is not None and C.element_size() == 4 else 0
+    f = _format(out_format)
+    size = 4 if f == 3 else 2
+    w, ws = _rows(Wq, N, K, w_stride, "Wq", 1)
+    x, xs = _rows(Xq, T, K, x_stride, "Xq", 1)
+    c, cs = _rows(C, T, size * N, c_stride, "C", size)
+    code = lib().skgemm_i8(w, _ptr(w_scale, 4 * _n(N), "w_scale"), x, _ptr(x_scale, 4 * _n(T), "x_scale"), c, T, N, K, f,
+                           ws, xs, cs, _stream(stream))
+    _check(code, "skgemm_i8")
 
 
 def skgemm_mxfp8_dequant(Wq8, Wscale, W_out, N: int, K: int, stream=None) -> None:

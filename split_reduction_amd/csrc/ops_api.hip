@@ -55,4 +55,36 @@ SKGEMM_API int skgemm_rmsnorm(const void* X, const void* R, const void* G, void*
   return e == hipSuccess ? SKGEMM_OK : skg::hip_fail(e);
 }
 
+SKGEMM_API int skgemm_i8(const void* Wq, const float* w_scale, const void* Xq, const float* x_scale,
+                         void* C, int T, int N, int K, int out_format, size_t w_stride,
+                         size_t x_stride, size_t c_stride, hipStream_t stream) {
+  if (T < 0 || N < 0 || K < 0) return SKGEMM_EINVAL;
+  if (out_format != SKGEMM_BF16 && out_format != SKGEMM_F32) return SKGEMM_EINVAL;
+  if (K % 16 != 0 || K > SKGEMM_MAX_K_I8 || N > SKGEMM_MAX_N) return SKGEMM_ESHAPE;
+  if (T == 0 || N == 0) return SKGEMM_OK;
+  if (C == nullptr || w_scale == nullptr || x_scale == nullptr) return SKGEMM_EINVAL;
+  if (K > 0 && (Wq == nullptr || Xq == nullptr)) return SKGEMM_EINVAL;
+  if (!aligned(Wq, 16) || !aligned(Xq, 16) || !aligned(C, 16) || !aligned(w_scale, 4) || !aligned(x_scale, 4))
+    return SKGEMM_EALIGN;
+  const size_t size = out_format == SKGEMM_F32 ? 4 : 2;
+  if (w_stride % 16 != 0 || x_stride % 16 != 0 || c_stride % size != 0) return SKGEMM_EALIGN;
+  if (w_stride > SKGEMM_MAX_ROW_STRIDE || x_stride > SKGEMM_MAX_ROW_STRIDE) return SKGEMM_ESHAPE;
+  if (w_stride < (size_t)K || x_stride < (size_t)K || c_stride < size * (size_t)N) return SKGEMM_EINVAL;
+  skg::I8Params p{};
+  p.w = static_cast<const uint8_t*>(Wq);
+  p.x = static_cast<const uint8_t*>(Xq);
+  p.w_scale = w_scale;
+  p.x_scale = x_scale;
+  p.c = static_cast<uint8_t*>(C);
+  p.w_stride = w_stride;
+  p.x_stride = x_stride;
+  p.c_stride = c_stride;
+  p.T = T;
+  p.N = N;
+  p.K = K;
+  p.out_f32 = out_format == SKGEMM_F32;
+  const hipError_t e = skg::launch_i8(p, stream);
+  return e == hipSuccess ? SKGEMM_OK : skg::hip_fail(e);
+}
+
 }  // extern "C"

@@ -20,6 +20,18 @@ struct NormParams {
   float eps;
 };
 
+struct I8Params {
+  const uint8_t* w;      // int8 [N, K]
+  const uint8_t* x;      // int8 [T, K]
+  const float* w_scale;  // [N]
+  const float* x_scale;  // [T]
+  uint8_t* c;            // bf16 or float [T, N]
+  size_t w_stride, x_stride, c_stride;  // bytes
+  int T, N, K;
+  int out_f32;
+};
+
+hipError_t launch_i8(const I8Params& p, hipStream_t s);
 hipError_t launch_rmsnorm(const NormParams& p, int out_format, hipStream_t s);
 
 // hip_fail and the retained error live with the other entry points (api.hip).
