@@ -224,9 +224,12 @@ enum skgemm_format {
   SKGEMM_E4M3 = 2, /* OCP E4M3FN codes, one FP32 scale a row                    */
   SKGEMM_F32 = 3
 };
-#define SKGEMM_MAX_H (1 << 15)  /* skgemm_rmsnorm */
-#define SKGEMM_MAX_K_I8 131056  /* skgemm_i8: 2^14 K stays below 2^31 */
+#define SKGEMM_MAX_ROWS (1 << 21) /* T of each call below */
+#define SKGEMM_MAX_H (1 << 15)    /* skgemm_rmsnorm */
+#define SKGEMM_MAX_K_I8 131056    /* skgemm_i8: 2^14 K stays below 2^31 */
 #define SKGEMM_MAX_ROW_STRIDE ((size_t)1 << 22) /* skgemm_i8: W and X, bytes */
+#define SKGEMM_MAX_V (1 << 20)    /* skgemm_logprobs, skgemm_logprobs_grad */
+#define SKGEMM_MAX_TOP 64
 
 /*
  * skgemm_rmsnorm: h = X + R (in FP32, from here on unrounded), R_out = bf16(h),
@@ -267,6 +270,48 @@ SKGEMM_API int skgemm_rmsnorm(const void* X, const void* R, const void* G, void*
 SKGEMM_API int skgemm_i8(const void* Wq, const float* w_scale, const void* Xq, const float* x_scale,
                          void* C, int T, int N, int K, int out_format, size_t w_stride,
                          size_t x_stride, size_t c_stride, hipStream_t stream);
+
+/*
+ * skgemm_logprobs: of a row z = scale * logits[t, :] (V values):
+ *   lse = log(sum exp(z)), logprob = z[tokens[t]] - lse,
+ *   entropy = lse - sum_j exp(z[j] - lse) z[j], and the top_k largest logits,
+ *   largest first and of equal ones the lowest index first, as
+ *   top_logprob[t, i] = z[top_ids[t, i]] - lse.
+ *   logits bf16 or float (logits_format SKGEMM_BF16 or SKGEMM_F32), 16-byte
+ *   aligned, `stride` a multiple of the element's size and at least a row.
+ *   tokens int64 [T], or null (then logprob is null too). An index below 0
+ *   marks padding: its logprob is 0. An index >= V gives a NaN logprob.
+ *   logprob, entropy, lse float [T], each may be null. top_logprob float and
+ *   top_ids int64 [T, top_k], 0 <= top_k <= min(V, SKGEMM_MAX_TOP).
+ *   0 <= V <= SKGEMM_MAX_V; scale finite and > 0 (1 / temperature). Sums are
+ *   FP32.
+ * A logit of -inf is a banned token: probability 0, nothing added to the
+ * entropy, logprob -inf. A row of nothing but -inf has lse -inf, entropy 0 and
+ * logprobs -inf. A row with a NaN or +inf has NaN for every float output and
+ * -1 for every id.
+ */
+SKGEMM_API int skgemm_logprobs(const void* logits, const int64_t* tokens, float* logprob,
+                               float* entropy, float* lse, float* top_logprob, int64_t* top_ids,
+                               int T, int V, int top_k, float scale, int logits_format,
+                               size_t stride, hipStream_t stream);
+
+/*
+ * skgemm_logprobs_grad: the gradient of sum_t g_logprob[t] logprob[t] +
+ * g_entropy[t] entropy[t] to the logits, with lse and entropy as
+ * skgemm_logprobs gave them for the same logits and scale:
+ *   p_j = exp(z_j - lse), d_logits[t, j] = scale * (g_logprob[t] *
+ *   ([j == tokens[t]] - p_j) - g_entropy[t] * p_j * (z_j - lse + entropy)).
+ *   d_logits has the logits' type and may be the logits themselves (same
+ *   stride); other overlaps are not supported. g_logprob or g_entropy null:
+ *   zeros (tokens null only with g_logprob null; entropy null only with
+ *   g_entropy null). A padding row (token < 0) has no logprob term. Rows of
+ *   nothing but -inf get zeros; a NaN lse gives a NaN row.
+ */
+SKGEMM_API int skgemm_logprobs_grad(const void* logits, const int64_t* tokens, const float* lse,
+                                    const float* entropy, const float* g_logprob,
+                                    const float* g_entropy, void* d_logits, int T, int V,
+                                    float scale, int logits_format, size_t stride, size_t d_stride,
+                                    hipStream_t stream);
 
 /*
  * skgemm_reserve: make sure the workspace of (current device, stream) can

@@ -70,6 +70,8 @@ def _declare(lib):
         "skgemm_bf16_e4m3": [vp, vp, vp, ctypes.c_float, i, i, i, i, st],
         "skgemm_bf16_chain": [vp, vp, vp, vp, i, i, i, st],
         "skgemm_i8": [vp, vp, vp, vp, vp, i, i, i, i, sz, sz, sz, st],
+        "skgemm_logprobs": [vp, vp, vp, vp, vp, vp, vp, i, i, i, ctypes.c_float, i, sz, st],
+        "skgemm_logprobs_grad": [vp, vp, vp, vp, vp, vp, vp, i, i, ctypes.c_float, i, sz, sz, st],
         "skgemm_rmsnorm": [vp, vp, vp, vp, vp, vp, i, i, ctypes.c_float, i, sz, sz, sz, sz, st],
     }
     for name, args in sig.items():
@@ -323,6 +325,43 @@ def skgemm_i8(Wq, w_scale, Xq, x_scale, C, T: int, N: int, K: int, out_format=No
     code = lib().skgemm_i8(w, _ptr(w_scale, 4 * _n(N), "w_scale"), x, _ptr(x_scale, 4 * _n(T), "x_scale"), c, T, N, K, f,
                            ws, xs, cs, _stream(stream))
     _check(code, "skgemm_i8")
+
+
+def _logits_format(logits, logits_format) -> int:
+    if logits_format is None:
+        return 3 if logits is not None and not isinstance(logits, int) and logits.element_size() == 4 else 0
+    return _format(logits_format)
+
+
+def skgemm_logprobs(logits, tokens, logprob, entropy, lse, top_logprob, top_ids, T: int, V: int, top_k: int = 0,
+                    scale: float = 1.0, logits_format=None, stride=None, stream=None) -> None:
+    """Of each row of scale * logits: the log probability of its token, the
+    entropy, the log of the sum of exponentials, and the top_k best tokens with
+    their log probabilities. Outputs may be None; tokens and ids are int64.
+    logits_format "bf16" / "f32" (None: as the elements are, bf16 for an address)."""
+    f = _logits_format(logits, logits_format)
+    size = 4 if f == 3 else 2
+    z, zs = _rows(logits, T, size * V, stride, "logits", size)
+    code = lib().skgemm_logprobs(z, _ptr(tokens, 8 * _n(T), "tokens"), _ptr(logprob, 4 * _n(T), "logprob"),
+                                 _ptr(entropy, 4 * _n(T), "entropy"), _ptr(lse, 4 * _n(T), "lse"),
+                                 _ptr(top_logprob, 4 * _n(T, top_k), "top_logprob"),
+                                 _ptr(top_ids, 8 * _n(T, top_k), "top_ids"), T, V, top_k, scale, f, zs, _stream(stream))
+    _check(code, "skgemm_logprobs")
+
+
+def skgemm_logprobs_grad(logits, tokens, lse, entropy, g_logprob, g_entropy, d_logits, T: int, V: int,
+                         scale: float = 1.0, logits_format=None, stride=None, d_stride=None, stream=None) -> None:
+    """The gradient of sum(g_logprob * logprob) + sum(g_entropy * entropy) to the
+    logits, from the lse and entropy that skgemm_logprobs gave; d_logits may be
+    the logits themselves. g_logprob or g_entropy may be None (zeros)."""
+    f = _logits_format(logits, logits_format)
+    size = 4 if f == 3 else 2
+    z, zs = _rows(logits, T, size * V, stride, "logits", size)
+    d, ds = _rows(d_logits, T, size * V, d_stride, "d_logits", size)
+    code = lib().skgemm_logprobs_grad(z, _ptr(tokens, 8 * _n(T), "tokens"), _ptr(lse, 4 * _n(T), "lse"),
+                                      _ptr(entropy, 4 * _n(T), "entropy"), _ptr(g_logprob, 4 * _n(T), "g_logprob"),
+                                      _ptr(g_entropy, 4 * _n(T), "g_entropy"), d, T, V, scale, f, zs, ds, _stream(stream))
+    _check(code, "skgemm_logprobs_grad")
 
 
 def skgemm_mxfp8_dequant(Wq8, Wscale, W_out, N: int, K: int, stream=None) -> None:

@@ -1,0 +1,394 @@
+// Log probabilities of given tokens with entropy and the best alternatives
+// (skgemm_logprobs), and their gradient to the logits (skgemm_logprobs_grad).
+//
+// With m the largest logit x, c = scale / log 2 and d = (x - m) c:
+//   s = sum 2^d, u = sum 2^d d,
+//   lse = scale m + log s,  entropy = (log2 s - u / s) log 2,
+//   logprob = scale (x[token] - m) - log s.
+// The difference is taken before the scaling, so the type's lowest value does
+// not become an infinity on the way, every term is built from d, so nothing
+// cancels against m, and two parts of a row join by moving one to the other's
+// reference:  with f = (m - m') c:  s' = s 2^f,  u' = 2^f (u + f s).
+//
+// Bound by memory: the logits are read once (the gradient reads and writes
+// them). An element costs about nine vector operations, one of them an
+// exponential at a quarter rate: at 2 bytes a logit the arithmetic needs
+// nearly as long as the read, so what is not asked for is left out.
+
+#include "device/block.h"
+#include "device/pack.h"
+#include "ops_internal.h"
+#include "skgemm.h"
+
+namespace skg {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// Two floats to packed bf16 (round to nearest even) in one instruction.
+__device__ __forceinline__ uint32_t bf16_pair_hw(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
+constexpr float kInf = __builtin_inff();
+typedef unsigned long long u64;
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// One row's 16-byte vectors: the row starts `head` elements into vector 0 and
+// ends before element head + V. Only vector 0 and the last can be partial;
+// those are read element by element, so nothing outside the row is read.
+template <bool F32>
+struct Row {
+  static constexpr int kE = F32 ? 4 : 8;    // elements of a vector
+  static constexpr int kSize = F32 ? 4 : 2;
+  const uint8_t* base;  // vector 0, 16-byte aligned
+  int head, V, nvec;
+
+  __device__ __forceinline__ Row(const uint8_t* row, int v) {
+    const int off = (int)((uintptr_t)row & 15u);
+    base = row - off;
+    head = off / kSize;
+    V = v;
+    nvec = (head + v + kE - 1) / kE;
+  }
+  __device__ __forceinline__ bool whole(int j) const { return j * kE >= head && (j + 1) * kE <= head + V; }
+  // Index of element 0 of vector j (negative ahead of the row).
+  __device__ __forceinline__ int index(int j) const { return j * kE - head; }
+  __device__ __forceinline__ u32x4 load_whole(int j) const {
+    return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(base) + j);
+  }
+  __device__ __forceinline__ static void unpack(u32x4 v, float* x) {
+    if constexpr (F32) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(v[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[2 * e] = bf16_lo(v[e]);
+        x[2 * e + 1] = bf16_hi(v[e]);
+      }
+    }
+  }
+  __device__ __forceinline__ float at(int i) const {  // element i of the row
+    const uint8_t* p = base + (size_t)(head + i) * kSize;
+    if constexpr (F32) return *reinterpret_cast<const float*>(p);
+    return __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(p) << 16);
+  }
+  // Vector j's elements; those outside the row are `fill`.
+  __device__ __forceinline__ void load(int j, float* x, float fill) const {
+    if (whole(j)) {
+      unpack(load_whole(j), x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        const int i = index(j) + e;
+        x[e] = (i >= 0 && i < V) ? at(i) : fill;
+      }
+    }
+  }
+};
+
+// ---- the sums ---------------------------------------------------------------
+
+struct Sums {
+  float m, s, u;  // reference (a logit), sum, weighted sum; m = -inf: no term yet
+};
+
+// Moves both parts to the larger reference and adds them. A part without a
+// term has s = u = 0 and may have m = -inf.
+__device__ __forceinline__ Sums join(Sums a, Sums b, float mul) {
+  const float m = fmaxf(a.m, b.m);
+  if (m == -kInf) return {m, a.s + b.s, a.u + b.u};  // + keeps a NaN
+  const float da = (a.m - m) * mul, db = (b.m - m) * mul;
+  const float ea = exp2_hw(da), eb = exp2_hw(db);
+  // -inf times a zero sum would be NaN.
+  return {m, a.s * ea + b.s * eb, ea * (a.u + fmaxf(da, -1e30f) * a.s) + eb * (b.u + fmaxf(db, -1e30f) * b.s)};
+}
+
+__device__ __forceinline__ float shfl_xor(float v, int off) { return __shfl_xor(v, off, 64); }
+
+// ---- the best k ---------------------------------------------------------------
+//
+// Order: value first, then the lower index. A key holds both: the value's bits
+// made monotonic (as unsigned) above the complement of the index, so keys are
+// distinct and the larger key is the better element; 0 is no element.
+__device__ __forceinline__ uint32_t order_bits(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);  // -0 becomes 0
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float order_value(uint32_t o) {
+  return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
+}
+__device__ __forceinline__ u64 make_key(float v, int i) { return ((u64)order_bits(v) << 32) | (uint32_t)~i; }
+__device__ __forceinline__ int key_index(u64 k) { return (int)~(uint32_t)k; }
+
+constexpr int kCand = 1024;  // candidates held in LDS
+
+struct TopLds {
+  uint32_t best[kThreads];
+  int owners[kThreads];
+  u64 cand[kCand];
+  int n_own, n_cand, count;
+};
+
+// Sorted best k of the keys that `src` holds, to out(rank, key), ranks 0 ..
+// k-1 (fewer if fewer keys). Thread t owns src's items t, t + 256, ...; `best`
+// is order_bits of its best key (0: none), known from the pass over the data.
+//
+// If the k-th largest of the owners' bests is b, every key of the best k lies
+// with an owner whose best is at least b, and is at least b itself: k keys
+// (the bests) reach it. So only those owners' items are read again: about k of
+// 256, a fraction k / 256 of the data, whatever the values are. Ties at b can
+// make the candidates many; past kCand the exact k-th key is searched bit by
+// bit over the owners' items (rows of mostly equal logits).
+template <class Src, class Out>
+__device__ __forceinline__ void block_top(const Src& src, uint32_t best, int k, TopLds& l, Out out) {
+  const int tid = (int)threadIdx.x, lane = tid & 63;
+  l.best[tid] = best;
+  if (tid == 0) l.n_own = l.n_cand = 0;
+  __syncthreads();
+  // Each wave finds b by itself: four bests a lane, one bit a step.
+  uint32_t b4[4], thr = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b4[i] = l.best[lane + 64 * i];
+  for (uint32_t bit = 0x80000000u; bit != 0; bit >>= 1) {
+    const uint32_t c = thr | bit;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) n += __popcll(__ballot(b4[i] >= c));
+    if (n >= k) thr = c;
+  }
+  if (best >= thr && best != 0) l.owners[atomicAdd(&l.n_own, 1)] = tid;
+  __syncthreads();
+  const int n_own = l.n_own, per = src.per_owner();
+  const long items = (long)n_own * per;
+  u64 lowest = (u64)thr << 32;
+  auto gather = [&]() {
+    for (long it = tid; it < items; it += kThreads) {
+      u64 key[Src::kE];
+      src.keys(l.owners[it / per] + (int)(it % per) * kThreads, key);
+#pragma unroll
+      for (int e = 0; e < Src::kE; ++e)
+        if (key[e] != 0 && key[e] >= lowest) {
+          const int at = atomicAdd(&l.n_cand, 1);
+          if (at < kCand) l.cand[at] = key[e];
+        }
+    }
+    __syncthreads();
+  };
+  gather();
+  if (l.n_cand > kCand) {
+    // The k-th largest key itself, one bit a step; then exactly k keys reach it.
+    u64 kth = 0;
+    for (int bit = 63; bit >= 0; --bit) {
+      const u64 c = kth | ((u64)1 << bit);
+      if (tid == 0) l.count = 0;
+      __syncthreads();
+      int n = 0;
+      for (long it = tid; it < items; it += kThreads) {
+        u64 key[Src::kE];
+        src.keys(l.owners[it / per] + (int)(it % per) * kThreads, key);
+#pragma unroll
+        for (int e = 0; e < Src::kE; ++e) n += key[e] >= c;
+      }
+      atomicAdd(&l.count, n);
+      __syncthreads();
+      if (l.count >= k) kth = c;
+      __syncthreads();
+    }
+    lowest = kth;
+    if (tid == 0) l.n_cand = 0;
+    __syncthreads();
+    gather();
+  }
+  const int n = l.n_cand;
+  for (int i = tid; i < n; i += kThreads) {
+    const u64 key = l.cand[i];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += l.cand[j] > key;
+    if (rank < k) out(rank, key);
+  }
+}
+
+// A row's vectors first .. first + n as block_top's items.
+template <bool F32>
+struct RowItems {
+  static constexpr int kE = Row<F32>::kE;
+  const Row<F32>& row;
+  int first, n;
+  __device__ __forceinline__ int per_owner() const { return (n + kThreads - 1) / kThreads; }
+  __device__ __forceinline__ void keys(int item, u64* key) const {
+#pragma unroll
+    for (int e = 0; e < kE; ++e) key[e] = 0;
+    if (item >= n) return;
+    float x[kE];
+    row.load(first + item, x, 0.0f);
+#pragma unroll
+    for (int e = 0; e < kE; ++e) {
+      const int i = row.index(first + item) + e;
+      if (i >= 0 && i < row.V) key[e] = make_key(x[e], i);
+    }
+  }
+};
+
+template <bool F32>
+__global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobParams p) {
+  __shared__ TopLds top;
+  __shared__ Sums part[kThreads / 64];
+  const size_t t = blockIdx.x;
+  const Row<F32> row(p.logits + t * p.stride, p.V);
+  constexpr int kE = Row<F32>::kE;
+  const float mul = p.scale * kLog2e;
+  Sums a = {-kInf, 0.0f, 0.0f};
+  const bool any = (int)threadIdx.x < row.nvec;
+  for (int j = (int)threadIdx.x; j < row.nvec; j += kThreads) {
+    float x[kE];
+    row.load(j, x, -kInf);
+    float m = a.m;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) m = fmaxf(m, x[e]);
+    if (m > a.m) {
+      const float d = (a.m - m) * mul, f = exp2_hw(d);
+      a.u = f * (a.u + fmaxf(d, -1e30f) * a.s);
+      a.s *= f;
+      a.m = m;
+    }
+    const float ref = m == -kInf ? 0.0f : m;  // nothing but banned tokens so far: d = -inf
+#pragma unroll
+    for (int e = 0; e < kE; ++e) {
+      const float d = (x[e] - ref) * mul, w = exp2_hw(d);
+      a.s += w;
+      a.u = fmaf(w, fmaxf(d, -1e30f), a.u);  // 0 * -1e30 where 0 * -inf would be NaN
+    }
+  }
+  const float most = a.m;  // of this thread's logits
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) a = join(a, Sums{shfl_xor(a.m, off), shfl_xor(a.s, off), shfl_xor(a.u, off)}, mul);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = a;
+  __syncthreads();
+  a = part[0];
+  for (int i = 1; i < kThreads / 64; ++i) a = join(a, part[i], mul);
+  // s is NaN exactly where the row holds a NaN or +inf.
+  const bool bad = !(a.s == a.s), empty = a.s == 0.0f;
+  const float log_s = __builtin_amdgcn_logf(a.s);  // log2
+  if (threadIdx.x == 0) {
+    if (p.lse != nullptr) p.lse[t] = bad ? a.s : empty ? -kInf : fmaf(a.m, p.scale, log_s * kLn2);
+    if (p.entropy != nullptr) p.entropy[t] = empty ? 0.0f : (log_s - a.u / a.s) * kLn2;
+    if (p.logprob != nullptr) {
+      const int64_t tok = p.tokens[t];
+      float v;
+      if (tok < 0) v = 0.0f;
+      else if (tok >= p.V || bad) v = __builtin_nanf("");
+      else if (empty) v = -kInf;
+      else v = (row.at((int)tok) - a.m) * p.scale - log_s * kLn2;
+      p.logprob[t] = v;
+    }
+  }
+  if (p.k == 0) return;
+  float* tv = p.top_logprob + t * (size_t)p.k;
+  int64_t* ti = p.top_ids + t * (size_t)p.k;
+  if (bad) {
+    if ((int)threadIdx.x < p.k) {
+      tv[threadIdx.x] = a.s;
+      ti[threadIdx.x] = -1;
+    }
+    return;
+  }
+  const RowItems<F32> items{row, 0, row.nvec};
+  block_top(items, any ? order_bits(most) : 0u, p.k, top, [&](int rank, u64 key) {
+    const float v = order_value((uint32_t)(key >> 32));
+    tv[rank] = empty ? -kInf : (v - a.m) * p.scale - log_s * kLn2;
+    ti[rank] = key_index(key);
+  });
+}
+
+// ---- the gradient -------------------------------------------------------------
+//
+//   d_j = scale * (g ([j == token] - p_j) - gH p_j (log p_j + H))
+//       = p_j * (c0 + c1 log2 p_j) + [j == token] scale g,
+//   c0 = -scale (g + gH H),  c1 = -scale gH ln 2.
+// One workgroup takes a run of a row's vectors; elementwise, so d_logits may be
+// the logits.
+template <bool F32>
+__global__ __launch_bounds__(kThreads) void logprobs_grad_kernel(LogprobGradParams p) {
+  const size_t t = blockIdx.x / p.parts;
+  const Row<F32> row(p.logits + t * p.stride, p.V);
+  const Row<F32> out(p.d_logits + t * p.d_stride, p.V);
+  constexpr int kE = Row<F32>::kE;
+  const int64_t tok = p.tokens != nullptr ? p.tokens[t] : -1;
+  const float lse = p.lse[t];
+  const bool empty = lse == -kInf;
+  float g = (p.g_logprob != nullptr && tok >= 0) ? p.g_logprob[t] : 0.0f;
+  if (p.g_logprob != nullptr && tok >= p.V) g = __builtin_nanf("");
+  const float gh = p.g_entropy != nullptr ? p.g_entropy[t] : 0.0f;
+  const float ent = p.g_entropy != nullptr ? p.entropy[t] : 0.0f;
+  const float ref = empty ? 0.0f : lse;
+  // The clamp below would swallow a NaN lse, so it goes into c0.
+  const float c0 = lse == lse ? -p.scale * (g + gh * ent) : lse, c1 = -p.scale * gh * kLn2;
+  const float hit = empty ? 0.0f : p.scale * g;
+  const bool same = row.head == out.head;
+  uint8_t* const base = p.d_logits + t * p.d_stride - (size_t)out.head * Row<F32>::kSize;
+  const int hit_at = tok >= 0 && tok < p.V ? (int)tok + row.head : -1;  // counted from vector 0
+  for (int j = (int)(blockIdx.x % p.parts * kThreads + threadIdx.x); j < row.nvec; j += (int)(p.parts * kThreads)) {
+    float x[kE];
+    row.load(j, x, 0.0f);
+#pragma unroll
+    for (int e = 0; e < kE; ++e) {
+      // Past -1e30 the exponential is 0 either way; -inf would make 0 * inf.
+      const float lp = fmaxf(fmaf(x[e], p.scale, -ref) * kLog2e, -1e30f);
+      x[e] = exp2_hw(lp) * fmaf(c1, lp, c0);
+    }
+    if ((unsigned)(hit_at - j * kE) < (unsigned)kE) {
+#pragma unroll
+      for (int e = 0; e < kE; ++e)
+        if (j * kE + e == hit_at) x[e] += hit;
+    }
+    if (same && row.whole(j)) {
+      u32x4 w;
+      if constexpr (F32) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(x[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = bf16_pair_hw(x[2 * e], x[2 * e + 1]);
+      }
+      reinterpret_cast<u32x4*>(base)[j] = w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        const int i = row.index(j) + e;
+        if (i < 0 || i >= p.V) continue;
+        if constexpr (F32)
+          reinterpret_cast<float*>(base)[out.head + i] = x[e];
+        else
+          reinterpret_cast<uint16_t*>(base)[out.head + i] = (uint16_t)bf16_rne(x[e]);
+      }
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_logprobs(const LogprobParams& p, bool f32, hipStream_t s) {
+  if (f32)
+    hipLaunchKernelGGL(logprobs_kernel<true>, dim3((unsigned)p.T), dim3(kThreads), 0, s, p);
+  else
+    hipLaunchKernelGGL(logprobs_kernel<false>, dim3((unsigned)p.T), dim3(kThreads), 0, s, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_logprobs_grad(LogprobGradParams p, bool f32, hipStream_t s) {
+  p.parts = 4;
+  const dim3 grid((unsigned)p.T * p.parts);
+  if (f32)
+    hipLaunchKernelGGL(logprobs_grad_kernel<true>, grid, dim3(kThreads), 0, s, p);
+  else
+    hipLaunchKernelGGL(logprobs_grad_kernel<false>, grid, dim3(kThreads), 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace skg

@@ -11,6 +11,19 @@ namespace {
 
 bool aligned(const void* p, uintptr_t n) { return (uintptr_t)p % n == 0; }
 
+// The logits' (or their gradient's) own arguments.
+int check_logits(const void* logits, int T, int V, float scale, int format, size_t stride) {
+  if (T < 0 || V < 0 || (format != SKGEMM_BF16 && format != SKGEMM_F32)) return SKGEMM_EINVAL;
+  if (!(scale > 0.0f) || !(scale < INFINITY)) return SKGEMM_EINVAL;
+  if (V > SKGEMM_MAX_V || T > SKGEMM_MAX_ROWS) return SKGEMM_ESHAPE;
+  if (T == 0 || V == 0) return SKGEMM_OK;
+  if (logits == nullptr) return SKGEMM_EINVAL;
+  const size_t size = format == SKGEMM_F32 ? 4 : 2;
+  if (!aligned(logits, 16) || (T > 1 && stride % size != 0)) return SKGEMM_EALIGN;
+  if (T > 1 && stride < size * (size_t)V) return SKGEMM_EINVAL;
+  return SKGEMM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -22,7 +35,7 @@ SKGEMM_API int skgemm_rmsnorm(const void* X, const void* R, const void* G, void*
   if (T < 0 || H < 0) return SKGEMM_EINVAL;
   if (out_format != SKGEMM_BF16 && out_format != SKGEMM_I8 && out_format != SKGEMM_E4M3) return SKGEMM_EINVAL;
   if (!(eps >= 1e-30f) || !(eps < INFINITY)) return SKGEMM_EINVAL;
-  if (H % 8 != 0 || H > SKGEMM_MAX_H) return SKGEMM_ESHAPE;
+  if (H % 8 != 0 || H > SKGEMM_MAX_H || T > SKGEMM_MAX_ROWS) return SKGEMM_ESHAPE;
   if (T == 0 || H == 0) return SKGEMM_OK;
   const bool codes = out_format != SKGEMM_BF16;
   if (X == nullptr || Y == nullptr || (codes && y_scale == nullptr)) return SKGEMM_EINVAL;
@@ -60,7 +73,7 @@ SKGEMM_API int skgemm_i8(const void* Wq, const float* w_scale, const void* Xq, c
                          size_t x_stride, size_t c_stride, hipStream_t stream) {
   if (T < 0 || N < 0 || K < 0) return SKGEMM_EINVAL;
   if (out_format != SKGEMM_BF16 && out_format != SKGEMM_F32) return SKGEMM_EINVAL;
-  if (K % 16 != 0 || K > SKGEMM_MAX_K_I8 || N > SKGEMM_MAX_N) return SKGEMM_ESHAPE;
+  if (K % 16 != 0 || K > SKGEMM_MAX_K_I8 || N > SKGEMM_MAX_N || T > SKGEMM_MAX_ROWS) return SKGEMM_ESHAPE;
   if (T == 0 || N == 0) return SKGEMM_OK;
   if (C == nullptr || w_scale == nullptr || x_scale == nullptr) return SKGEMM_EINVAL;
   if (K > 0 && (Wq == nullptr || Xq == nullptr)) return SKGEMM_EINVAL;
@@ -84,6 +97,69 @@ SKGEMM_API int skgemm_i8(const void* Wq, const float* w_scale, const void* Xq, c
   p.K = K;
   p.out_f32 = out_format == SKGEMM_F32;
   const hipError_t e = skg::launch_i8(p, stream);
+  return e == hipSuccess ? SKGEMM_OK : skg::hip_fail(e);
+}
+
+SKGEMM_API int skgemm_logprobs(const void* logits, const int64_t* tokens, float* logprob,
+                               float* entropy, float* lse, float* top_logprob, int64_t* top_ids,
+                               int T, int V, int top_k, float scale, int logits_format,
+                               size_t stride, hipStream_t stream) {
+  int rc = check_logits(logits, T, V, scale, logits_format, stride);
+  if (rc != SKGEMM_OK) return rc;
+  if (top_k < 0) return SKGEMM_EINVAL;
+  if (top_k > SKGEMM_MAX_TOP) return SKGEMM_ESHAPE;
+  if (T == 0 || V == 0) return SKGEMM_OK;
+  if (top_k > V || (logprob != nullptr && tokens == nullptr)) return SKGEMM_EINVAL;
+  if (top_k > 0 && (top_logprob == nullptr || top_ids == nullptr)) return SKGEMM_EINVAL;
+  if (!aligned(tokens, 8) || !aligned(top_ids, 8) || !aligned(logprob, 4) || !aligned(entropy, 4) || !aligned(lse, 4) ||
+      !aligned(top_logprob, 4))
+    return SKGEMM_EALIGN;
+  skg::LogprobParams p{};
+  p.logits = static_cast<const uint8_t*>(logits);
+  p.tokens = tokens;
+  p.logprob = logprob;
+  p.entropy = entropy;
+  p.lse = lse;
+  p.top_logprob = top_logprob;
+  p.top_ids = top_ids;
+  p.stride = stride;
+  p.T = T;
+  p.V = V;
+  p.k = top_k;
+  p.scale = scale;
+  const hipError_t e = skg::launch_logprobs(p, logits_format == SKGEMM_F32, stream);
+  return e == hipSuccess ? SKGEMM_OK : skg::hip_fail(e);
+}
+
+SKGEMM_API int skgemm_logprobs_grad(const void* logits, const int64_t* tokens, const float* lse,
+                                    const float* entropy, const float* g_logprob,
+                                    const float* g_entropy, void* d_logits, int T, int V,
+                                    float scale, int logits_format, size_t stride, size_t d_stride,
+                                    hipStream_t stream) {
+  int rc = check_logits(logits, T, V, scale, logits_format, stride);
+  if (rc != SKGEMM_OK) return rc;
+  if (T == 0 || V == 0) return SKGEMM_OK;
+  if (d_logits == nullptr || lse == nullptr) return SKGEMM_EINVAL;
+  if ((g_logprob != nullptr && tokens == nullptr) || (g_entropy != nullptr && entropy == nullptr)) return SKGEMM_EINVAL;
+  rc = check_logits(d_logits, T, V, scale, logits_format, d_stride);
+  if (rc != SKGEMM_OK) return rc;
+  if (d_logits == logits && T > 1 && d_stride != stride) return SKGEMM_EINVAL;
+  if (!aligned(tokens, 8) || !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(g_logprob, 4) || !aligned(g_entropy, 4))
+    return SKGEMM_EALIGN;
+  skg::LogprobGradParams p{};
+  p.logits = static_cast<const uint8_t*>(logits);
+  p.tokens = tokens;
+  p.lse = lse;
+  p.entropy = entropy;
+  p.g_logprob = g_logprob;
+  p.g_entropy = g_entropy;
+  p.d_logits = static_cast<uint8_t*>(d_logits);
+  p.stride = stride;
+  p.d_stride = d_stride;
+  p.T = T;
+  p.V = V;
+  p.scale = scale;
+  const hipError_t e = skg::launch_logprobs_grad(p, logits_format == SKGEMM_F32, stream);
   return e == hipSuccess ? SKGEMM_OK : skg::hip_fail(e);
 }
 

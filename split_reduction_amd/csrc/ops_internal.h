@@ -31,6 +31,30 @@ struct I8Params {
   int out_f32;
 };
 
+struct LogprobParams {
+  const uint8_t* logits;  // bf16 or float [T, V]
+  const int64_t* tokens;  // [T], null where logprob is
+  float *logprob, *entropy, *lse;  // [T], each may be null
+  float* top_logprob;     // [T, k]
+  int64_t* top_ids;       // [T, k]
+  size_t stride;          // bytes between rows of logits
+  int T, V, k;
+  float scale;
+};
+
+struct LogprobGradParams {
+  const uint8_t* logits;
+  const int64_t* tokens;  // null: no logprob term
+  const float *lse, *entropy, *g_logprob, *g_entropy;
+  uint8_t* d_logits;
+  size_t stride, d_stride;
+  int T, V;
+  unsigned parts;  // workgroups a row
+  float scale;
+};
+
+hipError_t launch_logprobs(const LogprobParams& p, bool f32, hipStream_t s);
+hipError_t launch_logprobs_grad(LogprobGradParams p, bool f32, hipStream_t s);
 hipError_t launch_i8(const I8Params& p, hipStream_t s);
 hipError_t launch_rmsnorm(const NormParams& p, int out_format, hipStream_t s);
 
