@@ -216,8 +216,13 @@ SKGEMM_API int skgemm_mxfp8_batched(const void* Wq8, const void* Wscale, const v
 /*
  * The operators around the quantised layers and the language-model head.
  * Rows may be further apart than their length: *_stride is the distance of two
- * rows in BYTES. Sizes of zero enqueue nothing and succeed.
+ * rows in BYTES. Sizes of zero enqueue nothing and succeed. Work split over
+ * several workgroups meets in a workspace of the stream that is separate from
+ * the split-K workspace above and of one fixed size: the first call on a stream
+ * allocates it, skgemm_reserve_ops does so ahead of a graph capture, and
+ * skgemm_release frees it.
  */
+#define SKGEMM_OPS_WORKSPACE_BYTES ((size_t)33 << 20)
 enum skgemm_format {
   SKGEMM_BF16 = 0,
   SKGEMM_I8 = 1,   /* two's complement codes in -127..127, one FP32 scale a row */
@@ -312,6 +317,10 @@ SKGEMM_API int skgemm_logprobs_grad(const void* logits, const int64_t* tokens, c
                                     const float* g_entropy, void* d_logits, int T, int V,
                                     float scale, int logits_format, size_t stride, size_t d_stride,
                                     hipStream_t stream);
+
+/* skgemm_reserve_ops: allocate the stream's workspace of the calls above now
+ * (they cannot allocate it while the stream is captured: SKGEMM_ENOMEM). */
+SKGEMM_API int skgemm_reserve_ops(hipStream_t stream);
 
 /*
  * skgemm_reserve: make sure the workspace of (current device, stream) can
@@ -468,8 +477,10 @@ enum skgemm_knob {
   SKGEMM_KNOB_PDEFER = 6,      /* persistent kernel: partials held in LDS 0/1 */
   SKGEMM_KNOB_OWNER_WAIT = 7,  /* owner wait bound, 100 MHz ticks (0: hand the
                                   tile over at once)                          */
-  SKGEMM_KNOB_HANDOFF = 8      /* persistent kernel's split-K hand-off:
+  SKGEMM_KNOB_HANDOFF = 8,     /* persistent kernel's split-K hand-off:
                                   0 arrival counter, 1 tagged mailbox         */
+  SKGEMM_KNOB_I8_SHAPE = 9,    /* skgemm_i8: tile shape index                 */
+  SKGEMM_KNOB_I8_SPLIT = 10    /* skgemm_i8: workgroups that split K          */
 };
 SKGEMM_API int skgemm_set_override(int knob, int value);
 

@@ -29,7 +29,7 @@ SKGEMM_ESCRATCH = -6
 
 # skgemm_set_override knobs (include/skgemm.h, enum skgemm_knob)
 KNOBS = {"kind": 0, "stream": 1, "shape": 2, "fold": 3, "cluster_c": 4, "wg_per_cu": 5,
-         "pdefer": 6, "owner_wait": 7, "handoff": 8}
+         "pdefer": 6, "owner_wait": 7, "handoff": 8, "i8_shape": 9, "i8_split": 10}
 
 # Element formats (include/skgemm.h, enum skgemm_format)
 FORMATS = {"bf16": 0, "i8": 1, "e4m3": 2, "f32": 3}
@@ -72,6 +72,7 @@ def _declare(lib):
         "skgemm_i8": [vp, vp, vp, vp, vp, i, i, i, i, sz, sz, sz, st],
         "skgemm_logprobs": [vp, vp, vp, vp, vp, vp, vp, i, i, i, ctypes.c_float, i, sz, st],
         "skgemm_logprobs_grad": [vp, vp, vp, vp, vp, vp, vp, i, i, ctypes.c_float, i, sz, sz, st],
+        "skgemm_reserve_ops": [st],
         "skgemm_rmsnorm": [vp, vp, vp, vp, vp, vp, i, i, ctypes.c_float, i, sz, sz, sz, sz, st],
     }
     for name, args in sig.items():
@@ -377,6 +378,12 @@ def skgemm_reserve_batched(max_T: int, max_N: int, max_split_k: int, max_L: int,
 
 def skgemm_reserve(max_T: int, max_N: int, max_split_k: int, stream=None) -> None:
     _check(lib().skgemm_reserve(max_T, max_N, max_split_k, _stream(stream)), "skgemm_reserve")
+
+
+def skgemm_reserve_ops(stream=None) -> None:
+    """Allocate the stream's workspace of skgemm_i8 and skgemm_logprobs now, as
+    they cannot while the stream is captured."""
+    _check(lib().skgemm_reserve_ops(_stream(stream)), "skgemm_reserve_ops")
 
 
 def skgemm_release() -> None:

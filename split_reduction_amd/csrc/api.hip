@@ -480,7 +480,8 @@ SKGEMM_API int skgemm_release(void) {
     const hipError_t e = hipSetDevice(caller_dev);
     if (e != hipSuccess && rc == SKGEMM_OK) rc = hip_fail(e);
   }
-  return rc;
+  const int ops = skg::release_ops_workspaces();
+  return rc == SKGEMM_OK ? ops : rc;
 }
 
 SKGEMM_API int skgemm_mxfp4_dequant(const void* Wq, const void* Wscale, void* W_out, int N, int K,

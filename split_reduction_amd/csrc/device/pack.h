@@ -28,6 +28,12 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   return bf16_rne(lo) | (bf16_rne(hi) << 16);
 }
 
+// Two floats to packed bf16 (round to nearest even) in one instruction.
+__device__ __forceinline__ uint32_t bf16_pair_hw(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
 // Four float32 -> four bf16 in two words (element 0 in the low half of word 0).
 __device__ __forceinline__ u32x2 bf16_quad(f32x4 v) {
   u32x2 w;

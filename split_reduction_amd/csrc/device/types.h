@@ -67,6 +67,14 @@ __device__ __forceinline__ uint32_t ld2_if(bool ok, rsrc_t r, uint32_t off) {
   return __builtin_amdgcn_raw_buffer_load_b16(r, ok ? off : kOOB, 0, POLICY);
 }
 
+// 16 bytes a lane straight from memory into LDS: lane l's go to lds + 16 l (lds
+// is the same in every lane). An offset at or past the bound gives zeros.
+__device__ __forceinline__ void ld16_to_lds(rsrc_t r, uint32_t off, uint32_t uniform_off, void* lds) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass knows no 16-byte form
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, off, uniform_off, 0, 0);
+#endif
+}
+
 // Stores dropped (no branch) when !ok.
 __device__ __forceinline__ void st16_if(bool ok, u32x4 v, rsrc_t r, uint32_t off) {
   __builtin_amdgcn_raw_buffer_store_b128(v, r, ok ? off : kOOB, 0, kPolicyDefault);

@@ -10,6 +10,7 @@
 #include "device/block.h"
 #include "device/pack.h"
 #include "ops_internal.h"
+#include "skgemm_internal.h"
 #include "skgemm.h"
 
 namespace skg {
@@ -24,17 +25,25 @@ __device__ __forceinline__ i32x4 mfma_i8(u32x4 a, u32x4 b, i32x4 c) {
 
 // Outputs n .. n+3 of token t from their integer sums. The sum is rounded to
 // FP32, both products are FP32, and bf16 rounds once more.
-__device__ __forceinline__ void store_sums(const I8Params& p, int t, int n, i32x4 s, float xs) {
-  if (t >= p.T) return;
-  uint8_t* row = p.c + (size_t)t * p.c_stride;
+__device__ __forceinline__ void store_sums(const I8Params& p, int t, int n, i32x4 s, float xs, const float* ws) {
+  uint8_t* const row = p.c + (size_t)t * p.c_stride;
+  float v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = (float)s[e] * xs * ws[e];
+  if (p.c_quads && n + 3 < p.N) {  // every row's n is aligned for one store
+    if (p.out_f32)
+      *reinterpret_cast<f32x4*>(row + (size_t)n * 4) = f32x4{v[0], v[1], v[2], v[3]};
+    else
+      *reinterpret_cast<u32x2*>(row + (size_t)n * 2) = u32x2{bf16_pair_hw(v[0], v[1]), bf16_pair_hw(v[2], v[3])};
+    return;
+  }
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     if (n + e >= p.N) break;
-    const float v = (float)s[e] * xs * p.w_scale[n + e];
     if (p.out_f32)
-      reinterpret_cast<float*>(row)[n + e] = v;
+      reinterpret_cast<float*>(row)[n + e] = v[e];
     else
-      reinterpret_cast<uint16_t*>(row)[n + e] = (uint16_t)bf16_rne(v);
+      reinterpret_cast<uint16_t*>(row)[n + e] = (uint16_t)bf16_pair_hw(v[e], 0.0f);
   }
 }
 
@@ -69,19 +78,226 @@ __global__ __launch_bounds__(256) void i8_rows_kernel(I8Params p) {
     i32x4 s = part[0][j][lane];
 #pragma unroll
     for (int v = 1; v < 4; ++v) s += part[v][j][lane];
-    const int t = t0 + 16 * j + i;
-    store_sums(p, t, n0 + 4 * g, s, t < p.T ? p.x_scale[t] : 0.0f);
+    const int t = t0 + 16 * j + i, n = n0 + 4 * g;
+    float ws[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) ws[e] = n + e < p.N ? p.w_scale[n + e] : 0.0f;
+    if (t < p.T) store_sums(p, t, n, s, p.x_scale[t], ws);
+  }
+}
+
+// A tile of BT tokens x BN features, K in steps of 128 bytes through LDS.
+//
+// Each step's 128-byte row pieces come straight from memory into LDS
+// (buffer_load ... lds, 16 bytes a lane, 8 whole lines an instruction) into one
+// of STG buffers, STG - 1 steps ahead. Row r's 16-byte chunk c lies at position
+// c ^ (r & 7) of its line: an operand read takes one chunk of 16 rows, and
+// without the exchange all 16 would meet in the same banks. The exchange is on
+// the memory side (lane l of a load fetches chunk (l % 8) ^ (l / 8) of row
+// l / 8), as the LDS side of such a load is linear.
+//
+// WT x WN waves share the tile; a wave holds (BT / WT) x (BN / WN) sums in
+// registers. One barrier a step: past it, every wave's loads of this step have
+// landed and every wave has read the previous step's buffer, which the next
+// loads then fill.
+//
+// S workgroups may split K: each stores its sums to the workspace and the last
+// to arrive adds the others' (integers: the order does not matter).
+template <int BT, int BN, int WT, int WN, int STG>
+__global__ __launch_bounds__(64 * WT * WN) void i8_tile_kernel(I8Params p) {
+  constexpr int kWaves = WT * WN, kMT = BT / WT / 16, kNT = BN / WN / 16;
+  constexpr int kXL = BT / 8 / kWaves, kWL = BN / 8 / kWaves;  // loads of a wave and step
+  constexpr int kStage = (BT + BN) * 128;
+  static_assert(kXL >= 1 && kWL >= 1 && kXL * kWaves * 8 == BT && kWL * kWaves * 8 == BN, "whole loads");
+  __shared__ __align__(1024) uint8_t lds[STG * kStage];
+  __shared__ uint32_t arrived;
+  const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int i = lane & 15, g = lane >> 4;
+
+  // Workgroups go to the 8 XCDs in turn; each XCD takes a run of tiles whose
+  // operands its L2 then holds, four token tiles for each feature tile.
+  const int ttiles = (p.T + BT - 1) / BT, ntiles = (p.N + BN - 1) / BN, tiles = ttiles * ntiles;
+  const int total = tiles * p.S;
+  int idx = (int)blockIdx.x;
+  {
+    const int xcd = idx & 7, each = total >> 3, more = total & 7;
+    idx = (idx >> 3) + xcd * each + min(xcd, more);
+  }
+  const int rank = idx % p.S, tile = idx / p.S;
+  const int group = tile / (4 * ntiles), in_group = tile - group * 4 * ntiles;
+  const int gt = min(4, ttiles - 4 * group);
+  const int t0 = (4 * group + in_group % gt) * BT, n0 = in_group / gt * BN;
+  const int tokens = min(BT, p.T - t0), rows = min(BN, p.N - n0);
+  const rsrc_t w = make_rsrc(p.w + (size_t)n0 * p.w_stride, (uint32_t)((rows - 1) * p.w_stride + p.K));
+  const rsrc_t x = make_rsrc(p.x + (size_t)t0 * p.x_stride, (uint32_t)((tokens - 1) * p.x_stride + p.K));
+  const int steps = (p.K + 127) / 128;
+  const int s0 = (int)((long)steps * rank / p.S), s1 = (int)((long)steps * (rank + 1) / p.S);
+
+  // This lane's offsets; a row past the tile's end loads zeros (out of range).
+  const int row8 = lane >> 3, chunk = 16 * ((lane & 7) ^ row8);
+  uint32_t xoff[kXL], woff[kWL];
+#pragma unroll
+  for (int q = 0; q < kXL; ++q) {
+    const int r = 8 * (wave * kXL + q) + row8;
+    xoff[q] = r < tokens ? (uint32_t)(r * p.x_stride + chunk) : kOOB;
+  }
+#pragma unroll
+  for (int q = 0; q < kWL; ++q) {
+    const int r = 8 * (wave * kWL + q) + row8;
+    woff[q] = r < rows ? (uint32_t)(r * p.w_stride + chunk) : kOOB;
+  }
+  auto issue = [&](int s, int buf) {
+    uint8_t* const at = lds + buf * kStage;
+    const uint32_t past = 128 * s + chunk < p.K ? 0u : kOOB;  // K ends inside the last step
+#pragma unroll
+    for (int q = 0; q < kWL; ++q)
+      ld16_to_lds(w, woff[q] | past, 128 * s, at + BT * 128 + (wave * kWL + q) * 1024);
+#pragma unroll
+    for (int q = 0; q < kXL; ++q)
+      ld16_to_lds(x, xoff[q] | past, 128 * s, at + (wave * kXL + q) * 1024);
+  };
+
+  i32x4 acc[kNT][kMT] = {};
+  const int wt = wave / WN, wn = wave % WN;
+  const int pos0 = i * 128 + 16 * (g ^ (i & 7)), pos1 = i * 128 + 16 * ((4 + g) ^ (i & 7));
+  const int xbase = wt * (BT / WT) * 128, wbase = BT * 128 + wn * (BN / WN) * 128;
+#pragma unroll
+  for (int s = 0; s < STG - 1; ++s)
+    if (s0 + s < s1) issue(s0 + s, s);
+  int buf = 0;
+  for (int s = s0; s < s1; ++s) {
+    // The loads of steps s + 1 .. s + STG - 2 may stay in flight.
+    if (s + STG - 2 < s1)
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STG - 2) * (kXL + kWL)) : "memory");
+    else
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (s + STG - 1 < s1) issue(s + STG - 1, buf == 0 ? STG - 1 : buf - 1);
+    const uint8_t* const at = lds + buf * kStage;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int pos = h ? pos1 : pos0;
+      u32x4 a[kNT], b[kMT];
+#pragma unroll
+      for (int j = 0; j < kNT; ++j) a[j] = *reinterpret_cast<const u32x4*>(at + wbase + j * 2048 + pos);
+#pragma unroll
+      for (int j = 0; j < kMT; ++j) b[j] = *reinterpret_cast<const u32x4*>(at + xbase + j * 2048 + pos);
+#pragma unroll
+      for (int j = 0; j < kMT; ++j)
+#pragma unroll
+        for (int k = 0; k < kNT; ++k) acc[k][j] = mfma_i8(a[k], b[j], acc[k][j]);
+    }
+    buf = buf + 1 == STG ? 0 : buf + 1;
+  }
+
+  if (p.S > 1) {
+    // Sums as they lie in the registers: 16 bytes a lane, 1 KB a store.
+    constexpr uint32_t kTile = BT * BN * 4;
+    const rsrc_t part = make_rsrc(p.part + (size_t)tile * p.S * kTile, (uint32_t)p.S * kTile);
+    const uint32_t own = (uint32_t)rank * kTile + (uint32_t)(wave * kNT * kMT * 1024 + lane * 16);
+#pragma unroll
+    for (int k = 0; k < kNT; ++k)
+#pragma unroll
+      for (int j = 0; j < kMT; ++j)
+        st16_coherent_if(true, __builtin_bit_cast(u32x4, acc[k][j]), part, own + (uint32_t)(k * kMT + j) * 1024u);
+    wait_vmem_all();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      uint32_t* const cnt = p.cnt + (size_t)tile * kOpsCounterStride;
+      const uint32_t a = __hip_atomic_fetch_add(cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      // Everyone has arrived: the counter is ready for the next call.
+      if (a + 1 == (uint32_t)p.S) __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      arrived = a;
+    }
+    __syncthreads();
+    if (arrived + 1 != (uint32_t)p.S) return;
+    handoff_order();
+    for (int r = 0; r < p.S; ++r) {
+      if (r == rank) continue;
+      const uint32_t other = (uint32_t)r * kTile + (uint32_t)(wave * kNT * kMT * 1024 + lane * 16);
+#pragma unroll
+      for (int k = 0; k < kNT; ++k)
+#pragma unroll
+        for (int j = 0; j < kMT; ++j)
+          acc[k][j] += __builtin_bit_cast(i32x4, ld16_coherent_if(true, part, other + (uint32_t)(k * kMT + j) * 1024u));
+    }
+  }
+
+#pragma unroll
+  for (int k = 0; k < kNT; ++k) {
+    const int n = n0 + wn * (BN / WN) + 16 * k + 4 * g;
+    float ws[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) ws[e] = n + e < p.N ? p.w_scale[n + e] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < kMT; ++j) {
+      const int t = t0 + wt * (BT / WT) + 16 * j + i;
+      if (t < p.T) store_sums(p, t, n, acc[k][j], p.x_scale[t], ws);
+    }
   }
 }
 
 }  // namespace
 
-hipError_t launch_i8(const I8Params& p, hipStream_t s) {
-  const unsigned tiles = (unsigned)((p.N + 15) / 16);
-  if (p.T <= 16)
-    hipLaunchKernelGGL(i8_rows_kernel<1>, dim3(tiles, (unsigned)((p.T + 15) / 16)), dim3(256), 0, s, p);
-  else
-    hipLaunchKernelGGL(i8_rows_kernel<4>, dim3(tiles, (unsigned)((p.T + 63) / 64)), dim3(256), 0, s, p);
+namespace {
+
+struct TileShape {
+  int bt, bn;
+};
+constexpr TileShape kShapes[] = {{256, 256}, {256, 128}, {128, 128}, {128, 128}, {64, 128}, {64, 64}, {32, 128}, {32, 64}};
+constexpr int kShapeCount = (int)(sizeof(kShapes) / sizeof(kShapes[0]));
+
+template <int BT, int BN, int WT, int WN, int STG>
+void launch_tile(const I8Params& p, int grid, hipStream_t s) {
+  hipLaunchKernelGGL((i8_tile_kernel<BT, BN, WT, WN, STG>), dim3((unsigned)grid), dim3(64 * WT * WN), 0, s, p);
+}
+
+void launch_shape(int shape, const I8Params& p, int grid, hipStream_t s) {
+  switch (shape) {
+    case 0: return launch_tile<256, 256, 2, 4, 2>(p, grid, s);
+    case 1: return launch_tile<256, 128, 2, 4, 3>(p, grid, s);
+    case 2: return launch_tile<128, 128, 2, 2, 2>(p, grid, s);
+    case 3: return launch_tile<128, 128, 2, 2, 4>(p, grid, s);
+    case 4: return launch_tile<64, 128, 1, 4, 4>(p, grid, s);
+    case 5: return launch_tile<64, 64, 1, 4, 4>(p, grid, s);
+    case 6: return launch_tile<32, 128, 1, 4, 4>(p, grid, s);
+    default: return launch_tile<32, 64, 1, 4, 4>(p, grid, s);
+  }
+}
+
+}  // namespace
+
+I8Tactic pick_i8(int T, int N, int K) {
+  I8Tactic t;
+  t.shape = knob(kKnobI8Shape, T <= 64 ? -1 : T >= 1024 ? 0 : 2);
+  t.S = knob(kKnobI8Split, 1);
+  if (t.shape < 0 || t.shape >= kShapeCount) {
+    t.shape = -1;
+    t.S = 1;
+    return t;
+  }
+  const TileShape& sh = kShapes[t.shape];
+  t.tiles = (int)(((long)T + sh.bt - 1) / sh.bt * ((N + sh.bn - 1) / sh.bn));
+  const int steps = (K + 127) / 128;
+  if (t.S > steps) t.S = steps > 0 ? steps : 1;
+  t.part_bytes = t.S > 1 ? (size_t)t.tiles * t.S * sh.bt * sh.bn * 4 : 0;
+  if (t.part_bytes > kOpsPartBytes || t.tiles > kOpsCounters) t.S = 1, t.part_bytes = 0;
+  return t;
+}
+
+hipError_t launch_i8(const I8Params& q, const I8Tactic& tac, hipStream_t s) {
+  I8Params p = q;
+  p.S = tac.S;
+  const int per = p.out_f32 ? 16 : 8;  // bytes of four outputs
+  p.c_quads = p.c_stride % per == 0;
+  if (tac.shape < 0) {
+    const unsigned tiles = (unsigned)((p.N + 15) / 16);
+    if (p.T <= 16)
+      hipLaunchKernelGGL(i8_rows_kernel<1>, dim3(tiles, (unsigned)((p.T + 15) / 16)), dim3(256), 0, s, p);
+    else
+      hipLaunchKernelGGL(i8_rows_kernel<4>, dim3(tiles, (unsigned)((p.T + 63) / 64)), dim3(256), 0, s, p);
+  } else {
+    launch_shape(tac.shape, p, tac.tiles * tac.S, s);
+  }
   return hipGetLastError();
 }
 

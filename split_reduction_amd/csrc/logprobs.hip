@@ -27,12 +27,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// Two floats to packed bf16 (round to nearest even) in one instruction.
-__device__ __forceinline__ uint32_t bf16_pair_hw(float lo, float hi) {
-  typedef float f32x2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
-}
-
 constexpr float kInf = __builtin_inff();
 typedef unsigned long long u64;
 

@@ -4,12 +4,54 @@
 
 #include <math.h>
 
+#include <map>
+#include <mutex>
+#include <utility>
+
 #include "ops_internal.h"
 #include "skgemm.h"
 
 namespace {
 
 bool aligned(const void* p, uintptr_t n) { return (uintptr_t)p % n == 0; }
+
+// ---- workspace: one of a fixed size per (device, stream) -------------------
+
+std::mutex g_mu;
+std::map<std::pair<int, hipStream_t>, uint8_t*> g_work;
+
+static_assert(skg::kOpsPartBytes + (size_t)skg::kOpsCounters * skg::kOpsCounterStride * 4 <= SKGEMM_OPS_WORKSPACE_BYTES,
+              "partial results and counters fit");
+
+// The stream's workspace, allocated and its counters zeroed on the first call.
+// It never grows or moves, so graphs captured with it stay valid until
+// skgemm_release. Under capture nothing can be allocated.
+int ops_workspace(hipStream_t stream, uint8_t** out) {
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return skg::hip_fail(e);
+  std::lock_guard<std::mutex> lock(g_mu);
+  auto it = g_work.find(std::make_pair(dev, stream));
+  if (it != g_work.end()) {
+    *out = it->second;
+    return SKGEMM_OK;
+  }
+  hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+  e = hipStreamIsCapturing(stream, &st);
+  if (e != hipSuccess) return skg::hip_fail(e);
+  if (st != hipStreamCaptureStatusNone) return SKGEMM_ENOMEM;
+  void* p = nullptr;
+  if (hipMalloc(&p, SKGEMM_OPS_WORKSPACE_BYTES) != hipSuccess) return SKGEMM_ENOMEM;
+  e = hipMemsetAsync(static_cast<uint8_t*>(p) + skg::kOpsPartBytes, 0, (size_t)skg::kOpsCounters * skg::kOpsCounterStride * 4,
+                     stream);
+  if (e != hipSuccess) {
+    (void)hipFree(p);
+    return skg::hip_fail(e);
+  }
+  g_work[std::make_pair(dev, stream)] = static_cast<uint8_t*>(p);
+  *out = static_cast<uint8_t*>(p);
+  return SKGEMM_OK;
+}
 
 // The logits' (or their gradient's) own arguments.
 int check_logits(const void* logits, int T, int V, float scale, int format, size_t stride) {
@@ -26,7 +68,31 @@ int check_logits(const void* logits, int T, int V, float scale, int format, size
 
 }  // namespace
 
+int skg::release_ops_workspaces() {
+  std::lock_guard<std::mutex> lock(g_mu);
+  int rc = SKGEMM_OK, caller_dev = -1;
+  if (hipGetDevice(&caller_dev) != hipSuccess) caller_dev = -1;
+  for (auto& kv : g_work) {
+    hipError_t e = hipSetDevice(kv.first.first);
+    if (e == hipSuccess) e = hipDeviceSynchronize();
+    if (e != hipSuccess) rc = hip_fail(e);
+    (void)hipFree(kv.second);
+  }
+  const bool any = !g_work.empty();
+  g_work.clear();
+  if (any && caller_dev >= 0) {
+    const hipError_t e = hipSetDevice(caller_dev);
+    if (e != hipSuccess && rc == SKGEMM_OK) rc = hip_fail(e);
+  }
+  return rc;
+}
+
 extern "C" {
+
+SKGEMM_API int skgemm_reserve_ops(hipStream_t stream) {
+  uint8_t* w = nullptr;
+  return ops_workspace(stream, &w);
+}
 
 SKGEMM_API int skgemm_rmsnorm(const void* X, const void* R, const void* G, void* R_out, void* Y,
                               float* y_scale, int T, int H, float eps, int out_format,
@@ -96,7 +162,15 @@ SKGEMM_API int skgemm_i8(const void* Wq, const float* w_scale, const void* Xq, c
   p.N = N;
   p.K = K;
   p.out_f32 = out_format == SKGEMM_F32;
-  const hipError_t e = skg::launch_i8(p, stream);
+  const skg::I8Tactic tac = skg::pick_i8(T, N, K);
+  if (tac.S > 1) {
+    uint8_t* w = nullptr;
+    const int rc = ops_workspace(stream, &w);
+    if (rc != SKGEMM_OK) return rc;
+    p.part = w;
+    p.cnt = reinterpret_cast<uint32_t*>(w + skg::kOpsPartBytes);
+  }
+  const hipError_t e = skg::launch_i8(p, tac, stream);
   return e == hipSuccess ? SKGEMM_OK : skg::hip_fail(e);
 }
 

@@ -29,7 +29,24 @@ struct I8Params {
   size_t w_stride, x_stride, c_stride;  // bytes
   int T, N, K;
   int out_f32;
+  int c_quads;    // four outputs of a row are aligned for one store
+  int S;          // workgroups that split K
+  uint8_t* part;  // sums [tiles, S, tile] (S > 1)
+  uint32_t* cnt;  // one arrival counter a tile, kOpsCounterStride words apart
 };
+
+// The workspace: partial results, then arrival counters, a 128-byte line each.
+constexpr size_t kOpsPartBytes = (size_t)32 << 20;
+constexpr int kOpsCounterStride = 32;
+constexpr int kOpsCounters = 8192;
+
+// How a call is run: tile shape (-1: operands straight into registers), K
+// split and what it needs of the workspace.
+struct I8Tactic {
+  int shape = -1, S = 1, tiles = 0;
+  size_t part_bytes = 0;
+};
+I8Tactic pick_i8(int T, int N, int K);
 
 struct LogprobParams {
   const uint8_t* logits;  // bf16 or float [T, V]
@@ -55,7 +72,7 @@ struct LogprobGradParams {
 
 hipError_t launch_logprobs(const LogprobParams& p, bool f32, hipStream_t s);
 hipError_t launch_logprobs_grad(LogprobGradParams p, bool f32, hipStream_t s);
-hipError_t launch_i8(const I8Params& p, hipStream_t s);
+hipError_t launch_i8(const I8Params& p, const I8Tactic& t, hipStream_t s);
 hipError_t launch_rmsnorm(const NormParams& p, int out_format, hipStream_t s);
 
 // hip_fail and the retained error live with the other entry points (api.hip).

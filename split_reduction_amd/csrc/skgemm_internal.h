@@ -57,6 +57,8 @@ enum Knob {
   kKnobPdefer,       // persistent kernel: partials held in LDS (1) or not (0)
   kKnobOwnerWait,    // owner wait bound in device-clock ticks
   kKnobHandoff,      // split-K hand-off of the persistent kernel: 0 counter, 1 mailbox
+  kKnobI8Shape,      // skgemm_i8: tile shape index (a value past the last: no tile)
+  kKnobI8Split,      // skgemm_i8: workgroups that split K
   kKnobCount
 };
 int knob(int k, int dflt);
