@@ -67,11 +67,31 @@ __device__ __forceinline__ uint32_t ld2_if(bool ok, rsrc_t r, uint32_t off) {
   return __builtin_amdgcn_raw_buffer_load_b16(r, ok ? off : kOOB, 0, POLICY);
 }
 
-// 16 bytes a lane straight from memory into LDS: lane l's go to lds + 16 l (lds
-// is the same in every lane). An offset at or past the bound gives zeros.
-__device__ __forceinline__ void ld16_to_lds(rsrc_t r, uint32_t off, uint32_t uniform_off, void* lds) {
-#ifdef __HIP_DEVICE_COMPILE__  // the host pass knows no 16-byte form
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, off, uniform_off, 0, 0);
+// A raw buffer resource as the four words an asm operand takes, in scalar
+// registers (base and bound are the same in every lane).
+__device__ __forceinline__ u32x4 make_rsrc_words(const void* base, uint32_t bytes) {
+  const uint64_t b = (uint64_t)(uintptr_t)base;
+  return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b),
+               (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(b >> 32) & 0xFFFFu)),
+               (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), (uint32_t)kRsrcWord3};
+}
+
+// The byte offset of an LDS object, as M0 and ds instructions count it.
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)p;
+}
+
+// 16 bytes a lane straight from memory into LDS, past the vector registers:
+// lane l's go to `lds` + 16 l (the same in every lane). An offset at or past the
+// bound gives zeros. In asm, because the compiler would wait for every such
+// load (vmcnt 0) at the next LDS read, whatever buffer that reads: the caller
+// counts the loads and waits itself before the barrier that publishes them.
+// No register is written, so nothing can be overwritten by a load in flight.
+__device__ __forceinline__ void ld16_to_lds(u32x4 rsrc, uint32_t off, uint32_t uniform_off, uint32_t lds) {
+#ifdef __HIP_DEVICE_COMPILE__
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(off), "s"(rsrc),
+               "s"(uniform_off)
+               : "memory", "m0");
 #endif
 }
 

@@ -103,76 +103,143 @@ __global__ __launch_bounds__(256) void i8_rows_kernel(I8Params p) {
 //
 // S workgroups may split K: each stores its sums to the workspace and the last
 // to arrive adds the others' (integers: the order does not matter).
+template <int BT, int BN>
+struct Tile {
+  int tile, rank, t0, n0, tokens, rows, s0, s1;
+  u32x4 w, x;  // buffer resources of the tile's rows
+
+  __device__ __forceinline__ explicit Tile(const I8Params& p) {
+    // Workgroups go to the 8 XCDs in turn; each XCD takes a run of tiles whose
+    // operands its L2 then holds, four token tiles for each feature tile.
+    const int ttiles = (p.T + BT - 1) / BT, ntiles = (p.N + BN - 1) / BN;
+    const int total = ttiles * ntiles * p.S, xcd = (int)blockIdx.x & 7;
+    const int idx = ((int)blockIdx.x >> 3) + xcd * (total >> 3) + min(xcd, total & 7);
+    rank = idx % p.S;
+    tile = idx / p.S;
+    const int group = tile / (4 * ntiles), in_group = tile - group * 4 * ntiles;
+    const int gt = min(4, ttiles - 4 * group);
+    t0 = (4 * group + in_group % gt) * BT;
+    n0 = in_group / gt * BN;
+    tokens = min(BT, p.T - t0);
+    rows = min(BN, p.N - n0);
+    w = make_rsrc_words(p.w + (size_t)n0 * p.w_stride, (uint32_t)((rows - 1) * p.w_stride + p.K));
+    x = make_rsrc_words(p.x + (size_t)t0 * p.x_stride, (uint32_t)((tokens - 1) * p.x_stride + p.K));
+    const long steps = (p.K + 127) / 128;
+    s0 = (int)(steps * rank / p.S);
+    s1 = (int)(steps * (rank + 1) / p.S);
+  }
+};
+
+// A wave's share of the loads of a step: kXL and kWL instructions.
+template <int BT, int BN, int kWaves>
+struct Loader {
+  static constexpr int kXL = BT / 8 / kWaves, kWL = BN / 8 / kWaves;
+  static constexpr int kStage = (BT + BN) * 128;
+  static_assert(kXL >= 1 && kWL >= 1 && kXL * kWaves * 8 == BT && kWL * kWaves * 8 == BN, "whole loads");
+  uint32_t xoff[kXL], woff[kWL];
+  int chunk, wave;
+
+  __device__ __forceinline__ Loader(const I8Params& p, const Tile<BT, BN>& t, int lane, int wave_) : wave(wave_) {
+    const int row8 = lane >> 3;
+    chunk = 16 * ((lane & 7) ^ row8);
+    // A row past the tile's end loads zeros (out of range).
+#pragma unroll
+    for (int q = 0; q < kXL; ++q) {
+      const int r = 8 * (wave * kXL + q) + row8;
+      xoff[q] = r < t.tokens ? (uint32_t)(r * p.x_stride + chunk) : kOOB;
+    }
+#pragma unroll
+    for (int q = 0; q < kWL; ++q) {
+      const int r = 8 * (wave * kWL + q) + row8;
+      woff[q] = r < t.rows ? (uint32_t)(r * p.w_stride + chunk) : kOOB;
+    }
+  }
+  __device__ __forceinline__ void issue(const Tile<BT, BN>& t, int K, int s, uint32_t at) const {
+    const uint32_t past = 128 * s + chunk < K ? 0u : kOOB;  // K ends inside the last step
+#pragma unroll
+    for (int q = 0; q < kWL; ++q) ld16_to_lds(t.w, woff[q] | past, 128 * s, at + BT * 128 + (wave * kWL + q) * 1024);
+#pragma unroll
+    for (int q = 0; q < kXL; ++q) ld16_to_lds(t.x, xoff[q] | past, 128 * s, at + (wave * kXL + q) * 1024);
+  }
+};
+
+// Joins the sums of the S workgroups of a tile (true in the one that holds them
+// all afterwards). Sums are stored as they lie in the registers: 16 bytes a
+// lane, 1 KB a store.
+template <int kTile, int kSums>
+__device__ __forceinline__ bool join_ranks(const I8Params& p, int tile, int rank, i32x4* acc, int lane, int wave) {
+  __shared__ uint32_t arrived;
+  const rsrc_t part = make_rsrc(p.part + (size_t)tile * p.S * kTile, (uint32_t)p.S * kTile);
+  const uint32_t at = (uint32_t)(wave * kSums * 1024 + lane * 16);
+#pragma unroll
+  for (int k = 0; k < kSums; ++k)
+    st16_coherent_if(true, __builtin_bit_cast(u32x4, acc[k]), part, (uint32_t)rank * kTile + at + k * 1024u);
+  wait_vmem_all();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    uint32_t* const cnt = p.cnt + (size_t)tile * kOpsCounterStride;
+    const uint32_t a = __hip_atomic_fetch_add(cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    // Everyone has arrived: the counter is ready for the next call.
+    if (a + 1 == (uint32_t)p.S) __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    arrived = a;
+  }
+  __syncthreads();
+  if (arrived + 1 != (uint32_t)p.S) return false;
+  handoff_order();
+  for (int r = 0; r < p.S; ++r) {
+    if (r == rank) continue;
+#pragma unroll
+    for (int k = 0; k < kSums; ++k)
+      acc[k] += __builtin_bit_cast(i32x4, ld16_coherent_if(true, part, (uint32_t)r * kTile + at + k * 1024u));
+  }
+  return true;
+}
+
+// The outputs of a wave's kNT x kMT blocks of 16 features x 16 tokens, block
+// (0, 0) at feature n0 and token t0.
+template <int kNT, int kMT>
+__device__ __forceinline__ void store_blocks(const I8Params& p, int t0, int n0, const i32x4* acc, int lane) {
+  const int i = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int k = 0; k < kNT; ++k) {
+    const int n = n0 + 16 * k + 4 * g;
+    float ws[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) ws[e] = n + e < p.N ? p.w_scale[n + e] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < kMT; ++j) {
+      const int t = t0 + 16 * j + i;
+      if (t < p.T) store_sums(p, t, n, acc[k * kMT + j], p.x_scale[t], ws);
+    }
+  }
+}
+
 template <int BT, int BN, int WT, int WN, int STG>
 __global__ __launch_bounds__(64 * WT * WN) void i8_tile_kernel(I8Params p) {
-  constexpr int kWaves = WT * WN, kMT = BT / WT / 16, kNT = BN / WN / 16;
-  constexpr int kXL = BT / 8 / kWaves, kWL = BN / 8 / kWaves;  // loads of a wave and step
-  constexpr int kStage = (BT + BN) * 128;
-  static_assert(kXL >= 1 && kWL >= 1 && kXL * kWaves * 8 == BT && kWL * kWaves * 8 == BN, "whole loads");
-  __shared__ __align__(1024) uint8_t lds[STG * kStage];
-  __shared__ uint32_t arrived;
+  constexpr int kMT = BT / WT / 16, kNT = BN / WN / 16;
+  typedef Loader<BT, BN, WT * WN> L;
+  __shared__ __align__(1024) uint8_t lds[STG * L::kStage];
   const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int i = lane & 15, g = lane >> 4;
-
-  // Workgroups go to the 8 XCDs in turn; each XCD takes a run of tiles whose
-  // operands its L2 then holds, four token tiles for each feature tile.
-  const int ttiles = (p.T + BT - 1) / BT, ntiles = (p.N + BN - 1) / BN, tiles = ttiles * ntiles;
-  const int total = tiles * p.S;
-  int idx = (int)blockIdx.x;
-  {
-    const int xcd = idx & 7, each = total >> 3, more = total & 7;
-    idx = (idx >> 3) + xcd * each + min(xcd, more);
-  }
-  const int rank = idx % p.S, tile = idx / p.S;
-  const int group = tile / (4 * ntiles), in_group = tile - group * 4 * ntiles;
-  const int gt = min(4, ttiles - 4 * group);
-  const int t0 = (4 * group + in_group % gt) * BT, n0 = in_group / gt * BN;
-  const int tokens = min(BT, p.T - t0), rows = min(BN, p.N - n0);
-  const rsrc_t w = make_rsrc(p.w + (size_t)n0 * p.w_stride, (uint32_t)((rows - 1) * p.w_stride + p.K));
-  const rsrc_t x = make_rsrc(p.x + (size_t)t0 * p.x_stride, (uint32_t)((tokens - 1) * p.x_stride + p.K));
-  const int steps = (p.K + 127) / 128;
-  const int s0 = (int)((long)steps * rank / p.S), s1 = (int)((long)steps * (rank + 1) / p.S);
-
-  // This lane's offsets; a row past the tile's end loads zeros (out of range).
-  const int row8 = lane >> 3, chunk = 16 * ((lane & 7) ^ row8);
-  uint32_t xoff[kXL], woff[kWL];
-#pragma unroll
-  for (int q = 0; q < kXL; ++q) {
-    const int r = 8 * (wave * kXL + q) + row8;
-    xoff[q] = r < tokens ? (uint32_t)(r * p.x_stride + chunk) : kOOB;
-  }
-#pragma unroll
-  for (int q = 0; q < kWL; ++q) {
-    const int r = 8 * (wave * kWL + q) + row8;
-    woff[q] = r < rows ? (uint32_t)(r * p.w_stride + chunk) : kOOB;
-  }
-  auto issue = [&](int s, int buf) {
-    uint8_t* const at = lds + buf * kStage;
-    const uint32_t past = 128 * s + chunk < p.K ? 0u : kOOB;  // K ends inside the last step
-#pragma unroll
-    for (int q = 0; q < kWL; ++q)
-      ld16_to_lds(w, woff[q] | past, 128 * s, at + BT * 128 + (wave * kWL + q) * 1024);
-#pragma unroll
-    for (int q = 0; q < kXL; ++q)
-      ld16_to_lds(x, xoff[q] | past, 128 * s, at + (wave * kXL + q) * 1024);
-  };
-
-  i32x4 acc[kNT][kMT] = {};
+  const Tile<BT, BN> t(p);
+  const L load(p, t, lane, wave);
+  const uint32_t base = lds_offset(lds);
+  i32x4 acc[kNT * kMT] = {};
   const int wt = wave / WN, wn = wave % WN;
   const int pos0 = i * 128 + 16 * (g ^ (i & 7)), pos1 = i * 128 + 16 * ((4 + g) ^ (i & 7));
   const int xbase = wt * (BT / WT) * 128, wbase = BT * 128 + wn * (BN / WN) * 128;
 #pragma unroll
   for (int s = 0; s < STG - 1; ++s)
-    if (s0 + s < s1) issue(s0 + s, s);
+    if (t.s0 + s < t.s1) load.issue(t, p.K, t.s0 + s, base + s * L::kStage);
   int buf = 0;
-  for (int s = s0; s < s1; ++s) {
+  for (int s = t.s0; s < t.s1; ++s) {
     // The loads of steps s + 1 .. s + STG - 2 may stay in flight.
-    if (s + STG - 2 < s1)
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STG - 2) * (kXL + kWL)) : "memory");
+    if (s + STG - 2 < t.s1)
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STG - 2) * (L::kXL + L::kWL)) : "memory");
     else
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (s + STG - 1 < s1) issue(s + STG - 1, buf == 0 ? STG - 1 : buf - 1);
-    const uint8_t* const at = lds + buf * kStage;
+    if (s + STG - 1 < t.s1) load.issue(t, p.K, s + STG - 1, base + (buf == 0 ? STG - 1 : buf - 1) * L::kStage);
+    const uint8_t* const at = lds + buf * L::kStage;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int pos = h ? pos1 : pos0;
@@ -184,56 +251,89 @@ __global__ __launch_bounds__(64 * WT * WN) void i8_tile_kernel(I8Params p) {
 #pragma unroll
       for (int j = 0; j < kMT; ++j)
 #pragma unroll
-        for (int k = 0; k < kNT; ++k) acc[k][j] = mfma_i8(a[k], b[j], acc[k][j]);
+        for (int k = 0; k < kNT; ++k) acc[k * kMT + j] = mfma_i8(a[k], b[j], acc[k * kMT + j]);
     }
     buf = buf + 1 == STG ? 0 : buf + 1;
   }
+  if (p.S > 1 && !join_ranks<BT * BN * 4, kNT * kMT>(p, t.tile, t.rank, acc, lane, wave)) return;
+  store_blocks<kNT, kMT>(p, t.t0 + wt * (BT / WT), t.n0 + wn * (BN / WN), acc, lane);
+}
 
-  if (p.S > 1) {
-    // Sums as they lie in the registers: 16 bytes a lane, 1 KB a store.
-    constexpr uint32_t kTile = BT * BN * 4;
-    const rsrc_t part = make_rsrc(p.part + (size_t)tile * p.S * kTile, (uint32_t)p.S * kTile);
-    const uint32_t own = (uint32_t)rank * kTile + (uint32_t)(wave * kNT * kMT * 1024 + lane * 16);
+// The same tile for matrix-core bound calls: 256 x 256, two waves a SIMD that
+// take turns. A step is four phases, each closed by a barrier: operands of the
+// first 64 bytes of K from LDS (R0), their products (M0), the other 64 bytes
+// (R1, M1). Waves 4-7 (the second of each SIMD) run one phase behind waves 0-3,
+// so that while one wave of a SIMD multiplies the other reads: the matrix unit
+// is fed without a pause and only four waves at a time share the LDS
+// (12 x 8 cycles each, 384 against 512 of a phase's 32 products).
+// With A's step s in phases 4s .. 4s+3 and B's one later, the last reads of
+// step s - 1 are B's R1 in phase 4s - 1: from phase 4s on its buffer may be
+// filled for step s + 1 (A issues in its R0, B in its M1 before), and the loads
+// have to have landed by the end of phase 4s + 3 (A waits in its M1, B in its
+// R1): four phases, about a microsecond.
+__global__ __launch_bounds__(512) void i8_big_kernel(I8Params p) {
+  constexpr int kMT = 8, kNT = 4;
+  typedef Loader<256, 256, 8> L;
+  __shared__ __align__(1024) uint8_t lds[2 * L::kStage];
+  const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int i = lane & 15, g = lane >> 4;
+  const Tile<256, 256> t(p);
+  const L load(p, t, lane, wave);
+  const uint32_t base = lds_offset(lds);
+  const bool second = wave >= 4;
+  // Two token halves x four feature quarters.
+  const int wt = wave & 1, wn = wave >> 1;
+  const int pos0 = i * 128 + 16 * (g ^ (i & 7)), pos1 = i * 128 + 16 * ((4 + g) ^ (i & 7));
+  const int xbase = wt * 128 * 128, wbase = 256 * 128 + wn * 64 * 128;
+  i32x4 acc[kNT * kMT] = {};
+  u32x4 a[kNT], b[kMT];
+  auto read = [&](const uint8_t* at, int pos) {
 #pragma unroll
-    for (int k = 0; k < kNT; ++k)
+    for (int j = 0; j < kNT; ++j) a[j] = *reinterpret_cast<const u32x4*>(at + wbase + j * 2048 + pos);
 #pragma unroll
-      for (int j = 0; j < kMT; ++j)
-        st16_coherent_if(true, __builtin_bit_cast(u32x4, acc[k][j]), part, own + (uint32_t)(k * kMT + j) * 1024u);
-    wait_vmem_all();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      uint32_t* const cnt = p.cnt + (size_t)tile * kOpsCounterStride;
-      const uint32_t a = __hip_atomic_fetch_add(cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      // Everyone has arrived: the counter is ready for the next call.
-      if (a + 1 == (uint32_t)p.S) __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      arrived = a;
-    }
-    __syncthreads();
-    if (arrived + 1 != (uint32_t)p.S) return;
-    handoff_order();
-    for (int r = 0; r < p.S; ++r) {
-      if (r == rank) continue;
-      const uint32_t other = (uint32_t)r * kTile + (uint32_t)(wave * kNT * kMT * 1024 + lane * 16);
+    for (int j = 0; j < kMT; ++j) b[j] = *reinterpret_cast<const u32x4*>(at + xbase + j * 2048 + pos);
+  };
+  auto multiply = [&]() {
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-      for (int k = 0; k < kNT; ++k)
+    for (int j = 0; j < kMT; ++j)
 #pragma unroll
-        for (int j = 0; j < kMT; ++j)
-          acc[k][j] += __builtin_bit_cast(i32x4, ld16_coherent_if(true, part, other + (uint32_t)(k * kMT + j) * 1024u));
-    }
+      for (int k = 0; k < kNT; ++k) acc[k * kMT + j] = mfma_i8(a[k], b[j], acc[k * kMT + j]);
+    __builtin_amdgcn_s_setprio(0);
+  };
+  auto close = [&]() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto close_loads = [&]() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  if (t.s0 < t.s1) load.issue(t, p.K, t.s0, base);
+  close_loads();
+  if (second) {
+    if (t.s0 + 1 < t.s1) load.issue(t, p.K, t.s0 + 1, base + L::kStage);
+    close();
   }
-
-#pragma unroll
-  for (int k = 0; k < kNT; ++k) {
-    const int n = n0 + wn * (BN / WN) + 16 * k + 4 * g;
-    float ws[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) ws[e] = n + e < p.N ? p.w_scale[n + e] : 0.0f;
-#pragma unroll
-    for (int j = 0; j < kMT; ++j) {
-      const int t = t0 + wt * (BT / WT) + 16 * j + i;
-      if (t < p.T) store_sums(p, t, n, acc[k][j], p.x_scale[t], ws);
-    }
+  for (int s = t.s0; s < t.s1; ++s) {
+    const uint32_t buf = (uint32_t)(s - t.s0) & 1u;
+    const uint8_t* const at = lds + buf * L::kStage;
+    if (!second && s + 1 < t.s1) load.issue(t, p.K, s + 1, base + (buf ^ 1u) * L::kStage);
+    read(at, pos0);
+    close();
+    multiply();
+    close();
+    read(at, pos1);
+    if (second) close_loads(); else close();
+    if (second && s + 2 < t.s1) load.issue(t, p.K, s + 2, base + buf * L::kStage);
+    multiply();
+    if (!second) close_loads(); else close();
   }
+  if (!second) close();  // the waves behind have one phase to go
+  if (p.S > 1 && !join_ranks<256 * 256 * 4, kNT * kMT>(p, t.tile, t.rank, acc, lane, wave)) return;
+  store_blocks<kNT, kMT>(p, t.t0 + wt * 128, t.n0 + wn * 64, acc, lane);
 }
 
 }  // namespace
@@ -253,7 +353,9 @@ void launch_tile(const I8Params& p, int grid, hipStream_t s) {
 
 void launch_shape(int shape, const I8Params& p, int grid, hipStream_t s) {
   switch (shape) {
-    case 0: return launch_tile<256, 256, 2, 4, 2>(p, grid, s);
+    case 0:
+      hipLaunchKernelGGL(i8_big_kernel, dim3((unsigned)grid), dim3(512), 0, s, p);
+      return;
     case 1: return launch_tile<256, 128, 2, 4, 3>(p, grid, s);
     case 2: return launch_tile<128, 128, 2, 2, 2>(p, grid, s);
     case 3: return launch_tile<128, 128, 2, 2, 4>(p, grid, s);
