@@ -119,6 +119,13 @@ def _check(code: int, name: str) -> None:
         raise SkgemmError(code, f"{name}: {strerror(code)}{extra}")
 
 
+def _on_gpu(a) -> bool:
+    try:
+        return a.is_cuda  # a tenth of the time that a.device.type takes
+    except AttributeError:
+        return a.device.type == "cuda"
+
+
 def _ptr(a, nbytes: int = 0, what: str = "argument") -> int:
     """Device address of a tensor or of a plain integer address (None is 0).
 
@@ -132,7 +139,7 @@ def _ptr(a, nbytes: int = 0, what: str = "argument") -> int:
         return 0
     if isinstance(a, int):
         return a
-    if a.device.type != "cuda":
+    if not _on_gpu(a):
         raise SkgemmError(SKGEMM_EINVAL, f"{what}: a tensor on {a.device}, not on the GPU")
     if not a.is_contiguous():
         raise SkgemmError(SKGEMM_EINVAL, f"{what}: not contiguous")
@@ -149,9 +156,11 @@ def _rows(a, rows: int, row_bytes: int, stride, what: str, esize: int = 0):
     `esize` bytes (0: any) and reach to the end of the last row."""
     if a is None or isinstance(a, int):
         return a or 0, row_bytes if stride is None else stride
-    if a.device.type != "cuda":
+    if not _on_gpu(a):
         raise SkgemmError(SKGEMM_EINVAL, f"{what}: a tensor on {a.device}, not on the GPU")
     size = a.element_size()
+    if (size == esize or not esize) and stride is None and a.numel() * size == rows * row_bytes and a.is_contiguous():
+        return a.data_ptr(), row_bytes  # dense
     if esize and size != esize:
         raise SkgemmError(SKGEMM_EINVAL, f"{what}: elements of {size} bytes, the call's have {esize}")
     n = a.numel() * size
@@ -200,11 +209,20 @@ def _batched(L: int, stride: int, one: int) -> int:
     return 0 if L <= 0 or one == 0 else (L - 1) * max(stride, 0) + one
 
 
+def _current_stream() -> int:
+    """torch's current stream on the current device, without the Stream object
+    that torch.cuda.current_stream() builds (2.7 us of a call's 11)."""
+    import torch
+
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return torch.cuda.current_stream().cuda_stream
+    return raw(torch.cuda.current_device())
+
+
 def _stream(stream) -> int:
     if stream is None:
-        import torch
-
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -15,6 +15,8 @@
 // exponential at a quarter rate: at 2 bytes a logit the arithmetic needs
 // nearly as long as the read, so what is not asked for is left out.
 
+#include <algorithm>
+
 #include "device/block.h"
 #include "device/pack.h"
 #include "ops_internal.h"
@@ -229,19 +231,43 @@ struct RowItems {
   }
 };
 
+// Keys in the workspace, kept by the workgroups of a row, as block_top's items.
+struct KeyItems {
+  static constexpr int kE = 1;
+  const uint8_t* work;
+  int k, n;  // keys a part, keys in all
+  __device__ __forceinline__ int per_owner() const { return (n + kThreads - 1) / kThreads; }
+  __device__ __forceinline__ u64 at(int item) const {
+    const u64* p = reinterpret_cast<const u64*>(work + (size_t)(item / k) * kLogprobPart + 16) + item % k;
+    return __hip_atomic_load(const_cast<u64*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __device__ __forceinline__ void keys(int item, u64* key) const { key[0] = item < n ? at(item) : 0; }
+};
+
+__device__ __forceinline__ void store_agent(float* p, float v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float load_agent(float* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// A row, or where there are few rows one of p.parts runs of its vectors: the
+// workgroup that finishes a row's last run joins the sums and the best k that
+// the others left in the workspace.
 template <bool F32>
 __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobParams p) {
   __shared__ TopLds top;
   __shared__ Sums part[kThreads / 64];
-  const size_t t = blockIdx.x;
+  __shared__ uint32_t arrived;
+  const int tid = (int)threadIdx.x;
+  const size_t t = blockIdx.x / (unsigned)p.parts;
+  const int run = (int)(blockIdx.x - (unsigned)t * (unsigned)p.parts);
   const Row<F32> row(p.logits + t * p.stride, p.V);
   constexpr int kE = Row<F32>::kE;
   const float mul = p.scale * kLog2e;
+  const int first = run * p.per, n = max(0, min(p.per, row.nvec - first));
   Sums a = {-kInf, 0.0f, 0.0f};
-  const bool any = (int)threadIdx.x < row.nvec;
-  for (int j = (int)threadIdx.x; j < row.nvec; j += kThreads) {
-    float x[kE];
-    row.load(j, x, -kInf);
+  auto add = [&](const float* x) {
     float m = a.m;
 #pragma unroll
     for (int e = 0; e < kE; ++e) m = fmaxf(m, x[e]);
@@ -258,18 +284,98 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobParams p) {
       a.s += w;
       a.u = fmaf(w, fmaxf(d, -1e30f), a.u);  // 0 * -1e30 where 0 * -inf would be NaN
     }
+  };
+  {
+    // Thread tid takes vectors first + tid, + 256, ...: whole ones four loads at
+    // a time, then the row's partial ends where they are this thread's.
+    const int w0 = row.whole(0) ? 0 : 1, w1 = row.whole(row.nvec - 1) ? row.nvec : row.nvec - 1;
+    const int end = min(first + n, w1);
+    int j = first + tid;
+    if (j < w0) j += kThreads;
+    for (; j + 3 * kThreads < end; j += 4 * kThreads) {
+      u32x4 v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = row.load_whole(j + q * kThreads);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float x[kE];
+        Row<F32>::unpack(v[q], x);
+        add(x);
+      }
+    }
+    for (; j < end; j += kThreads) {
+      float x[kE];
+      Row<F32>::unpack(row.load_whole(j), x);
+      add(x);
+    }
+    const int last = row.nvec - 1;
+    for (int q = 0; q < 2; ++q) {
+      const int edge = q == 0 ? 0 : last;
+      if (row.whole(edge) || (q == 1 && last == 0)) continue;
+      if (edge < first || edge >= first + n || (edge - first) % kThreads != tid) continue;
+      float x[kE];
+      row.load(edge, x, -kInf);
+      add(x);
+    }
   }
   const float most = a.m;  // of this thread's logits
+  const bool any = tid < n;
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) a = join(a, Sums{shfl_xor(a.m, off), shfl_xor(a.s, off), shfl_xor(a.u, off)}, mul);
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = a;
+  if ((tid & 63) == 0) part[tid >> 6] = a;
   __syncthreads();
   a = part[0];
   for (int i = 1; i < kThreads / 64; ++i) a = join(a, part[i], mul);
+  const RowItems<F32> items{row, first, n};
+  const uint32_t best = any ? order_bits(most) : 0u;
+
+  if (p.parts > 1) {
+    uint8_t* const work = p.part + t * (size_t)p.parts * kLogprobPart;
+    uint8_t* const mine = work + (size_t)run * kLogprobPart;
+    if (tid == 0) {
+      store_agent(reinterpret_cast<float*>(mine), a.m);
+      store_agent(reinterpret_cast<float*>(mine) + 1, a.s);
+      store_agent(reinterpret_cast<float*>(mine) + 2, a.u);
+    }
+    if (p.k > 0) {
+      u64* const keys = reinterpret_cast<u64*>(mine + 16);
+      block_top(items, best, p.k, top, [&](int rank, u64 key) {
+        __hip_atomic_store(keys + rank, key, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      });
+      // A run of fewer than k elements leaves the rest empty.
+      if (tid >= top.n_cand && tid < p.k)
+        __hip_atomic_store(keys + tid, (u64)0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    wait_vmem_all();
+    __syncthreads();
+    if (tid == 0) {
+      uint32_t* const cnt = p.cnt + t * kOpsCounterStride;
+      const uint32_t c = __hip_atomic_fetch_add(cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (c + 1 == (uint32_t)p.parts) __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      arrived = c;
+    }
+    __syncthreads();
+    if (arrived + 1 != (uint32_t)p.parts) return;
+    handoff_order();
+    a = Sums{-kInf, 0.0f, 0.0f};
+    if (tid < p.parts) {  // at most 64: one wave
+      float* const f = reinterpret_cast<float*>(work + (size_t)tid * kLogprobPart);
+      a = Sums{load_agent(f), load_agent(f + 1), load_agent(f + 2)};
+    }
+    if (tid < 64) {
+#pragma unroll
+      for (int off = 32; off > 0; off >>= 1)
+        a = join(a, Sums{shfl_xor(a.m, off), shfl_xor(a.s, off), shfl_xor(a.u, off)}, mul);
+      if (tid == 0) part[0] = a;
+    }
+    __syncthreads();
+    a = part[0];
+  }
+
   // s is NaN exactly where the row holds a NaN or +inf.
   const bool bad = !(a.s == a.s), empty = a.s == 0.0f;
   const float log_s = __builtin_amdgcn_logf(a.s);  // log2
-  if (threadIdx.x == 0) {
+  if (tid == 0) {
     if (p.lse != nullptr) p.lse[t] = bad ? a.s : empty ? -kInf : fmaf(a.m, p.scale, log_s * kLn2);
     if (p.entropy != nullptr) p.entropy[t] = empty ? 0.0f : (log_s - a.u / a.s) * kLn2;
     if (p.logprob != nullptr) {
@@ -286,18 +392,28 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobParams p) {
   float* tv = p.top_logprob + t * (size_t)p.k;
   int64_t* ti = p.top_ids + t * (size_t)p.k;
   if (bad) {
-    if ((int)threadIdx.x < p.k) {
-      tv[threadIdx.x] = a.s;
-      ti[threadIdx.x] = -1;
+    if (tid < p.k) {
+      tv[tid] = a.s;
+      ti[tid] = -1;
     }
     return;
   }
-  const RowItems<F32> items{row, 0, row.nvec};
-  block_top(items, any ? order_bits(most) : 0u, p.k, top, [&](int rank, u64 key) {
+  auto out = [&](int rank, u64 key) {
     const float v = order_value((uint32_t)(key >> 32));
     tv[rank] = empty ? -kInf : (v - a.m) * p.scale - log_s * kLn2;
     ti[rank] = key_index(key);
-  });
+  };
+  if (p.parts == 1) {
+    block_top(items, best, p.k, top, out);
+  } else {
+    const KeyItems kept{p.part + t * (size_t)p.parts * kLogprobPart, p.k, p.parts * p.k};
+    u64 high = 0;
+    for (int i = tid; i < kept.n; i += kThreads) {
+      const u64 key = kept.at(i);
+      high = key > high ? key : high;
+    }
+    block_top(kept, (uint32_t)(high >> 32), p.k, top, out);
+  }
 }
 
 // ---- the gradient -------------------------------------------------------------
@@ -367,11 +483,22 @@ __global__ __launch_bounds__(kThreads) void logprobs_grad_kernel(LogprobGradPara
 
 }  // namespace
 
+// A row is split while there are fewer workgroups than keep the card busy, down
+// to one vector a thread; at most 64 runs, so that one wave joins them.
+int logprob_parts(int T, int V, bool f32, int* per) {
+  const int steps = (V / (f32 ? 4 : 8) + 2 + kThreads - 1) / kThreads;  // vectors a thread, partial ends included
+  const int want = std::max(1, std::min(64, 2048 / std::max(T, 1)));
+  const int each = (steps + want - 1) / want;
+  *per = each * kThreads;
+  return (steps + each - 1) / each;
+}
+
 hipError_t launch_logprobs(const LogprobParams& p, bool f32, hipStream_t s) {
+  const dim3 grid((unsigned)p.T * (unsigned)p.parts);
   if (f32)
-    hipLaunchKernelGGL(logprobs_kernel<true>, dim3((unsigned)p.T), dim3(kThreads), 0, s, p);
+    hipLaunchKernelGGL(logprobs_kernel<true>, grid, dim3(kThreads), 0, s, p);
   else
-    hipLaunchKernelGGL(logprobs_kernel<false>, dim3((unsigned)p.T), dim3(kThreads), 0, s, p);
+    hipLaunchKernelGGL(logprobs_kernel<false>, grid, dim3(kThreads), 0, s, p);
   return hipGetLastError();
 }
 

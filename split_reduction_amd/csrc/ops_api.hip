@@ -201,6 +201,14 @@ SKGEMM_API int skgemm_logprobs(const void* logits, const int64_t* tokens, float*
   p.V = V;
   p.k = top_k;
   p.scale = scale;
+  p.parts = skg::logprob_parts(T, V, logits_format == SKGEMM_F32, &p.per);
+  if (p.parts > 1) {  // then T <= 1024: at most 2048 runs
+    uint8_t* w = nullptr;
+    rc = ops_workspace(stream, &w);
+    if (rc != SKGEMM_OK) return rc;
+    p.part = w;
+    p.cnt = reinterpret_cast<uint32_t*>(w + skg::kOpsPartBytes);
+  }
   const hipError_t e = skg::launch_logprobs(p, logits_format == SKGEMM_F32, stream);
   return e == hipSuccess ? SKGEMM_OK : skg::hip_fail(e);
 }

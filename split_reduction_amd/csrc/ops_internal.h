@@ -57,7 +57,12 @@ struct LogprobParams {
   size_t stride;          // bytes between rows of logits
   int T, V, k;
   float scale;
+  int parts, per;  // workgroups a row, vectors a workgroup
+  uint8_t* part;   // their results [T, parts], kLogprobPart bytes each (parts > 1)
+  uint32_t* cnt;   // one arrival counter a row
 };
+constexpr size_t kLogprobPart = 16 + 64 * 8;  // three sums, the best 64 keys
+int logprob_parts(int T, int V, bool f32, int* per);
 
 struct LogprobGradParams {
   const uint8_t* logits;
