@@ -222,7 +222,7 @@ SKGEMM_API int skgemm_mxfp8_batched(const void* Wq8, const void* Wscale, const v
  * allocates it, skgemm_reserve_ops does so ahead of a graph capture, and
  * skgemm_release frees it.
  */
-#define SKGEMM_OPS_WORKSPACE_BYTES ((size_t)33 << 20)
+#define SKGEMM_OPS_WORKSPACE_BYTES ((size_t)65 << 20)
 enum skgemm_format {
   SKGEMM_BF16 = 0,
   SKGEMM_I8 = 1,   /* two's complement codes in -127..127, one FP32 scale a row */

@@ -35,6 +35,7 @@ KNOBS = {"kind": 0, "stream": 1, "shape": 2, "fold": 3, "cluster_c": 4, "wg_per_
 FORMATS = {"bf16": 0, "i8": 1, "e4m3": 2, "f32": 3}
 
 _lib = None
+_raw_stream = _device = None  # torch's functions, bound by the first call that asks for the stream
 
 
 class SkgemmError(RuntimeError):
@@ -159,10 +160,10 @@ def _rows(a, rows: int, row_bytes: int, stride, what: str, esize: int = 0):
     if not _on_gpu(a):
         raise SkgemmError(SKGEMM_EINVAL, f"{what}: a tensor on {a.device}, not on the GPU")
     size = a.element_size()
-    if (size == esize or not esize) and stride is None and a.numel() * size == rows * row_bytes and a.is_contiguous():
-        return a.data_ptr(), row_bytes  # dense
     if esize and size != esize:
         raise SkgemmError(SKGEMM_EINVAL, f"{what}: elements of {size} bytes, the call's have {esize}")
+    if stride is None and a.numel() * size == rows * row_bytes and a.is_contiguous():
+        return a.data_ptr(), row_bytes  # dense
     n = a.numel() * size
     if a.is_contiguous():
         if stride is None:
@@ -212,12 +213,15 @@ def _batched(L: int, stride: int, one: int) -> int:
 def _current_stream() -> int:
     """torch's current stream on the current device, without the Stream object
     that torch.cuda.current_stream() builds (2.7 us of a call's 11)."""
-    import torch
+    global _raw_stream, _device
+    if _device is None:
+        import torch
 
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is None:
-        return torch.cuda.current_stream().cuda_stream
-    return raw(torch.cuda.current_device())
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if _raw_stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        _device = torch.cuda.current_device
+    return _raw_stream(_device())
 
 
 def _stream(stream) -> int:

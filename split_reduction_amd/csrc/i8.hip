@@ -7,6 +7,8 @@
 // row (column) i at K block g, and D's rows 4g..4g+3 of column i. Sums of
 // 32-bit integers are exact and commute, so K is split over waves freely.
 
+#include <algorithm>
+
 #include "device/block.h"
 #include "device/pack.h"
 #include "ops_internal.h"
@@ -47,38 +49,89 @@ __device__ __forceinline__ void store_sums(const I8Params& p, int t, int n, i32x
   }
 }
 
-// Four waves a workgroup split K over a tile of 16 features x 16 NT tokens,
-// operands straight from memory into registers, sums joined in LDS.
-template <int NT>
-__global__ __launch_bounds__(256) void i8_rows_kernel(I8Params p) {
-  __shared__ i32x4 part[4][NT][64];
-  const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-  const int i = lane & 15, g = lane >> 4;
-  const int n0 = (int)blockIdx.x * 16, t0 = (int)blockIdx.y * 16 * NT;
-  const int rows = min(16, p.N - n0), tokens = min(16 * NT, p.T - t0);
-  // Resources end with the tile's last row: a row past it reads zeros, and so
-  // does K past a row's end by an out-of-range offset.
+// Few tokens: the weights' stream is everything. A workgroup of WAVES waves
+// takes 16 RG features x 16 NT tokens, operands straight from memory into
+// registers; the waves take the row's 128-byte units in turn and their sums meet
+// in LDS, so K is split without a second pass.
+//
+// Both operands come as line pairs (device/types.h): 8 rows x 128 bytes a load,
+// whole lines; one DPP move a register makes the two 16-row operands. With at
+// most 8 tokens the second load of the activations' pair is left out. U units
+// are in flight in each wave: a slot is consumed, then refilled.
+template <int NT, bool LOW, int RG, int WAVES, int U>
+__global__ __launch_bounds__(64 * WAVES) void i8_rows_kernel(I8Params p) {
+  constexpr int kXL = LOW ? 1 : 2;  // loads of 16 tokens
+  static_assert(!LOW || NT == 1, "at most 8 tokens are one half tile");
+  __shared__ i32x4 part[WAVES][RG * NT][64];
+  const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int li = lane & 15, g = lane >> 4;
+  const int ntiles = (p.N + 16 * RG - 1) / (16 * RG);
+  const int tt = (int)blockIdx.x / ntiles;
+  const int n0 = ((int)blockIdx.x - tt * ntiles) * 16 * RG, t0 = tt * 16 * NT;
+  const int rows = min(16 * RG, p.N - n0), tokens = min(16 * NT, p.T - t0);
   const rsrc_t w = make_rsrc(p.w + (size_t)n0 * p.w_stride, (uint32_t)((rows - 1) * p.w_stride + p.K));
   const rsrc_t x = make_rsrc(p.x + (size_t)t0 * p.x_stride, (uint32_t)((tokens - 1) * p.x_stride + p.K));
-  i32x4 acc[NT] = {};
-  for (int k = wave * 64; k < p.K; k += 256) {
-    const int kk = k + 16 * g;
-    const bool ok = kk < p.K;
-    const u32x4 a = ld16_if(ok && i < rows, w, (uint32_t)(i * p.w_stride + kk));
+  const int in_line = 64 * (li >> 3) + 16 * g;  // this lane's bytes of a unit
+  // Rows past the tile's end read zeros.
+  uint32_t woff[2 * RG], xoff[kXL * NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const u32x4 b = ld16_if(ok && 16 * j + i < tokens, x, (uint32_t)((16 * j + i) * p.x_stride + kk));
-      acc[j] = mfma_i8(a, b, acc[j]);
+  for (int q = 0; q < 2 * RG; ++q) {
+    const int r = 8 * q + (li & 7);
+    woff[q] = r < rows ? (uint32_t)(r * p.w_stride + in_line) : kOOB;
+  }
+#pragma unroll
+  for (int q = 0; q < kXL * NT; ++q) {
+    const int r = 8 * q + (li & 7);
+    xoff[q] = r < tokens ? (uint32_t)(r * p.x_stride + in_line) : kOOB;
+  }
+  u32x4 wv[U][2 * RG], xv[U][kXL * NT];
+  auto fill = [&](int u, int k) {  // k past the row's end: zeros
+    const uint32_t past = k + in_line < p.K ? 0u : kOOB;
+#pragma unroll
+    for (int q = 0; q < kXL * NT; ++q)
+      xv[u][q] = __builtin_amdgcn_raw_buffer_load_b128(x, xoff[q] | past, k, kPolicyDefault);
+#pragma unroll
+    for (int q = 0; q < 2 * RG; ++q)
+      wv[u][q] = __builtin_amdgcn_raw_buffer_load_b128(w, woff[q] | past, k, kPolicyStream);
+  };
+  i32x4 acc[RG * NT] = {};
+  constexpr int kStep = 128 * WAVES;
+#pragma unroll
+  for (int u = 0; u < U; ++u) fill(u, 128 * wave + u * kStep);
+  auto use = [&](int u) {
+    u32x4 x0[NT], x1[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      line_pair_to_operands(xv[u][kXL * j], LOW ? u32x4{0, 0, 0, 0} : xv[u][kXL * j + kXL - 1], x0[j], x1[j]);
+#pragma unroll
+    for (int r = 0; r < RG; ++r) {
+      u32x4 w0, w1;
+      line_pair_to_operands(wv[u][2 * r], wv[u][2 * r + 1], w0, w1);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        acc[r * NT + j] = mfma_i8(w0, x0[j], acc[r * NT + j]);
+        acc[r * NT + j] = mfma_i8(w1, x1[j], acc[r * NT + j]);
+      }
+    }
+  };
+  int k = 128 * wave;
+  for (; k + U * kStep < p.K; k += U * kStep) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      use(u);
+      fill(u, k + (U + u) * kStep);
     }
   }
 #pragma unroll
-  for (int j = 0; j < NT; ++j) part[wave][j][lane] = acc[j];
+  for (int u = 0; u < U; ++u) use(u);
+#pragma unroll
+  for (int j = 0; j < RG * NT; ++j) part[wave][j][lane] = acc[j];
   __syncthreads();
-  for (int j = wave; j < NT; j += 4) {
+  for (int j = wave; j < RG * NT; j += WAVES) {
     i32x4 s = part[0][j][lane];
 #pragma unroll
-    for (int v = 1; v < 4; ++v) s += part[v][j][lane];
-    const int t = t0 + 16 * j + i, n = n0 + 4 * g;
+    for (int v = 1; v < WAVES; ++v) s += part[v][j][lane];
+    const int t = t0 + 16 * (j % NT) + li, n = n0 + 16 * (j / NT) + 4 * g;
     float ws[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) ws[e] = n + e < p.N ? p.w_scale[n + e] : 0.0f;
@@ -101,21 +154,31 @@ __global__ __launch_bounds__(256) void i8_rows_kernel(I8Params p) {
 // landed and every wave has read the previous step's buffer, which the next
 // loads then fill.
 //
-// S workgroups may split K: each stores its sums to the workspace and the last
-// to arrive adds the others' (integers: the order does not matter).
+// S workgroups may split K of a tile: each stores its sums to the workspace and
+// the last to arrive adds the others' (integers: the order does not matter).
+// Only the tiles past the last full round of workgroups are split, so that the
+// last round is as full as the others.
 template <int BT, int BN>
 struct Tile {
-  int tile, rank, t0, n0, tokens, rows, s0, s1;
+  int slot, S, rank, t0, n0, tokens, rows, s0, s1;  // slot: this tile's place in the workspace (S > 1)
   u32x4 w, x;  // buffer resources of the tile's rows
 
   __device__ __forceinline__ explicit Tile(const I8Params& p) {
     // Workgroups go to the 8 XCDs in turn; each XCD takes a run of tiles whose
     // operands its L2 then holds, four token tiles for each feature tile.
     const int ttiles = (p.T + BT - 1) / BT, ntiles = (p.N + BN - 1) / BN;
-    const int total = ttiles * ntiles * p.S, xcd = (int)blockIdx.x & 7;
-    const int idx = ((int)blockIdx.x >> 3) + xcd * (total >> 3) + min(xcd, total & 7);
-    rank = idx % p.S;
-    tile = idx / p.S;
+    int b = (int)blockIdx.x, total = p.whole, tile = 0;
+    S = 1;
+    if (b >= p.whole) {  // the tiles past the last full round of workgroups are split
+      b -= p.whole;
+      S = p.S;
+      total = (ttiles * ntiles - p.whole) * S;
+      tile = p.whole;
+    }
+    const int xcd = b & 7, idx = (b >> 3) + xcd * (total >> 3) + min(xcd, total & 7);
+    rank = idx % S;
+    slot = idx / S;
+    tile += slot;
     const int group = tile / (4 * ntiles), in_group = tile - group * 4 * ntiles;
     const int gt = min(4, ttiles - 4 * group);
     t0 = (4 * group + in_group % gt) * BT;
@@ -125,8 +188,8 @@ struct Tile {
     w = make_rsrc_words(p.w + (size_t)n0 * p.w_stride, (uint32_t)((rows - 1) * p.w_stride + p.K));
     x = make_rsrc_words(p.x + (size_t)t0 * p.x_stride, (uint32_t)((tokens - 1) * p.x_stride + p.K));
     const long steps = (p.K + 127) / 128;
-    s0 = (int)(steps * rank / p.S);
-    s1 = (int)(steps * (rank + 1) / p.S);
+    s0 = (int)(steps * rank / S);
+    s1 = (int)(steps * (rank + 1) / S);
   }
 };
 
@@ -167,9 +230,9 @@ struct Loader {
 // all afterwards). Sums are stored as they lie in the registers: 16 bytes a
 // lane, 1 KB a store.
 template <int kTile, int kSums>
-__device__ __forceinline__ bool join_ranks(const I8Params& p, int tile, int rank, i32x4* acc, int lane, int wave) {
+__device__ __forceinline__ bool join_ranks(const I8Params& p, int tile, int S, int rank, i32x4* acc, int lane, int wave) {
   __shared__ uint32_t arrived;
-  const rsrc_t part = make_rsrc(p.part + (size_t)tile * p.S * kTile, (uint32_t)p.S * kTile);
+  const rsrc_t part = make_rsrc(p.part + (size_t)tile * S * kTile, (uint32_t)S * kTile);
   const uint32_t at = (uint32_t)(wave * kSums * 1024 + lane * 16);
 #pragma unroll
   for (int k = 0; k < kSums; ++k)
@@ -180,13 +243,13 @@ __device__ __forceinline__ bool join_ranks(const I8Params& p, int tile, int rank
     uint32_t* const cnt = p.cnt + (size_t)tile * kOpsCounterStride;
     const uint32_t a = __hip_atomic_fetch_add(cnt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     // Everyone has arrived: the counter is ready for the next call.
-    if (a + 1 == (uint32_t)p.S) __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (a + 1 == (uint32_t)S) __hip_atomic_store(cnt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     arrived = a;
   }
   __syncthreads();
-  if (arrived + 1 != (uint32_t)p.S) return false;
+  if (arrived + 1 != (uint32_t)S) return false;
   handoff_order();
-  for (int r = 0; r < p.S; ++r) {
+  for (int r = 0; r < S; ++r) {
     if (r == rank) continue;
 #pragma unroll
     for (int k = 0; k < kSums; ++k)
@@ -255,7 +318,7 @@ __global__ __launch_bounds__(64 * WT * WN) void i8_tile_kernel(I8Params p) {
     }
     buf = buf + 1 == STG ? 0 : buf + 1;
   }
-  if (p.S > 1 && !join_ranks<BT * BN * 4, kNT * kMT>(p, t.tile, t.rank, acc, lane, wave)) return;
+  if (t.S > 1 && !join_ranks<BT * BN * 4, kNT * kMT>(p, t.slot, t.S, t.rank, acc, lane, wave)) return;
   store_blocks<kNT, kMT>(p, t.t0 + wt * (BT / WT), t.n0 + wn * (BN / WN), acc, lane);
 }
 
@@ -332,7 +395,7 @@ __global__ __launch_bounds__(512) void i8_big_kernel(I8Params p) {
     if (!second) close_loads(); else close();
   }
   if (!second) close();  // the waves behind have one phase to go
-  if (p.S > 1 && !join_ranks<256 * 256 * 4, kNT * kMT>(p, t.tile, t.rank, acc, lane, wave)) return;
+  if (t.S > 1 && !join_ranks<256 * 256 * 4, kNT * kMT>(p, t.slot, t.S, t.rank, acc, lane, wave)) return;
   store_blocks<kNT, kMT>(p, t.t0 + wt * 128, t.n0 + wn * 64, acc, lane);
 }
 
@@ -340,12 +403,24 @@ __global__ __launch_bounds__(512) void i8_big_kernel(I8Params p) {
 
 namespace {
 
+// The tile shapes and what a call with each costs, fitted to the times of 6279
+// calls (T = 9..4096, N = 549..18432, K = 1024..16384, every shape, K split 1
+// to 8 ways): a workgroup pays kStart and then `alone` a step while the CU
+// has room for it (`fit` at once), or `crowded` a step for each workgroup of
+// the CU where they queue; K split S ways adds kJoinRank S and the sums'
+// traffic. Over those sizes the choice is 2 % slower on average than the
+// fastest call found for each, 15 % at worst.
 struct TileShape {
-  int bt, bn;
+  int bt, bn, fit;
+  float alone, crowded;  // us a step of 128 bytes of K
 };
-constexpr TileShape kShapes[] = {{256, 256}, {256, 128}, {128, 128}, {128, 128}, {64, 128}, {64, 64}, {32, 128}, {32, 64}};
+constexpr TileShape kShapes[] = {
+    {256, 256, 1, 1.78f, 1.72f}, {128, 128, 2, 0.950f, 0.474f}, {128, 128, 1, 0.272f, 0.821f},
+    {64, 64, 2, 0.314f, 0.230f}, {32, 64, 3, 0.217f, 0.135f},
+};
+constexpr float kStart = 0.315f, kJoinRank = 0.152f;         // us
+constexpr float kWeights = 5.74e6f, kSums = 4.42e6f;         // bytes a us
 constexpr int kShapeCount = (int)(sizeof(kShapes) / sizeof(kShapes[0]));
-
 template <int BT, int BN, int WT, int WN, int STG>
 void launch_tile(const I8Params& p, int grid, hipStream_t s) {
   hipLaunchKernelGGL((i8_tile_kernel<BT, BN, WT, WN, STG>), dim3((unsigned)grid), dim3(64 * WT * WN), 0, s, p);
@@ -356,49 +431,82 @@ void launch_shape(int shape, const I8Params& p, int grid, hipStream_t s) {
     case 0:
       hipLaunchKernelGGL(i8_big_kernel, dim3((unsigned)grid), dim3(512), 0, s, p);
       return;
-    case 1: return launch_tile<256, 128, 2, 4, 3>(p, grid, s);
-    case 2: return launch_tile<128, 128, 2, 2, 2>(p, grid, s);
-    case 3: return launch_tile<128, 128, 2, 2, 4>(p, grid, s);
-    case 4: return launch_tile<64, 128, 1, 4, 4>(p, grid, s);
-    case 5: return launch_tile<64, 64, 1, 4, 4>(p, grid, s);
-    case 6: return launch_tile<32, 128, 1, 4, 4>(p, grid, s);
+    case 1: return launch_tile<128, 128, 2, 2, 2>(p, grid, s);
+    case 2: return launch_tile<128, 128, 2, 2, 4>(p, grid, s);
+    case 3: return launch_tile<64, 64, 1, 4, 4>(p, grid, s);
     default: return launch_tile<32, 64, 1, 4, 4>(p, grid, s);
   }
+}
+
+template <int NT, bool LOW, int RG, int WAVES, int U>
+void launch_rows(const I8Params& p, hipStream_t s) {
+  const int ntiles = (p.N + 16 * RG - 1) / (16 * RG), ttiles = (p.T + 16 * NT - 1) / (16 * NT);
+  hipLaunchKernelGGL((i8_rows_kernel<NT, LOW, RG, WAVES, U>), dim3((unsigned)(ntiles * ttiles)), dim3(64 * WAVES), 0, s, p);
+}
+
+// Units in flight: one load round of a wave where K is short (the workgroups of
+// a CU hide each other's latency), seven from K = 4096 on. Measured with U = 1 /
+// U = 7: T=1 N=4096 K=1024 3.4 / 4.7 us, T=1 N=16384 K=1024 5.5 / 11.5 us; T=8
+// N=4096 K=7168 8.9 / 7.9 us, T=8 N=K=16384 60.8 / 51.3 us.
+void launch_rows_for(const I8Params& p, hipStream_t s) {
+  if (p.K < 4096) {
+    if (p.T <= 8) return launch_rows<1, true, 1, 8, 1>(p, s);
+    return launch_rows<1, false, 1, 8, 1>(p, s);
+  }
+  if (p.T <= 8) return launch_rows<1, true, 1, 8, 7>(p, s);
+  return launch_rows<1, false, 1, 8, 7>(p, s);
 }
 
 }  // namespace
 
 I8Tactic pick_i8(int T, int N, int K) {
-  I8Tactic t;
-  t.shape = knob(kKnobI8Shape, T <= 64 ? -1 : T >= 1024 ? 0 : 2);
-  t.S = knob(kKnobI8Split, 1);
-  if (t.shape < 0 || t.shape >= kShapeCount) {
-    t.shape = -1;
-    t.S = 1;
-    return t;
+  I8Tactic best;
+  const int pinned = knob(kKnobI8Shape, -1), split = knob(kKnobI8Split, 0);
+  // Few tokens, or little work: straight into registers (shape -1).
+  const long work = (long)N * K;
+  const bool rows = T <= 8 || (T <= 16 && work <= 8L << 20) || (T <= 32 && work <= 2L << 20);
+  if (pinned >= kShapeCount || (pinned < 0 && rows)) return best;
+  const int steps = std::max(1, (K + 127) / 128);
+  float least = 0.0f;
+  for (int i = 0; i < kShapeCount; ++i) {
+    if (pinned >= 0 && i != pinned) continue;
+    const TileShape& sh = kShapes[i];
+    const long tiles = ((long)T + sh.bt - 1) / sh.bt * ((N + sh.bn - 1) / sh.bn);
+    const size_t bytes = (size_t)sh.bt * sh.bn * 4;
+    for (int S = 1; S <= 8; ++S) {
+      if (split > 0 && S != std::min(split, steps)) continue;
+      if (S > steps) break;
+      // Only the tiles past the last full round of workgroups are split.
+      const long round = 256L * sh.fit, whole = S > 1 ? tiles / round * round : 0, rest = tiles - whole;
+      if (S > 1 && (rest == 0 || (size_t)(rest * S) * bytes > kOpsPartBytes || rest > kOpsCounters)) continue;
+      const long m = (rest * S + 255) / 256, each = (steps + S - 1) / S;
+      float us = std::max((float)((m + sh.fit - 1) / sh.fit) * (kStart + (float)each * sh.alone),
+                          (float)m * (kStart + (float)each * sh.crowded));
+      us += (float)(whole / 256) * (kStart + (float)steps * sh.crowded);
+      us = std::max(us, ((float)N + (float)T) * (float)K / kWeights);
+      if (S > 1) us += kJoinRank * (float)S + 8.0f * (float)(S * rest) * (float)(sh.bt * sh.bn) / kSums;
+      if (best.shape < 0 || us < least) {
+        least = us;
+        best.shape = i;
+        best.S = S;
+        best.whole = (int)whole;
+        best.tiles = (int)tiles;
+      }
+    }
   }
-  const TileShape& sh = kShapes[t.shape];
-  t.tiles = (int)(((long)T + sh.bt - 1) / sh.bt * ((N + sh.bn - 1) / sh.bn));
-  const int steps = (K + 127) / 128;
-  if (t.S > steps) t.S = steps > 0 ? steps : 1;
-  t.part_bytes = t.S > 1 ? (size_t)t.tiles * t.S * sh.bt * sh.bn * 4 : 0;
-  if (t.part_bytes > kOpsPartBytes || t.tiles > kOpsCounters) t.S = 1, t.part_bytes = 0;
-  return t;
+  return best;
 }
 
 hipError_t launch_i8(const I8Params& q, const I8Tactic& tac, hipStream_t s) {
   I8Params p = q;
   p.S = tac.S;
+  p.whole = tac.whole;
   const int per = p.out_f32 ? 16 : 8;  // bytes of four outputs
   p.c_quads = p.c_stride % per == 0;
   if (tac.shape < 0) {
-    const unsigned tiles = (unsigned)((p.N + 15) / 16);
-    if (p.T <= 16)
-      hipLaunchKernelGGL(i8_rows_kernel<1>, dim3(tiles, (unsigned)((p.T + 15) / 16)), dim3(256), 0, s, p);
-    else
-      hipLaunchKernelGGL(i8_rows_kernel<4>, dim3(tiles, (unsigned)((p.T + 63) / 64)), dim3(256), 0, s, p);
+    launch_rows_for(p, s);
   } else {
-    launch_shape(tac.shape, p, tac.tiles * tac.S, s);
+    launch_shape(tac.shape, p, tac.whole + (tac.tiles - tac.whole) * tac.S, s);
   }
   return hipGetLastError();
 }

@@ -30,21 +30,20 @@ struct I8Params {
   int T, N, K;
   int out_f32;
   int c_quads;    // four outputs of a row are aligned for one store
-  int S;          // workgroups that split K
-  uint8_t* part;  // sums [tiles, S, tile] (S > 1)
+  int S, whole;   // workgroups that split K of each tile past the first `whole`
+  uint8_t* part;  // their sums [tiles - whole, S, tile] (S > 1)
   uint32_t* cnt;  // one arrival counter a tile, kOpsCounterStride words apart
 };
 
 // The workspace: partial results, then arrival counters, a 128-byte line each.
-constexpr size_t kOpsPartBytes = (size_t)32 << 20;
+constexpr size_t kOpsPartBytes = (size_t)64 << 20;
 constexpr int kOpsCounterStride = 32;
 constexpr int kOpsCounters = 8192;
 
-// How a call is run: tile shape (-1: operands straight into registers), K
-// split and what it needs of the workspace.
+// How a call is run: tile shape (-1: operands straight into registers), and K
+// split S ways in the tiles past the first `whole`.
 struct I8Tactic {
-  int shape = -1, S = 1, tiles = 0;
-  size_t part_bytes = 0;
+  int shape = -1, S = 1, whole = 0, tiles = 0;
 };
 I8Tactic pick_i8(int T, int N, int K);
 

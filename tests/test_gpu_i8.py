@@ -79,6 +79,40 @@ def test_i8_strides(T, N, K):
         check(run(w, ws, x, xs, kind, pad=pad, wpad=48, xpad=16), want, kind)
 
 
+# Every tile shape, and the kernel without tiles (5), pinned: sizes below, at and
+# past a tile, K that ends inside a step, and K split over workgroups, among them
+# calls of more tiles than one round of workgroups, of which only the last are
+# split.
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", range(6))
+@pytest.mark.parametrize("T,N,K", [(1, 1, 16), (33, 65, 144), (256, 256, 128), (257, 300, 1040), (700, 129, 4112)])
+def test_i8_shapes(T, N, K, shape, tune):
+    w, x, ws, xs = codes(N, K, 1), codes(T, K, 2), scales(N, 3), scales(T, 4)
+    _, want = O.i8_ref(x, xs, w, ws)
+    tune("i8_shape", shape)
+    got = {}
+    for S in (1, 2, 3, 5, 8):
+        tune("i8_split", S)
+        log(f"i8 shape {shape} split {S} T={T} N={N} K={K}")
+        got[S] = run(w, ws, x, xs, "f32")
+        check(got[S], want, "f32")
+        assert np.array_equal(got[S], got[1]), "a split changes bits"
+    check(run(w, ws, x, xs, "bf16"), want, "bf16")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape,T,N,K", [(0, 4000, 4300, 400), (1, 3000, 3100, 272), (2, 2000, 2200, 400), (3, 1500, 1600, 400),
+                                         (4, 1000, 1700, 400)])
+def test_i8_last_round_split(shape, T, N, K, tune):
+    w, x, ws, xs = codes(N, K, 1), codes(T, K, 2), scales(N, 3), scales(T, 4)
+    _, want = O.i8_ref(x, xs, w, ws)
+    tune("i8_shape", shape)
+    for S in (1, 2, 4):
+        tune("i8_split", S)
+        log(f"i8 last round shape {shape} split {S}")
+        check(run(w, ws, x, xs, "f32"), want, "f32")
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("T", [1, 40, 300])
 def test_i8_extremes(T):
