@@ -125,44 +125,64 @@ __device__ __forceinline__ int key_index(u64 k) { return (int)~(uint32_t)k; }
 constexpr int kCand = 1024;  // candidates held in LDS
 
 struct TopLds {
-  uint32_t best[kThreads];
+  u64 best[kThreads];
   int owners[kThreads];
   u64 cand[kCand];
   int n_own, n_cand, count;
 };
 
 // Sorted best k of the keys that `src` holds, to out(rank, key), ranks 0 ..
-// k-1 (fewer if fewer keys). Thread t owns src's items t, t + 256, ...; `best`
-// is order_bits of its best key (0: none), known from the pass over the data.
+// k-1 (fewer if fewer keys). Thread t owns src's items t, t + 256, ...; of its
+// best key it knows bounds low <= key <= high with the same value (0: no key):
+// the pass over the data notes the vector that holds it, not the element.
 //
-// If the k-th largest of the owners' bests is b, every key of the best k lies
-// with an owner whose best is at least b, and is at least b itself: k keys
-// (the bests) reach it. So only those owners' items are read again: about k of
-// 256, a fraction k / 256 of the data, whatever the values are. Ties at b can
-// make the candidates many; past kCand the exact k-th key is searched bit by
-// bit over the owners' items (rows of mostly equal logits).
+// If the k-th largest of the owners' `low` is b, then k keys reach it, so every
+// key of the best k is at least b and lies with an owner whose `high` is. Only
+// those owners' items are read again: about k of 256, a fraction k / 256 of the
+// data, whatever the values are, equal ones included. Should one owner hold
+// more than kCand keys past b, the exact k-th key is searched bit by bit over
+// the owners' items.
 template <class Src, class Out>
-__device__ __forceinline__ void block_top(const Src& src, uint32_t best, int k, TopLds& l, Out out) {
+__device__ __forceinline__ void block_top(const Src& src, u64 low, u64 high, int k, TopLds& l, Out out) {
   const int tid = (int)threadIdx.x, lane = tid & 63;
-  l.best[tid] = best;
+  l.best[tid] = low;
   if (tid == 0) l.n_own = l.n_cand = 0;
   __syncthreads();
-  // Each wave finds b by itself: four bests a lane, one bit a step.
-  uint32_t b4[4], thr = 0;
+  // Each wave finds b by itself, four bests a lane, one bit a step: first the
+  // value, then, where more than k owners share it, the index.
+  uint32_t v4[4], i4[4], value = 0, index = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) b4[i] = l.best[lane + 64 * i];
+  for (int i = 0; i < 4; ++i) {
+    const u64 b = l.best[lane + 64 * i];
+    v4[i] = (uint32_t)(b >> 32);
+    i4[i] = (uint32_t)b;
+  }
+  int reach = kThreads;
   for (uint32_t bit = 0x80000000u; bit != 0; bit >>= 1) {
-    const uint32_t c = thr | bit;
+    const uint32_t c = value | bit;
     int n = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) n += __popcll(__ballot(b4[i] >= c));
-    if (n >= k) thr = c;
+    for (int i = 0; i < 4; ++i) n += __popcll(__ballot(v4[i] >= c));
+    if (n >= k) {
+      value = c;
+      reach = n;
+    }
   }
-  if (best >= thr && best != 0) l.owners[atomicAdd(&l.n_own, 1)] = tid;
+  if (reach > k && value != 0) {
+    index = ~(uint32_t)(SKGEMM_MAX_V - 1);  // an index is below SKGEMM_MAX_V
+    for (uint32_t bit = SKGEMM_MAX_V >> 1; bit != 0; bit >>= 1) {
+      const uint32_t c = index | bit;
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) n += __popcll(__ballot(v4[i] > value || (v4[i] == value && i4[i] >= c)));
+      if (n >= k) index = c;
+    }
+  }
+  u64 lowest = ((u64)value << 32) | index;
+  if (high >= lowest && high != 0) l.owners[atomicAdd(&l.n_own, 1)] = tid;
   __syncthreads();
   const int n_own = l.n_own, per = src.per_owner();
   const long items = (long)n_own * per;
-  u64 lowest = (u64)thr << 32;
   auto gather = [&]() {
     for (long it = tid; it < items; it += kThreads) {
       u64 key[Src::kE];
@@ -267,7 +287,8 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobParams p) {
   const float mul = p.scale * kLog2e;
   const int first = run * p.per, n = max(0, min(p.per, row.nvec - first));
   Sums a = {-kInf, 0.0f, 0.0f};
-  auto add = [&](const float* x) {
+  int at = first + tid;  // the first vector that holds this thread's largest logit
+  auto add = [&](int j, const float* x) {
     float m = a.m;
 #pragma unroll
     for (int e = 0; e < kE; ++e) m = fmaxf(m, x[e]);
@@ -276,6 +297,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobParams p) {
       a.u = f * (a.u + fmaxf(d, -1e30f) * a.s);
       a.s *= f;
       a.m = m;
+      at = j;
     }
     const float ref = m == -kInf ? 0.0f : m;  // nothing but banned tokens so far: d = -inf
 #pragma unroll
@@ -287,11 +309,16 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobParams p) {
   };
   {
     // Thread tid takes vectors first + tid, + 256, ...: whole ones four loads at
-    // a time, then the row's partial ends where they are this thread's.
-    const int w0 = row.whole(0) ? 0 : 1, w1 = row.whole(row.nvec - 1) ? row.nvec : row.nvec - 1;
-    const int end = min(first + n, w1);
+    // a time, the row's partial ends where they are this thread's.
+    const int last = row.nvec - 1;
+    const int end = min(first + n, row.whole(last) ? row.nvec : last);
     int j = first + tid;
-    if (j < w0) j += kThreads;
+    if (j == 0 && n > 0 && !row.whole(0)) {
+      float x[kE];
+      row.load(0, x, -kInf);
+      add(0, x);
+      j += kThreads;
+    }
     for (; j + 3 * kThreads < end; j += 4 * kThreads) {
       u32x4 v[4];
 #pragma unroll
@@ -300,22 +327,18 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobParams p) {
       for (int q = 0; q < 4; ++q) {
         float x[kE];
         Row<F32>::unpack(v[q], x);
-        add(x);
+        add(j + q * kThreads, x);
       }
     }
     for (; j < end; j += kThreads) {
       float x[kE];
       Row<F32>::unpack(row.load_whole(j), x);
-      add(x);
+      add(j, x);
     }
-    const int last = row.nvec - 1;
-    for (int q = 0; q < 2; ++q) {
-      const int edge = q == 0 ? 0 : last;
-      if (row.whole(edge) || (q == 1 && last == 0)) continue;
-      if (edge < first || edge >= first + n || (edge - first) % kThreads != tid) continue;
+    if (last > 0 && end == last && j == last && last < first + n) {
       float x[kE];
-      row.load(edge, x, -kInf);
-      add(x);
+      row.load(last, x, -kInf);
+      add(last, x);
     }
   }
   const float most = a.m;  // of this thread's logits
@@ -327,7 +350,9 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobParams p) {
   a = part[0];
   for (int i = 1; i < kThreads / 64; ++i) a = join(a, part[i], mul);
   const RowItems<F32> items{row, first, n};
-  const uint32_t best = any ? order_bits(most) : 0u;
+  // The best key's index is one of vector `at`: bounds from its last and first.
+  const u64 low = any ? make_key(most, min(p.V - 1, row.index(at) + kE - 1)) : 0u;
+  const u64 high = any ? make_key(most, max(0, row.index(at))) : 0u;
 
   if (p.parts > 1) {
     uint8_t* const work = p.part + t * (size_t)p.parts * kLogprobPart;
@@ -339,7 +364,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobParams p) {
     }
     if (p.k > 0) {
       u64* const keys = reinterpret_cast<u64*>(mine + 16);
-      block_top(items, best, p.k, top, [&](int rank, u64 key) {
+      block_top(items, low, high, p.k, top, [&](int rank, u64 key) {
         __hip_atomic_store(keys + rank, key, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       });
       // A run of fewer than k elements leaves the rest empty.
@@ -404,15 +429,15 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobParams p) {
     ti[rank] = key_index(key);
   };
   if (p.parts == 1) {
-    block_top(items, best, p.k, top, out);
+    block_top(items, low, high, p.k, top, out);
   } else {
     const KeyItems kept{p.part + t * (size_t)p.parts * kLogprobPart, p.k, p.parts * p.k};
-    u64 high = 0;
+    u64 best = 0;
     for (int i = tid; i < kept.n; i += kThreads) {
       const u64 key = kept.at(i);
-      high = key > high ? key : high;
+      best = key > best ? key : best;
     }
-    block_top(kept, (uint32_t)(high >> 32), p.k, top, out);
+    block_top(kept, best, best, p.k, top, out);
   }
 }
 

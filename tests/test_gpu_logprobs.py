@@ -164,6 +164,30 @@ def test_logprobs_candidates_overflow():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [2, 1200])
+def test_logprobs_few_owners(T):
+    """Fewer threads than alternatives hold all the large logits, thousands of
+    them, distinct or equal: the candidates pass their buffer."""
+    V, k = 200001, 64
+    for kind, per in (("bf16", 8), ("f32", 4)):
+        rng = np.random.default_rng(2)
+        z = np.full((T, V), -1.0, np.float32)
+        hot = (np.arange(V) // per) % 256 < 3
+        z[0, hot] = 5 + rng.integers(0, 200, hot.sum()) / 8
+        z[1, hot] = 5.0
+        z[2:] = 3.0
+        log(f"logprobs few owners {kind} T={T}")
+        Z = dev_logits(z[:6], kind)
+        if T > 6:  # the rows past the sixth equal it
+            Z = torch().cat([Z, Z[5:].expand(T - 6, V)]).contiguous()
+        tok = np.zeros(T, np.int64)
+        got = forward(Z, tok, k, 1.0)
+        for name, a in got.items():
+            assert np.array_equal(a[6:], np.broadcast_to(a[5:6], a[6:].shape)) if T > 6 else True, name
+        check_forward(Z[:6], tok[:6], k, 1.0, got={n: a[:6] for n, a in got.items()})
+
+
+@pytest.mark.gpu
 def test_logprobs_optional_outputs():
     z, tok = make(4, 500, seed=1)
     Z = dev_logits(z, "f32")
