@@ -28,6 +28,26 @@ __device__ __forceinline__ float butterfly_max(float v) {
   return v;
 }
 
+// The largest of a wave's 64 unsigned values, in every lane.
+template <int OFF>
+__device__ __forceinline__ uint32_t xred_umax(uint32_t v) {
+  if constexpr (OFF >= 16) {
+    auto p = (OFF == 32) ? __builtin_amdgcn_permlane32_swap((int)v, (int)v, false, false)
+                         : __builtin_amdgcn_permlane16_swap((int)v, (int)v, false, false);
+    return max((uint32_t)p[0], (uint32_t)p[1]);
+  } else {
+    return max(v, (uint32_t)xshfl_dpp<OFF>((int)v));
+  }
+}
+__device__ __forceinline__ uint32_t butterfly_umax(uint32_t v) {
+  v = xred_umax<32>(v);
+  v = xred_umax<16>(v);
+  v = xred_umax<8>(v);
+  v = xred_umax<4>(v);
+  v = xred_umax<2>(v);
+  return xred_umax<1>(v);
+}
+
 // The sum of `a` and the largest `b` over a workgroup of up to 16 waves, in
 // every thread. `part` holds 32 floats of LDS that nobody else uses until the
 // next barrier after this call.

@@ -127,73 +127,140 @@ constexpr int kCand = 1024;  // candidates held in LDS
 struct TopLds {
   u64 best[kThreads];
   int owners[kThreads];
-  u64 cand[kCand];
+  u64 cand[kCand + 8];
+  u64 lowest;
   int n_own, n_cand, count;
 };
 
+// How a workgroup's vectors fall to 256 owners: owner o = (segment o / (256 / G),
+// group o % (256 / G)) holds the vectors that the G = 1 << lg threads of the
+// group take in `len` consecutive rounds of 256. G neighbouring vectors a round:
+// with G = 8, whole 128-byte lines, so that reading an owner's vectors again
+// moves no more than they hold.
+struct Owners {
+  int lg, len;
+  __device__ __forceinline__ explicit Owners(int rounds) {
+    lg = rounds >= 8 ? 3 : rounds >= 4 ? 2 : rounds >= 2 ? 1 : 0;
+    len = (rounds + (1 << lg) - 1) >> lg;
+  }
+  __device__ __forceinline__ int items() const { return len << lg; }
+  __device__ __forceinline__ int item(int o, int x) const {
+    const int group = o & ((kThreads >> lg) - 1), seg = o >> (8 - lg);
+    return (seg * len + (x >> lg)) * kThreads + (group << lg) + (x & ((1 << lg) - 1));
+  }
+};
+static_assert(kThreads == 256, "owner numbers are 8 bits");
+
 // Sorted best k of the keys that `src` holds, to out(rank, key), ranks 0 ..
-// k-1 (fewer if fewer keys). Thread t owns src's items t, t + 256, ...; of its
-// best key it knows bounds low <= key <= high with the same value (0: no key):
-// the pass over the data notes the vector that holds it, not the element.
+// k-1 (fewer if fewer keys). l.best holds, for each owner of src's items, a
+// bound below its best key of the same value, at most kE - 1 below it (the pass
+// over the data notes the vector that holds the largest logit, not the
+// element); 0: no key.
 //
-// If the k-th largest of the owners' `low` is b, then k keys reach it, so every
-// key of the best k is at least b and lies with an owner whose `high` is. Only
-// those owners' items are read again: about k of 256, a fraction k / 256 of the
-// data, whatever the values are, equal ones included. Should one owner hold
+// If k of these bounds reach some b, then k keys reach it, so every key
+// of the best k is at least b and lies with an owner whose bound + kE - 1 is.
+// Only those owners' items are read again: about k of 256, a fraction k / 256
+// of the data, whatever the values are, equal ones included. Should they hold
 // more than kCand keys past b, the exact k-th key is searched bit by bit over
 // the owners' items.
 template <class Src, class Out>
-__device__ __forceinline__ void block_top(const Src& src, u64 low, u64 high, int k, TopLds& l, Out out) {
+__device__ __forceinline__ void block_top(const Src& src, const Owners& who, int k, TopLds& l, Out out) {
   const int tid = (int)threadIdx.x, lane = tid & 63;
-  l.best[tid] = low;
   if (tid == 0) l.n_own = l.n_cand = 0;
   __syncthreads();
-  // Each wave finds b by itself, four bests a lane, one bit a step: first the
-  // value, then, where more than k owners share it, the index.
-  uint32_t v4[4], i4[4], value = 0, index = 0;
+  // One wave finds b, four bounds a lane, one bit a step: first the value, then,
+  // where many owners share it, the index. The common leading bits of all values
+  // are skipped, and any b that k .. k + slack owners reach will do: half a dozen
+  // steps as a rule. (All waves at it, exact: 53 steps, which cost T=256 V=50001
+  // 20 us more.)
+  if (tid < 64) {
+    uint32_t v4[4], i4[4], most = 0, least = ~0u;
+    int valid = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const u64 b = l.best[lane + 64 * i];
-    v4[i] = (uint32_t)(b >> 32);
-    i4[i] = (uint32_t)b;
-  }
-  int reach = kThreads;
-  for (uint32_t bit = 0x80000000u; bit != 0; bit >>= 1) {
-    const uint32_t c = value | bit;
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) n += __popcll(__ballot(v4[i] >= c));
-    if (n >= k) {
-      value = c;
-      reach = n;
+    for (int i = 0; i < 4; ++i) {
+      const u64 b = l.best[lane + 64 * i];
+      v4[i] = (uint32_t)(b >> 32);
+      i4[i] = (uint32_t)b;
+      most = max(most, v4[i]);
+      least = min(least, v4[i] != 0 ? v4[i] : ~0u);
+      valid += __popcll(__ballot(v4[i] != 0));
     }
-  }
-  if (reach > k && value != 0) {
-    index = ~(uint32_t)(SKGEMM_MAX_V - 1);  // an index is below SKGEMM_MAX_V
-    for (uint32_t bit = SKGEMM_MAX_V >> 1; bit != 0; bit >>= 1) {
-      const uint32_t c = index | bit;
-      int n = 0;
+    most = butterfly_umax(most);
+    least = ~butterfly_umax(~least);
+    uint32_t value = 0, index = 0;
+    if (valid >= k) {
+      const int slack = k / 2 + 8;
+      most = (uint32_t)__builtin_amdgcn_readfirstlane((int)most);
+      const uint32_t differ = most ^ (uint32_t)__builtin_amdgcn_readfirstlane((int)least);
+      uint32_t bit = differ != 0 ? 0x80000000u >> __builtin_clz(differ) : 0u;
+      value = bit != 0 ? most & ~(2u * bit - 1u) : most;
+      int reach = valid;
+      for (; bit != 0 && reach > k + slack; bit >>= 1) {
+        const uint32_t c = value | bit;
+        int n = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) n += __popcll(__ballot(v4[i] > value || (v4[i] == value && i4[i] >= c)));
-      if (n >= k) index = c;
-    }
-  }
-  u64 lowest = ((u64)value << 32) | index;
-  if (high >= lowest && high != 0) l.owners[atomicAdd(&l.n_own, 1)] = tid;
-  __syncthreads();
-  const int n_own = l.n_own, per = src.per_owner();
-  const long items = (long)n_own * per;
-  auto gather = [&]() {
-    for (long it = tid; it < items; it += kThreads) {
-      u64 key[Src::kE];
-      src.keys(l.owners[it / per] + (int)(it % per) * kThreads, key);
-#pragma unroll
-      for (int e = 0; e < Src::kE; ++e)
-        if (key[e] != 0 && key[e] >= lowest) {
-          const int at = atomicAdd(&l.n_cand, 1);
-          if (at < kCand) l.cand[at] = key[e];
+        for (int i = 0; i < 4; ++i) n += __popcll(__ballot(v4[i] >= c));
+        if (n >= k) {
+          value = c;
+          reach = n;
         }
+      }
+      if (reach > k + slack) {
+        index = ~(uint32_t)(2 * SKGEMM_MAX_V - 1);  // an index is below SKGEMM_MAX_V + kE
+        for (uint32_t low = SKGEMM_MAX_V; low != 0 && reach > k + slack; low >>= 1) {
+          const uint32_t c = index | low;
+          int n = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) n += __popcll(__ballot(v4[i] > value || (v4[i] == value && i4[i] >= c)));
+          if (n >= k) {
+            index = c;
+            reach = n;
+          }
+        }
+      }
     }
+    if (lane == 0) l.lowest = ((u64)value << 32) | index;
+  }
+  __syncthreads();
+  u64 lowest = l.lowest;
+  const u64 bound = l.best[tid];
+  if (bound != 0 && bound + (Src::kE - 1) >= lowest) l.owners[atomicAdd(&l.n_own, 1)] = tid;
+  __syncthreads();
+  // The owners' items over all threads, four loads of a thread in flight: a
+  // wave's round takes 64 >> shift owners, 1 << shift items of each.
+  const int n_own = l.n_own, per = who.items(), wave = tid >> 6;
+  int shift = 0;
+  while (shift < 6 && (1 << shift) < per) ++shift;
+  const int width = 64 >> shift, groups = (n_own + width - 1) / width, chunks = (per + (1 << shift) - 1) >> shift;
+  const int rounds = groups * chunks;
+  auto each_key = [&](u64 at_least, auto f) {  // f of each key; those below at_least may be left out
+    for (int r0 = wave; r0 < rounds; r0 += 4 * (kThreads / 64)) {
+      int item[4];
+      typename Src::Raw raw[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int r = r0 + q * (kThreads / 64), group = r / chunks, chunk = r - group * chunks;
+        const int own = group * width + (lane >> shift), j = (chunk << shift) + (lane & ((1 << shift) - 1));
+        item[q] = (r < rounds && own < n_own && j < per) ? who.item(l.owners[own], j) : -1;
+        raw[q] = src.load(item[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (!src.reaches(item[q], raw[q], (uint32_t)(at_least >> 32))) continue;
+        u64 key[Src::kE];
+        src.keys(item[q], raw[q], key);
+#pragma unroll
+        for (int e = 0; e < Src::kE; ++e) f(key[e]);
+      }
+    }
+  };
+  auto gather = [&]() {
+    each_key(lowest, [&](u64 key) {
+      if (key != 0 && key >= lowest) {
+        const int at = atomicAdd(&l.n_cand, 1);
+        if (at < kCand) l.cand[at] = key;
+      }
+    });
     __syncthreads();
   };
   gather();
@@ -205,12 +272,7 @@ __device__ __forceinline__ void block_top(const Src& src, u64 low, u64 high, int
       if (tid == 0) l.count = 0;
       __syncthreads();
       int n = 0;
-      for (long it = tid; it < items; it += kThreads) {
-        u64 key[Src::kE];
-        src.keys(l.owners[it / per] + (int)(it % per) * kThreads, key);
-#pragma unroll
-        for (int e = 0; e < Src::kE; ++e) n += key[e] >= c;
-      }
+      each_key(c, [&](u64 key) { n += key >= c; });
       atomicAdd(&l.count, n);
       __syncthreads();
       if (l.count >= k) kth = c;
@@ -222,10 +284,15 @@ __device__ __forceinline__ void block_top(const Src& src, u64 low, u64 high, int
     gather();
   }
   const int n = l.n_cand;
+  if (tid < 8) l.cand[n + tid] = 0;  // the ranks below are counted eight keys at a time
+  __syncthreads();
   for (int i = tid; i < n; i += kThreads) {
     const u64 key = l.cand[i];
     int rank = 0;
-    for (int j = 0; j < n; ++j) rank += l.cand[j] > key;
+    for (int j = 0; j < n; j += 8) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) rank += l.cand[j + q] > key;
+    }
     if (rank < k) out(rank, key);
   }
 }
@@ -236,17 +303,40 @@ struct RowItems {
   static constexpr int kE = Row<F32>::kE;
   const Row<F32>& row;
   int first, n;
-  __device__ __forceinline__ int per_owner() const { return (n + kThreads - 1) / kThreads; }
-  __device__ __forceinline__ void keys(int item, u64* key) const {
+  typedef u32x4 Raw;
+  // Item `item` (none: negative, or past the run). A partial vector is read
+  // element by element in keys().
+  __device__ __forceinline__ Raw load(int item) const {
+    if (item < 0 || item >= n || !row.whole(first + item)) return u32x4{0, 0, 0, 0};
+    return row.load_whole(first + item);
+  }
+  // Whether a key of this item can have a value of at least `order`: for whole
+  // vectors one comparison of the largest.
+  __device__ __forceinline__ bool reaches(int item, Raw raw, uint32_t order) const {
+    if (item < 0 || item >= n) return false;
+    if (!row.whole(first + item)) return true;
+    float x[kE], m;
+    Row<F32>::unpack(raw, x);
+    m = x[0];
+#pragma unroll
+    for (int e = 1; e < kE; ++e) m = fmaxf(m, x[e]);
+    return order_bits(m) >= order;
+  }
+  __device__ __forceinline__ void keys(int item, Raw raw, u64* key) const {
 #pragma unroll
     for (int e = 0; e < kE; ++e) key[e] = 0;
-    if (item >= n) return;
+    if (item < 0 || item >= n) return;
+    const int i0 = row.index(first + item);
     float x[kE];
-    row.load(first + item, x, 0.0f);
+    if (row.whole(first + item)) {
+      Row<F32>::unpack(raw, x);
 #pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      const int i = row.index(first + item) + e;
-      if (i >= 0 && i < row.V) key[e] = make_key(x[e], i);
+      for (int e = 0; e < kE; ++e) key[e] = make_key(x[e], i0 + e);
+    } else {
+      row.load(first + item, x, 0.0f);
+#pragma unroll
+      for (int e = 0; e < kE; ++e)
+        if (i0 + e >= 0 && i0 + e < row.V) key[e] = make_key(x[e], i0 + e);
     }
   }
 };
@@ -254,14 +344,15 @@ struct RowItems {
 // Keys in the workspace, kept by the workgroups of a row, as block_top's items.
 struct KeyItems {
   static constexpr int kE = 1;
-  const uint8_t* work;
-  int k, n;  // keys a part, keys in all
-  __device__ __forceinline__ int per_owner() const { return (n + kThreads - 1) / kThreads; }
-  __device__ __forceinline__ u64 at(int item) const {
-    const u64* p = reinterpret_cast<const u64*>(work + (size_t)(item / k) * kLogprobPart + 16) + item % k;
-    return __hip_atomic_load(const_cast<u64*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  typedef u64 Raw;
+  u64* keys_;
+  int n;
+  __device__ __forceinline__ Raw load(int item) const {
+    if (item < 0 || item >= n) return 0;
+    return __hip_atomic_load(keys_ + item, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
-  __device__ __forceinline__ void keys(int item, u64* key) const { key[0] = item < n ? at(item) : 0; }
+  __device__ __forceinline__ bool reaches(int, Raw raw, uint32_t order) const { return (uint32_t)(raw >> 32) >= order; }
+  __device__ __forceinline__ void keys(int, Raw raw, u64* key) const { key[0] = raw; }
 };
 
 __device__ __forceinline__ void store_agent(float* p, float v) {
@@ -274,7 +365,7 @@ __device__ __forceinline__ float load_agent(float* p) {
 // A row, or where there are few rows one of p.parts runs of its vectors: the
 // workgroup that finishes a row's last run joins the sums and the best k that
 // the others left in the workspace.
-template <bool F32>
+template <bool F32, bool TOP>
 __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobParams p) {
   __shared__ TopLds top;
   __shared__ Sums part[kThreads / 64];
@@ -287,19 +378,25 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobParams p) {
   const float mul = p.scale * kLog2e;
   const int first = run * p.per, n = max(0, min(p.per, row.nvec - first));
   Sums a = {-kInf, 0.0f, 0.0f};
-  int at = first + tid;  // the first vector that holds this thread's largest logit
+  const int rounds = (n + kThreads - 1) / kThreads;
+  const Owners who(TOP ? rounds : 1);
+  float seg_m = -kInf;  // TOP: this segment's largest logit, and the first vector that holds it
+  int at = -1;
   auto add = [&](int j, const float* x) {
-    float m = a.m;
+    float m = x[0];
 #pragma unroll
-    for (int e = 0; e < kE; ++e) m = fmaxf(m, x[e]);
+    for (int e = 1; e < kE; ++e) m = fmaxf(m, x[e]);
+    if constexpr (TOP) {
+      at = m > seg_m ? j : at;
+      seg_m = fmaxf(seg_m, m);
+    }
     if (m > a.m) {
       const float d = (a.m - m) * mul, f = exp2_hw(d);
       a.u = f * (a.u + fmaxf(d, -1e30f) * a.s);
       a.s *= f;
       a.m = m;
-      at = j;
     }
-    const float ref = m == -kInf ? 0.0f : m;  // nothing but banned tokens so far: d = -inf
+    const float ref = a.m == -kInf ? 0.0f : a.m;  // nothing but banned tokens so far: d = -inf
 #pragma unroll
     for (int e = 0; e < kE; ++e) {
       const float d = (x[e] - ref) * mul, w = exp2_hw(d);
@@ -308,41 +405,68 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobParams p) {
     }
   };
   {
-    // Thread tid takes vectors first + tid, + 256, ...: whole ones four loads at
-    // a time, the row's partial ends where they are this thread's.
+    // Thread tid takes vector first + 256 i + tid in round i: whole ones four
+    // loads at a time, the row's partial ends by themselves where they are this
+    // thread's, in their segment and in order.
     const int last = row.nvec - 1;
-    const int end = min(first + n, row.whole(last) ? row.nvec : last);
-    int j = first + tid;
-    if (j == 0 && n > 0 && !row.whole(0)) {
-      float x[kE];
-      row.load(0, x, -kInf);
-      add(0, x);
-      j += kThreads;
-    }
-    for (; j + 3 * kThreads < end; j += 4 * kThreads) {
-      u32x4 v[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] = row.load_whole(j + q * kThreads);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
+    const int w0 = row.whole(0) ? 0 : 1, w1 = min(first + n, row.whole(last) ? row.nvec : last);
+    const bool tail = last > 0 && !row.whole(last) && last < first + n;
+    int i = 0;
+    for (int seg = 0; seg < (1 << who.lg); ++seg) {
+      const int i1 = TOP ? min(rounds, (seg + 1) * who.len) : rounds;
+      const int j1 = first + i1 * kThreads;  // past this segment
+      int j = first + i * kThreads + tid;
+      if (j == 0 && n > 0 && w0 == 1) {
         float x[kE];
-        Row<F32>::unpack(v[q], x);
-        add(j + q * kThreads, x);
+        row.load(0, x, -kInf);
+        at = 0;
+        add(0, x);
+        j += kThreads;
+        ++i;
+      }
+      const int end = min(j1, w1);
+      // A segment of nothing but -inf keeps its first vector.
+      if (at < 0 && j < min(j1, first + n)) at = j;
+      for (; j + 3 * kThreads < end; j += 4 * kThreads) {
+        u32x4 v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = row.load_whole(j + q * kThreads);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float x[kE];
+          Row<F32>::unpack(v[q], x);
+          add(j + q * kThreads, x);
+        }
+      }
+      for (; j < end; j += kThreads) {
+        float x[kE];
+        Row<F32>::unpack(row.load_whole(j), x);
+        add(j, x);
+      }
+      if (tail && j == last && last < j1) {
+        float x[kE];
+        row.load(last, x, -kInf);
+        add(last, x);
+      }
+      i = i1;
+      if constexpr (TOP) {
+        // The group's best: its largest logit, the lowest vector among equals.
+        const uint32_t v = at >= 0 ? order_bits(seg_m) : 0u;
+        uint32_t most = v;
+        if (who.lg > 0) most = xred_umax<1>(most);
+        if (who.lg > 1) most = xred_umax<2>(most);
+        if (who.lg > 2) most = xred_umax<4>(most);
+        uint32_t low = at >= 0 && v == most ? ~(uint32_t)(row.index(at) + kE - 1) : 0u;
+        if (who.lg > 0) low = xred_umax<1>(low);
+        if (who.lg > 1) low = xred_umax<2>(low);
+        if (who.lg > 2) low = xred_umax<4>(low);
+        const u64 bound = ((u64)most << 32) | low;
+        if ((tid & ((1 << who.lg) - 1)) == 0) top.best[seg * (kThreads >> who.lg) + (tid >> who.lg)] = bound;
+        seg_m = -kInf;
+        at = -1;
       }
     }
-    for (; j < end; j += kThreads) {
-      float x[kE];
-      Row<F32>::unpack(row.load_whole(j), x);
-      add(j, x);
-    }
-    if (last > 0 && end == last && j == last && last < first + n) {
-      float x[kE];
-      row.load(last, x, -kInf);
-      add(last, x);
-    }
   }
-  const float most = a.m;  // of this thread's logits
-  const bool any = tid < n;
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) a = join(a, Sums{shfl_xor(a.m, off), shfl_xor(a.s, off), shfl_xor(a.u, off)}, mul);
   if ((tid & 63) == 0) part[tid >> 6] = a;
@@ -350,21 +474,19 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobParams p) {
   a = part[0];
   for (int i = 1; i < kThreads / 64; ++i) a = join(a, part[i], mul);
   const RowItems<F32> items{row, first, n};
-  // The best key's index is one of vector `at`: bounds from its last and first.
-  const u64 low = any ? make_key(most, min(p.V - 1, row.index(at) + kE - 1)) : 0u;
-  const u64 high = any ? make_key(most, max(0, row.index(at))) : 0u;
-
+  // The row's sums, then its keys, of all runs.
+  uint8_t* const work = p.part + t * (size_t)p.parts * kLogprobPart;
+  u64* const kept = reinterpret_cast<u64*>(work + 16 * (size_t)p.parts);
   if (p.parts > 1) {
-    uint8_t* const work = p.part + t * (size_t)p.parts * kLogprobPart;
-    uint8_t* const mine = work + (size_t)run * kLogprobPart;
+    float* const sums = reinterpret_cast<float*>(work);
     if (tid == 0) {
-      store_agent(reinterpret_cast<float*>(mine), a.m);
-      store_agent(reinterpret_cast<float*>(mine) + 1, a.s);
-      store_agent(reinterpret_cast<float*>(mine) + 2, a.u);
+      store_agent(sums + 4 * run, a.m);
+      store_agent(sums + 4 * run + 1, a.s);
+      store_agent(sums + 4 * run + 2, a.u);
     }
-    if (p.k > 0) {
-      u64* const keys = reinterpret_cast<u64*>(mine + 16);
-      block_top(items, low, high, p.k, top, [&](int rank, u64 key) {
+    if constexpr (TOP) {
+      u64* const keys = kept + run * p.k;
+      block_top(items, who, p.k, top, [&](int rank, u64 key) {
         __hip_atomic_store(keys + rank, key, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       });
       // A run of fewer than k elements leaves the rest empty.
@@ -384,7 +506,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobParams p) {
     handoff_order();
     a = Sums{-kInf, 0.0f, 0.0f};
     if (tid < p.parts) {  // at most 64: one wave
-      float* const f = reinterpret_cast<float*>(work + (size_t)tid * kLogprobPart);
+      float* const f = sums + 4 * tid;
       a = Sums{load_agent(f), load_agent(f + 1), load_agent(f + 2)};
     }
     if (tid < 64) {
@@ -413,7 +535,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobParams p) {
       p.logprob[t] = v;
     }
   }
-  if (p.k == 0) return;
+  if constexpr (!TOP) return;
   float* tv = p.top_logprob + t * (size_t)p.k;
   int64_t* ti = p.top_ids + t * (size_t)p.k;
   if (bad) {
@@ -429,15 +551,20 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobParams p) {
     ti[rank] = key_index(key);
   };
   if (p.parts == 1) {
-    block_top(items, low, high, p.k, top, out);
+    block_top(items, who, p.k, top, out);
   } else {
-    const KeyItems kept{p.part + t * (size_t)p.parts * kLogprobPart, p.k, p.parts * p.k};
+    const KeyItems items2{kept, p.parts * p.k};
     u64 best = 0;
-    for (int i = tid; i < kept.n; i += kThreads) {
-      const u64 key = kept.at(i);
+#pragma unroll 4
+    for (int i = tid; i < items2.n; i += kThreads) {
+      const u64 key = items2.load(i);
       best = key > best ? key : best;
     }
-    block_top(kept, best, best, p.k, top, out);
+    __syncthreads();  // the run's own bounds have been read
+    top.best[tid] = best;
+    Owners each(1);  // thread t's keys t, t + 256, ...
+    each.len = (items2.n + kThreads - 1) / kThreads;
+    block_top(items2, each, p.k, top, out);
   }
 }
 
@@ -520,10 +647,14 @@ int logprob_parts(int T, int V, bool f32, int* per) {
 
 hipError_t launch_logprobs(const LogprobParams& p, bool f32, hipStream_t s) {
   const dim3 grid((unsigned)p.T * (unsigned)p.parts);
-  if (f32)
-    hipLaunchKernelGGL(logprobs_kernel<true>, grid, dim3(kThreads), 0, s, p);
+  if (f32 && p.k > 0)
+    hipLaunchKernelGGL((logprobs_kernel<true, true>), grid, dim3(kThreads), 0, s, p);
+  else if (f32)
+    hipLaunchKernelGGL((logprobs_kernel<true, false>), grid, dim3(kThreads), 0, s, p);
+  else if (p.k > 0)
+    hipLaunchKernelGGL((logprobs_kernel<false, true>), grid, dim3(kThreads), 0, s, p);
   else
-    hipLaunchKernelGGL(logprobs_kernel<false>, grid, dim3(kThreads), 0, s, p);
+    hipLaunchKernelGGL((logprobs_kernel<false, false>), grid, dim3(kThreads), 0, s, p);
   return hipGetLastError();
 }
 
