@@ -87,11 +87,17 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 // load (vmcnt 0) at the next LDS read, whatever buffer that reads: the caller
 // counts the loads and waits itself before the barrier that publishes them.
 // No register is written, so nothing can be overwritten by a load in flight.
+template <bool STREAM = false>
 __device__ __forceinline__ void ld16_to_lds(u32x4 rsrc, uint32_t off, uint32_t uniform_off, uint32_t lds) {
 #ifdef __HIP_DEVICE_COMPILE__
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(off), "s"(rsrc),
-               "s"(uniform_off)
-               : "memory", "m0");
+  if constexpr (STREAM)  // non-temporal
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds" ::"s"(lds), "v"(off), "s"(rsrc),
+                 "s"(uniform_off)
+                 : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(off), "s"(rsrc),
+                 "s"(uniform_off)
+                 : "memory", "m0");
 #endif
 }
 

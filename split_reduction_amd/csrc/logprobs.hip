@@ -505,7 +505,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobParams p) {
     if (arrived + 1 != (uint32_t)p.parts) return;
     handoff_order();
     a = Sums{-kInf, 0.0f, 0.0f};
-    if (tid < p.parts) {  // at most 64: one wave
+    if (tid < p.parts) {  // at most 32: one wave
       float* const f = sums + 4 * tid;
       a = Sums{load_agent(f), load_agent(f + 1), load_agent(f + 2)};
     }
@@ -636,10 +636,14 @@ __global__ __launch_bounds__(kThreads) void logprobs_grad_kernel(LogprobGradPara
 }  // namespace
 
 // A row is split while there are fewer workgroups than keep the card busy, down
-// to one vector a thread; at most 64 runs, so that one wave joins them.
+// to one vector a thread; at most 32 runs (one wave joins them). About 1024
+// workgroups: with 2048 / 1024 / 512 / 256, T=67 V=50001 float took 21.2 / 17.7 /
+// 17.9 / 23.9 us, T=300 V=131072 bf16 44.1 / 37.8 / 42.4 / 42.5 us (8
+// alternatives); with up to 64 / 32 / 16 runs, T=1 V=131072 bf16 13.7 / 13.9 /
+// 14.6 us for 8 and 31.7 / 22.5 / 20.8 us for 64 alternatives.
 int logprob_parts(int T, int V, bool f32, int* per) {
   const int steps = (V / (f32 ? 4 : 8) + 2 + kThreads - 1) / kThreads;  // vectors a thread, partial ends included
-  const int want = std::max(1, std::min(64, 2048 / std::max(T, 1)));
+  const int want = std::max(1, std::min(32, 1024 / std::max(T, 1)));
   const int each = (steps + want - 1) / want;
   *per = each * kThreads;
   return (steps + each - 1) / each;

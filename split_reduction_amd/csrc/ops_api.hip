@@ -202,7 +202,7 @@ SKGEMM_API int skgemm_logprobs(const void* logits, const int64_t* tokens, float*
   p.k = top_k;
   p.scale = scale;
   p.parts = skg::logprob_parts(T, V, logits_format == SKGEMM_F32, &p.per);
-  if (p.parts > 1) {  // then T <= 1024: at most 2048 runs
+  if (p.parts > 1) {  // then T <= 512: at most 1024 runs
     uint8_t* w = nullptr;
     rc = ops_workspace(stream, &w);
     if (rc != SKGEMM_OK) return rc;
