@@ -413,23 +413,29 @@ __global__ __launch_bounds__(512) void i8_big_kernel(I8Params p) {
 
 namespace {
 
-// The tile shapes and what a call with each costs, fitted to the times of 6279
+// The tile shapes and what a call with each costs, fitted to the times of 7035
 // calls (T = 9..4096, N = 549..18432, K = 1024..16384, every shape, K split 1
-// to 8 ways): a workgroup pays kStart and then `alone` a step while the CU
-// has room for it (`fit` at once), or `crowded` a step for each workgroup of
-// the CU where they queue; K split S ways adds kJoinRank S and the sums'
-// traffic. Over those sizes the choice is 2 % slower on average than the
-// fastest call found for each, 15 % at worst.
+// to 8 ways) and then to the choices: a workgroup pays kStart and `alone` a step
+// while the CU has room for it (`fit` at once), or `crowded` a step for each
+// workgroup of the CU where they queue; the weights pass at kWeights at most; K
+// split S ways adds kJoinRank S and the sums' traffic. Over those 216 sizes the
+// choice is 1.5 % slower on average than the fastest call found for each (T=128
+// N=16384 K=4096, the worst: 26.8 against 21.9 us).
+// Why these six, each against the best of the others (us): 256 x 256 T=4096
+// N=K=16384 1007 / 1139; 256 x 128 T=1024 N=18432 K=7168 156 / 166; 128 x 128
+// two to a CU T=4096 N=12000 K=1024 74 / 83; 128 x 128 with four buffers T=256
+// N=18432 K=7168 62 / 66; 64 x 64 T=64 N=K=16384 56 / 64; 32 x 64 T=32 N=18432
+// K=7168 30 / 34.
 struct TileShape {
   int bt, bn, fit;
   float alone, crowded;  // us a step of 128 bytes of K
 };
 constexpr TileShape kShapes[] = {
-    {256, 256, 1, 1.78f, 1.72f}, {128, 128, 2, 0.950f, 0.474f}, {128, 128, 1, 0.272f, 0.821f},
-    {64, 64, 2, 0.314f, 0.230f}, {32, 64, 3, 0.217f, 0.135f},
+    {256, 256, 1, 2.081f, 1.922f}, {256, 128, 1, 0.301f, 1.116f}, {128, 128, 2, 0.956f, 0.532f},
+    {128, 128, 1, 0.499f, 0.634f}, {64, 64, 2, 0.324f, 0.204f},   {32, 64, 3, 0.226f, 0.179f},
 };
-constexpr float kStart = 0.315f, kJoinRank = 0.152f;         // us
-constexpr float kWeights = 5.74e6f, kSums = 4.42e6f;         // bytes a us
+constexpr float kStart = 0.41f, kJoinRank = 0.222f;    // us
+constexpr float kWeights = 10.69e6f, kSums = 4.56e6f;  // bytes a us
 constexpr int kShapeCount = (int)(sizeof(kShapes) / sizeof(kShapes[0]));
 template <int BT, int BN, int WT, int WN, int STG>
 void launch_tile(const I8Params& p, int grid, hipStream_t s) {
@@ -441,9 +447,10 @@ void launch_shape(int shape, const I8Params& p, int grid, hipStream_t s) {
     case 0:
       hipLaunchKernelGGL(i8_big_kernel, dim3((unsigned)grid), dim3(512), 0, s, p);
       return;
-    case 1: return launch_tile<128, 128, 2, 2, 2>(p, grid, s);
-    case 2: return launch_tile<128, 128, 2, 2, 4>(p, grid, s);
-    case 3: return launch_tile<64, 64, 1, 4, 4>(p, grid, s);
+    case 1: return launch_tile<256, 128, 4, 2, 3>(p, grid, s);
+    case 2: return launch_tile<128, 128, 4, 2, 2>(p, grid, s);
+    case 3: return launch_tile<128, 128, 2, 4, 4>(p, grid, s);
+    case 4: return launch_tile<64, 64, 2, 4, 4>(p, grid, s);
     default: return launch_tile<32, 64, 1, 4, 4>(p, grid, s);
   }
 }

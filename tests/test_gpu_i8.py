@@ -79,12 +79,12 @@ def test_i8_strides(T, N, K):
         check(run(w, ws, x, xs, kind, pad=pad, wpad=48, xpad=16), want, kind)
 
 
-# Every tile shape, and the kernel without tiles (5), pinned: sizes below, at and
+# Every tile shape, and the kernel without tiles (6), pinned: sizes below, at and
 # past a tile, K that ends inside a step, and K split over workgroups, among them
 # calls of more tiles than one round of workgroups, of which only the last are
 # split.
 @pytest.mark.gpu
-@pytest.mark.parametrize("shape", range(6))
+@pytest.mark.parametrize("shape", range(7))
 @pytest.mark.parametrize("T,N,K", [(1, 1, 16), (33, 65, 144), (256, 256, 128), (257, 300, 1040), (700, 129, 4112)])
 def test_i8_shapes(T, N, K, shape, tune):
     w, x, ws, xs = codes(N, K, 1), codes(T, K, 2), scales(N, 3), scales(T, 4)
@@ -101,8 +101,8 @@ def test_i8_shapes(T, N, K, shape, tune):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("shape,T,N,K", [(0, 4000, 4300, 400), (1, 3000, 3100, 272), (2, 2000, 2200, 400), (3, 1500, 1600, 400),
-                                         (4, 1000, 1700, 400)])
+@pytest.mark.parametrize("shape,T,N,K", [(0, 4000, 4300, 400), (1, 4000, 2300, 400), (2, 3000, 3100, 272),
+                                         (3, 2000, 2200, 400), (4, 1500, 1600, 400), (5, 1000, 1700, 400)])
 def test_i8_last_round_split(shape, T, N, K, tune):
     w, x, ws, xs = codes(N, K, 1), codes(T, K, 2), scales(N, 3), scales(T, 4)
     _, want = O.i8_ref(x, xs, w, ws)
