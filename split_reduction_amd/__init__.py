@@ -157,7 +157,7 @@ def _rows(a, rows: int, row_bytes: int, stride, what: str, esize: int = 0):
     `esize` bytes (0: any) and reach to the end of the last row."""
     if a is None or isinstance(a, int):
         return a or 0, row_bytes if stride is None else stride
-    if not _on_gpu(a):
+    if not a.is_cuda:
         raise SkgemmError(SKGEMM_EINVAL, f"{what}: a tensor on {a.device}, not on the GPU")
     size = a.element_size()
     if esize and size != esize:

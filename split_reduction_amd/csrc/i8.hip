@@ -421,11 +421,11 @@ namespace {
 // split S ways adds kJoinRank S and the sums' traffic. Over those 216 sizes the
 // choice is 1.5 % slower on average than the fastest call found for each (T=128
 // N=16384 K=4096, the worst: 26.8 against 21.9 us).
-// Why these six, each against the best of the others (us): 256 x 256 T=4096
-// N=K=16384 1007 / 1139; 256 x 128 T=1024 N=18432 K=7168 156 / 166; 128 x 128
-// two to a CU T=4096 N=12000 K=1024 74 / 83; 128 x 128 with four buffers T=256
-// N=18432 K=7168 62 / 66; 64 x 64 T=64 N=K=16384 56 / 64; 32 x 64 T=32 N=18432
-// K=7168 30 / 34.
+// Why these six, each against the best of the others (us): 256 x 256 T=N=4096
+// K=7168 111 / 122; 256 x 128 T=509 N=18432 K=7168 92 / 100; 128 x 128 two to a
+// CU T=384 N=18432 K=7168 66 / 80; 128 x 128 with four buffers T=128 N=16384
+// K=4096 21.9 / 26.8; 64 x 64 T=256 N=7168 K=2048 12.1 / 15.2; 32 x 64 T=64 N=6015
+// K=2736 10.3 / 12.4.
 struct TileShape {
   int bt, bn, fit;
   float alone, crowded;  // us a step of 128 bytes of K
