@@ -120,13 +120,6 @@ def _check(code: int, name: str) -> None:
         raise SkgemmError(code, f"{name}: {strerror(code)}{extra}")
 
 
-def _on_gpu(a) -> bool:
-    try:
-        return a.is_cuda  # a tenth of the time that a.device.type takes
-    except AttributeError:
-        return a.device.type == "cuda"
-
-
 def _ptr(a, nbytes: int = 0, what: str = "argument") -> int:
     """Device address of a tensor or of a plain integer address (None is 0).
 
@@ -140,7 +133,11 @@ def _ptr(a, nbytes: int = 0, what: str = "argument") -> int:
         return 0
     if isinstance(a, int):
         return a
-    if not _on_gpu(a):
+    try:
+        on_gpu = a.is_cuda  # a tenth of the time that a.device.type takes
+    except AttributeError:
+        on_gpu = a.device.type == "cuda"
+    if not on_gpu:
         raise SkgemmError(SKGEMM_EINVAL, f"{what}: a tensor on {a.device}, not on the GPU")
     if not a.is_contiguous():
         raise SkgemmError(SKGEMM_EINVAL, f"{what}: not contiguous")

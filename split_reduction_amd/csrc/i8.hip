@@ -427,7 +427,7 @@ namespace {
 // K=4096 21.9 / 26.8; 64 x 64 T=256 N=7168 K=2048 12.1 / 15.2; 32 x 64 T=64 N=6015
 // K=2736 10.3 / 12.4.
 struct TileShape {
-  int bt, bn, fit;
+  unsigned bt, bn, fit;
   float alone, crowded;  // us a step of 128 bytes of K
 };
 constexpr TileShape kShapes[] = {
@@ -483,20 +483,22 @@ I8Tactic pick_i8(int T, int N, int K) {
   const long work = (long)N * K;
   const bool rows = T <= 8 || (T <= 16 && work <= 8L << 20) || (T <= 32 && work <= 2L << 20);
   if (pinned >= kShapeCount || (pinned < 0 && rows)) return best;
-  const int steps = std::max(1, (K + 127) / 128);
+  const unsigned steps = std::max(1u, ((unsigned)K + 127) / 128);
   float least = 0.0f;
   for (int i = 0; i < kShapeCount; ++i) {
     if (pinned >= 0 && i != pinned) continue;
     const TileShape& sh = kShapes[i];
-    const long tiles = ((long)T + sh.bt - 1) / sh.bt * ((N + sh.bn - 1) / sh.bn);
-    const size_t bytes = (size_t)sh.bt * sh.bn * 4;
-    for (int S = 1; S <= 8; ++S) {
-      if (split > 0 && S != std::min(split, steps)) continue;
+    // At most 2^16 x 2^12 tiles; 32-bit divisions, as this is on every call's way.
+    const unsigned tiles = (((unsigned)T + sh.bt - 1) / sh.bt) * (((unsigned)N + sh.bn - 1) / sh.bn);
+    // Only the tiles past the last full round of workgroups are split.
+    const unsigned round = 256u * sh.fit, split_rest = tiles % round;
+    const size_t bytes = (size_t)(sh.bt * sh.bn) * 4;
+    for (unsigned S = 1; S <= 8; ++S) {
+      if (split > 0 && S != std::min((unsigned)split, steps)) continue;
       if (S > steps) break;
-      // Only the tiles past the last full round of workgroups are split.
-      const long round = 256L * sh.fit, whole = S > 1 ? tiles / round * round : 0, rest = tiles - whole;
-      if (S > 1 && (rest == 0 || (size_t)(rest * S) * bytes > kOpsPartBytes || rest > kOpsCounters)) continue;
-      const long m = (rest * S + 255) / 256, each = (steps + S - 1) / S;
+      const unsigned rest = S > 1 ? split_rest : tiles, whole = tiles - rest;
+      if (S > 1 && (rest == 0 || rest * S * bytes > kOpsPartBytes || rest > (unsigned)kOpsCounters)) continue;
+      const unsigned m = (rest * S + 255) / 256, each = (steps + S - 1) / S;
       float us = std::max((float)((m + sh.fit - 1) / sh.fit) * (kStart + (float)each * sh.alone),
                           (float)m * (kStart + (float)each * sh.crowded));
       us += (float)(whole / 256) * (kStart + (float)steps * sh.crowded);
@@ -505,7 +507,7 @@ I8Tactic pick_i8(int T, int N, int K) {
       if (best.shape < 0 || us < least) {
         least = us;
         best.shape = i;
-        best.S = S;
+        best.S = (int)S;
         best.whole = (int)whole;
         best.tiles = (int)tiles;
       }

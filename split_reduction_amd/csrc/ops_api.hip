@@ -48,7 +48,12 @@ int ops_workspace(hipStream_t stream, uint8_t** out) {
     (void)hipFree(p);
     return skg::hip_fail(e);
   }
-  g_work[std::make_pair(dev, stream)] = static_cast<uint8_t*>(p);
+  try {
+    g_work[std::make_pair(dev, stream)] = static_cast<uint8_t*>(p);
+  } catch (...) {  // no exception leaves a C entry
+    (void)hipFree(p);
+    return SKGEMM_ENOMEM;
+  }
   *out = static_cast<uint8_t*>(p);
   return SKGEMM_OK;
 }
