@@ -107,6 +107,17 @@ __device__ __forceinline__ Sums join(Sums a, Sums b, float mul) {
 
 __device__ __forceinline__ float shfl_xor(float v, int off) { return __shfl_xor(v, off, 64); }
 
+// The join of a workgroup's parts, in every thread. `part` is free again after
+// the next barrier.
+__device__ __forceinline__ void block_join(Sums& a, Sums* part, float mul) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) a = join(a, Sums{shfl_xor(a.m, off), shfl_xor(a.s, off), shfl_xor(a.u, off)}, mul);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = a;
+  __syncthreads();
+  a = part[0];
+  for (int i = 1; i < kThreads / 64; ++i) a = join(a, part[i], mul);
+}
+
 // ---- the best k ---------------------------------------------------------------
 //
 // Order: value first, then the lower index. A key holds both: the value's bits
@@ -382,6 +393,13 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobParams p) {
   const Owners who(TOP ? rounds : 1);
   float seg_m = -kInf;  // TOP: this segment's largest logit, and the first vector that holds it
   int at = -1;
+  // The sums are kept against ref = m mul, rounded (one fused operation a logit
+  // instead of two: the kernel is bound by its arithmetic at 2 bytes a logit),
+  // and moved to m itself at the end. A product past FP32's range (the type's
+  // lowest value, say) is held inside it; such a run's sums come out as 0 or not
+  // finite and are taken again below.
+  auto in_range = [](float v) { return fminf(fmaxf(v, -3e38f), 3e38f); };
+  float ref = -3e38f;
   auto add = [&](int j, const float* x) {
     float m = x[0];
 #pragma unroll
@@ -391,15 +409,15 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobParams p) {
       seg_m = fmaxf(seg_m, m);
     }
     if (m > a.m) {
-      const float d = (a.m - m) * mul, f = exp2_hw(d);
+      const float r = in_range(m * mul), d = ref - r, f = exp2_hw(d);
       a.u = f * (a.u + fmaxf(d, -1e30f) * a.s);
       a.s *= f;
       a.m = m;
+      ref = r;
     }
-    const float ref = a.m == -kInf ? 0.0f : a.m;  // nothing but banned tokens so far: d = -inf
 #pragma unroll
     for (int e = 0; e < kE; ++e) {
-      const float d = (x[e] - ref) * mul, w = exp2_hw(d);
+      const float d = fmaf(x[e], mul, -ref), w = exp2_hw(d);
       a.s += w;
       a.u = fmaf(w, fmaxf(d, -1e30f), a.u);  // 0 * -1e30 where 0 * -inf would be NaN
     }
@@ -467,12 +485,30 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobParams p) {
       }
     }
   }
+  if (a.s != 0.0f) {  // to the reference m: d = (x mul - ref) - (m mul - ref)
+    const float c = fmaf(a.m, mul, -ref), f = exp2_hw(-c);
+    a.u = f * (a.u - c * a.s);
+    a.s *= f;
+  }
+  block_join(a, part, mul);
+  if (fabsf(a.m) < kInf && !(a.s > 0.0f && a.s < kInf)) {
+    // Logits near the type's ends (or a NaN among finite ones): differences
+    // first, with the run's largest logit as the reference.
+    const float m = a.m;
+    a = Sums{m, 0.0f, 0.0f};
+    for (int j = first + tid; j < first + n; j += kThreads) {
+      float x[kE];
+      row.load(j, x, -kInf);
 #pragma unroll
-  for (int off = 32; off > 0; off >>= 1) a = join(a, Sums{shfl_xor(a.m, off), shfl_xor(a.s, off), shfl_xor(a.u, off)}, mul);
-  if ((tid & 63) == 0) part[tid >> 6] = a;
-  __syncthreads();
-  a = part[0];
-  for (int i = 1; i < kThreads / 64; ++i) a = join(a, part[i], mul);
+      for (int e = 0; e < kE; ++e) {
+        const float d = (x[e] - m) * mul, w = exp2_hw(d);
+        a.s += w;
+        a.u = fmaf(w, fmaxf(d, -1e30f), a.u);
+      }
+    }
+    __syncthreads();
+    block_join(a, part, mul);
+  }
   const RowItems<F32> items{row, first, n};
   // The row's sums, then its keys, of all runs.
   uint8_t* const work = p.part + t * (size_t)p.parts * kLogprobPart;
