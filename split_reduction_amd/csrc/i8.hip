@@ -269,21 +269,26 @@ __device__ __forceinline__ bool join_ranks(const I8Params& p, int tile, int S, i
 }
 
 // The outputs of a wave's kNT x kMT blocks of 16 features x 16 tokens, block
-// (0, 0) at feature n0 and token t0.
+// (0, 0) at feature n0 and token t0. A token's blocks go out one after another,
+// so that the 32-byte pieces of a line meet in the L2.
 template <int kNT, int kMT>
 __device__ __forceinline__ void store_blocks(const I8Params& p, int t0, int n0, const i32x4* acc, int lane) {
   const int i = lane & 15, g = lane >> 4;
+  float ws[kNT][4];
 #pragma unroll
-  for (int k = 0; k < kNT; ++k) {
-    const int n = n0 + 16 * k + 4 * g;
-    float ws[4];
+  for (int k = 0; k < kNT; ++k)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) ws[e] = n + e < p.N ? p.w_scale[n + e] : 0.0f;
-#pragma unroll
-    for (int j = 0; j < kMT; ++j) {
-      const int t = t0 + 16 * j + i;
-      if (t < p.T) store_sums(p, t, n, acc[k * kMT + j], p.x_scale[t], ws);
+    for (int e = 0; e < 4; ++e) {
+      const int n = n0 + 16 * k + 4 * g + e;
+      ws[k][e] = n < p.N ? p.w_scale[n] : 0.0f;
     }
+#pragma unroll
+  for (int j = 0; j < kMT; ++j) {
+    const int t = t0 + 16 * j + i;
+    if (t >= p.T) continue;
+    const float xs = p.x_scale[t];
+#pragma unroll
+    for (int k = 0; k < kNT; ++k) store_sums(p, t, n0 + 16 * k + 4 * g, acc[k * kMT + j], xs, ws[k]);
   }
 }
 
