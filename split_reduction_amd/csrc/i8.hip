@@ -57,7 +57,9 @@ __device__ __forceinline__ void store_sums(const I8Params& p, int t, int n, i32x
 // Both operands come as line pairs (device/types.h): 8 rows x 128 bytes a load,
 // whole lines; one DPP move a register makes the two 16-row operands. With at
 // most 8 tokens the second load of the activations' pair is left out. U units
-// are in flight in each wave: a slot is consumed, then refilled.
+// are in flight in each wave: a slot is consumed, then refilled. Bound by the
+// weights: T=1 N=18432 K=7168 23.5 us (5.6 TB/s), T=8 N=K=16384 51 us (5.2);
+// below about 30 MB by launch and latency (T=1 N=2048 K=7168 6.6 us).
 template <int NT, bool LOW, int RG, int WAVES, int U>
 __global__ __launch_bounds__(64 * WAVES) void i8_rows_kernel(I8Params p) {
   constexpr int kXL = LOW ? 1 : 2;  // loads of 16 tokens
@@ -153,6 +155,11 @@ __global__ __launch_bounds__(64 * WAVES) void i8_rows_kernel(I8Params p) {
 // registers. One barrier a step: past it, every wave's loads of this step have
 // landed and every wave has read the previous step's buffer, which the next
 // loads then fill.
+//
+// Bound by the products for large calls, by the weights' stream for few tokens
+// (T=32 N=18432 K=7168: 29.4 us, 4.5 TB/s) and in between by the loads into LDS,
+// up to 70 GB/s a CU (T=509 N=4100 K=7168: 30.4 us). Loads counted by hand: left
+// to the compiler, T=4096 N=18432 K=7168 took 664 instead of 582 us.
 //
 // S workgroups may split K of a tile: each stores its sums to the workspace and
 // the last to arrive adds the others' (integers: the order does not matter).
@@ -341,9 +348,13 @@ __global__ __launch_bounds__(64 * WT * WN) void i8_tile_kernel(I8Params p) {
 // take turns. A step is four phases, each closed by a barrier: operands of the
 // first 64 bytes of K from LDS (R0), their products (M0), the other 64 bytes
 // (R1, M1). Waves 4-7 (the second of each SIMD) run one phase behind waves 0-3,
-// so that while one wave of a SIMD multiplies the other reads: the matrix unit
-// is fed without a pause and only four waves at a time share the LDS
-// (12 x 8 cycles each, 384 against 512 of a phase's 32 products).
+// so that while one wave of a SIMD multiplies the other reads, and only four
+// waves at a time share the LDS (all eight in step: 591 against 561 us at
+// T=N=K=8192).
+// T=4096 N=18432 K=7168: 507 us, 2.13 POP/s; the clock is then held at 1.85 of
+// 2.4 GHz by power. T=N=K=8192 took 560 us, without the loads 430, without loads
+// and LDS reads 404; the 32 x 32 x 32 instruction took 617 against 534 us, four
+// stages of 64 bytes 602 against 560.
 // With A's step s in phases 4s .. 4s+3 and B's one later, the last reads of
 // step s - 1 are B's R1 in phase 4s - 1: from phase 4s on its buffer may be
 // filled for step s + 1 (A issues in its R0, B in its M1 before), and the loads
