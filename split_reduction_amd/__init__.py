@@ -152,6 +152,8 @@ def _rows(a, rows: int, row_bytes: int, stride, what: str, esize: int = 0):
     and contiguous, `stride` bytes apart (None: as the tensor's own rows are, or
     dense for an address). The tensor must be on the GPU, hold elements of
     `esize` bytes (0: any) and reach to the end of the last row."""
+    if stride is not None and stride < 0:
+        raise SkgemmError(SKGEMM_EINVAL, f"{what}: a negative row stride")
     if a is None or isinstance(a, int):
         return a or 0, row_bytes if stride is None else stride
     if not a.is_cuda:
