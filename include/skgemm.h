@@ -220,7 +220,8 @@ SKGEMM_API int skgemm_mxfp8_batched(const void* Wq8, const void* Wscale, const v
  * several workgroups meets in a workspace of the stream that is separate from
  * the split-K workspace above and of one fixed size: the first call on a stream
  * allocates it, skgemm_reserve_ops does so ahead of a graph capture, and
- * skgemm_release frees it.
+ * skgemm_release frees it. A captured call keeps the workspace of the stream it
+ * was captured on: its replays must not overlap other calls that use that one.
  */
 #define SKGEMM_OPS_WORKSPACE_BYTES ((size_t)65 << 20)
 enum skgemm_format {

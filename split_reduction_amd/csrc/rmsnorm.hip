@@ -11,9 +11,8 @@
 // free of rstd: sum(h^2) and max|h g| meet in one reduction behind one barrier.
 //
 // Bound by memory: 7 bytes an element (x, r, R_out, codes) and about 10 vector
-// operations. One vector a thread wherever 1024 threads reach that far, so that
-// all of a row's loads are in flight at once. T=8192 H=7168 with a residual and
-// E4M3 codes: 83.7 us, 4.9 TB/s (a large copy reaches 5.1); T=1: 3.5 us.
+// operations. T=8192 H=7168 with a residual and E4M3 codes: 70.6 us, 5.8 TB/s (a
+// large copy reaches 5.1); T=1: 3.5 us.
 
 #include "device/block.h"
 #include "device/pack.h"
@@ -38,9 +37,16 @@ constexpr float top_code() {
   return OUT == SKGEMM_I8 ? 127.0f : 448.0f;
 }
 
+template <bool STREAM>
+__device__ __forceinline__ u32x4 load16(const u32x4* p) {
+  if constexpr (STREAM) return __builtin_nontemporal_load(p);
+  return *p;
+}
+
+// STREAM: x and r are loaded non-temporally.
 // VPT: vectors of 8 elements a thread holds; thread i takes vectors i,
 // i + blockDim, ... so that a wave's loads and stores are contiguous.
-template <int VPT, int OUT>
+template <int VPT, int OUT, bool STREAM>
 __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormParams p) {
   __shared__ float part[32];
   const size_t t = blockIdx.x;
@@ -56,8 +62,8 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormParams p) {
   for (int i = 0; i < VPT; ++i) {
     const int v = (int)threadIdx.x + i * (int)blockDim.x;
     const bool ok = v < nv;
-    xv[i] = ok ? x[v] : u32x4{0, 0, 0, 0};
-    rv[i] = (ok && r != nullptr) ? r[v] : u32x4{0, 0, 0, 0};
+    xv[i] = ok ? load16<STREAM>(x + v) : u32x4{0, 0, 0, 0};
+    rv[i] = (ok && r != nullptr) ? load16<STREAM>(r + v) : u32x4{0, 0, 0, 0};
     gv[i] = (ok && g != nullptr) ? g[v] : ones;
   }
   float h[VPT * 8], hg[VPT * 8];
@@ -163,29 +169,35 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormParams p) {
   }
 }
 
-template <int VPT>
-void launch_vpt(const NormParams& p, int out_format, unsigned threads, hipStream_t s) {
-  const dim3 grid((unsigned)p.T), block(threads);
+template <int VPT, bool STREAM>
+void launch_vpt(const NormParams& p, int out_format, hipStream_t s) {
+  const int nv = p.H / 8;
+  const dim3 grid((unsigned)p.T), block((unsigned)((((nv + VPT - 1) / VPT) + 63) / 64 * 64));
   if (out_format == SKGEMM_BF16)
-    hipLaunchKernelGGL((rmsnorm_kernel<VPT, SKGEMM_BF16>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((rmsnorm_kernel<VPT, SKGEMM_BF16, STREAM>), grid, block, 0, s, p);
   else if (out_format == SKGEMM_I8)
-    hipLaunchKernelGGL((rmsnorm_kernel<VPT, SKGEMM_I8>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((rmsnorm_kernel<VPT, SKGEMM_I8, STREAM>), grid, block, 0, s, p);
   else
-    hipLaunchKernelGGL((rmsnorm_kernel<VPT, SKGEMM_E4M3>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((rmsnorm_kernel<VPT, SKGEMM_E4M3, STREAM>), grid, block, 0, s, p);
 }
 
 }  // namespace
 
+// Few rows: as many threads as a row has vectors, up to 1024, so that all loads
+// go out at once. Many rows of more than 512 vectors: four vectors a thread, so
+// that more rows share a CU (T=8192 H=7168: 101 us with one, 77 with two, 75 with
+// four; T=8192 H=1024 12.4 / 13.1 us, left at one). Inputs past the 256 MB that
+// the last cache holds are loaded non-temporally (T=4096 H=16384: 84 against 76
+// us; T=8192 H=1024, which it holds, 12.4 against 13.8).
 hipError_t launch_rmsnorm(const NormParams& p, int out_format, hipStream_t s) {
-  const int nv = p.H / 8;
-  int vpt = 1;
-  while (nv > vpt * 1024) vpt *= 2;  // H <= 32768: at most 4
-  const unsigned threads = (unsigned)((((nv + vpt - 1) / vpt) + 63) / 64 * 64);
-  switch (vpt) {
-    case 1: launch_vpt<1>(p, out_format, threads, s); break;
-    case 2: launch_vpt<2>(p, out_format, threads, s); break;
-    default: launch_vpt<4>(p, out_format, threads, s); break;
-  }
+  const int nv = p.H / 8;  // at most 4096
+  const bool stream = (size_t)p.T * (size_t)p.H * 7 > ((size_t)256 << 20);
+  const int vpt = nv > 2048 || (nv > 512 && p.T > 1024) ? 4 : nv > 1024 ? 2 : 1;
+  if (vpt == 4 && stream) launch_vpt<4, true>(p, out_format, s);
+  else if (vpt == 4) launch_vpt<4, false>(p, out_format, s);
+  else if (vpt == 2) launch_vpt<2, false>(p, out_format, s);  // T <= 1024: below 256 MB
+  else if (stream) launch_vpt<1, true>(p, out_format, s);
+  else launch_vpt<1, false>(p, out_format, s);
   return hipGetLastError();
 }
 

@@ -94,6 +94,15 @@ def test_rmsnorm(T, H, fmt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,H,fmt", [(1100, 4104, "i8"), (1100, 4104, "bf16"), (9400, 4096, "e4m3"), (5000, 8192, "i8")])
+def test_rmsnorm_many_rows(T, H, fmt):
+    """Several vectors a thread, and inputs past the last cache."""
+    x, r, g = rows(T, H, seed=T)
+    log(f"rmsnorm T={T} H={H} {fmt}")
+    check(x, r, g, *run(x, r, g, fmt), 1e-6, fmt)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("fmt", ["bf16", "i8", "e4m3"])
 @pytest.mark.parametrize("res,gain,keep", [(False, True, True), (True, False, False), (False, False, False)])
 def test_rmsnorm_without(res, gain, keep, fmt):
