@@ -175,6 +175,12 @@ static_assert(kThreads == 256, "owner numbers are 8 bits");
 // of the data, whatever the values are, equal ones included. Should they hold
 // more than kCand keys past b, the exact k-th key is searched bit by bit over
 // the owners' items.
+//
+// The values are ordered, so no NaN is among them (fmaxf passes over one, a key
+// orders it: reaches() and the keys would disagree, and the search would end
+// with any number of candidates). The caller does not select from a run that
+// holds one. The candidates are bounded by their buffer all the same, as the
+// data are read twice and may change where a caller writes them meanwhile.
 template <class Src, class Out>
 __device__ __forceinline__ void block_top(const Src& src, const Owners& who, int k, TopLds& l, Out out) {
   const int tid = (int)threadIdx.x, lane = tid & 63;
@@ -295,7 +301,7 @@ __device__ __forceinline__ void block_top(const Src& src, const Owners& who, int
     __syncthreads();
     gather();
   }
-  const int n = l.n_cand;
+  const int n = min(l.n_cand, kCand);
   if (tid < 8) l.cand[n + tid] = 0;  // the ranks below are counted eight keys at a time
   __syncthreads();
   for (int i = tid; i < n; i += kThreads) {
@@ -522,12 +528,15 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobParams p) {
       store_agent(sums + 4 * run + 2, a.u);
     }
     if constexpr (TOP) {
+      // A NaN sum makes the row's ids -1: nothing is selected from such a run.
+      const bool sound = a.s == a.s;
       u64* const keys = kept + run * p.k;
-      block_top(items, who, p.k, top, [&](int rank, u64 key) {
-        __hip_atomic_store(keys + rank, key, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      });
+      if (sound)
+        block_top(items, who, p.k, top, [&](int rank, u64 key) {
+          __hip_atomic_store(keys + rank, key, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        });
       // A run of fewer than k elements leaves the rest empty.
-      if (tid >= top.n_cand && tid < p.k)
+      if (tid >= (sound ? top.n_cand : 0) && tid < p.k)
         __hip_atomic_store(keys + tid, (u64)0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     wait_vmem_all();

@@ -387,3 +387,30 @@ def test_logprobs_binding_refusals():
         with pytest.raises(sk.SkgemmError) as e:
             call(t.zeros(2, 32))
         assert e.value.code == sk.SKGEMM_EINVAL and "not on the GPU" in str(e.value)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V", [(3, 131072), (64, 131072), (300, 50001), (700, 40000)])
+@pytest.mark.parametrize("k", [20, 64])
+def test_logprobs_rows_of_many_nan(T, V, k, kind):
+    """NaN among banned logits, among ordinary ones, and alone, in rows that are
+    split and rows that are not; the other rows keep their results."""
+    t = torch()
+    z, tok = make(6, V, seed=V + k)
+    rng = np.random.default_rng(k)
+    z[0, rng.random(V) < 0.5] = -np.inf
+    z[0, np.isfinite(z[0])] = np.nan
+    z[1, ::2] = np.nan
+    z[2] = np.nan
+    z[3] = -np.inf
+    z[3, V - V // 40 :: 3] = np.nan  # in a split row's last runs
+    z[4, ::2] = -np.inf
+    rows = np.resize(np.arange(6), T)
+    log(f"logprobs many NaN T={T} V={V} k={k} {kind}")
+    Z = dev_logits(z, kind)[t.from_numpy(rows).to(DEV)].contiguous()
+    got = forward(Z, tok[rows], k, 1.0)
+    n = min(T, 24)  # past these, rows and their alignments repeat
+    for name, a in got.items():
+        assert np.array_equal(a, a[np.arange(T) % 24], equal_nan=True), name
+    check_forward(Z[:n], tok[rows][:n], k, 1.0, got={name: a[:n] for name, a in got.items()})
