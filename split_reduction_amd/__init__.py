@@ -36,6 +36,7 @@ FORMATS = {"bf16": 0, "i8": 1, "e4m3": 2, "f32": 3}
 
 _lib = None
 _raw_stream = _device = None  # torch's functions, bound by the first call that asks for the stream
+_torch_types = {}  # torch's element types that an operator's argument may have, filled by the first call
 
 
 class SkgemmError(RuntimeError):
@@ -120,15 +121,32 @@ def _check(code: int, name: str) -> None:
         raise SkgemmError(code, f"{name}: {strerror(code)}{extra}")
 
 
-def _ptr(a, nbytes: int = 0, what: str = "argument") -> int:
+def _types() -> dict:
+    """The element types of the operators' tensors. A type of the same width
+    would be read as the call's own: float16 logits as bf16, say."""
+    if not _torch_types:
+        import torch as t
+
+        _torch_types.update(bf16=(t.bfloat16,), f32=(t.float32,), i64=(t.int64,), i8=(t.int8,),
+                            i8_out=(t.int8, t.uint8), e4m3_out=(t.uint8, t.float8_e4m3fn))
+    return _torch_types
+
+
+def _check_type(a, types, what: str) -> None:
+    if a.dtype not in types:
+        raise SkgemmError(SKGEMM_EINVAL, f"{what}: elements of {a.dtype}, the call takes {' or '.join(map(str, types))}")
+
+
+def _ptr(a, nbytes: int = 0, what: str = "argument", types=None) -> int:
     """Device address of a tensor or of a plain integer address (None is 0).
 
     A tensor must live on the GPU, be contiguous and hold at least `nbytes`
     from its first element: the kernels read or write that dense block at the
     address, so a host tensor, a strided view or a short buffer would reach the
     device as a bad address. Such tensors raise SkgemmError(SKGEMM_EINVAL) here,
-    before anything is launched. Integer addresses are passed through unchecked
-    (the caller vouches for them)."""
+    before anything is launched, and so do elements of another type than `types`
+    (None: any). Integer addresses are passed through unchecked (the caller
+    vouches for them)."""
     if a is None:
         return 0
     if isinstance(a, int):
@@ -139,6 +157,8 @@ def _ptr(a, nbytes: int = 0, what: str = "argument") -> int:
         on_gpu = a.device.type == "cuda"
     if not on_gpu:
         raise SkgemmError(SKGEMM_EINVAL, f"{what}: a tensor on {a.device}, not on the GPU")
+    if types is not None:
+        _check_type(a, types, what)
     if not a.is_contiguous():
         raise SkgemmError(SKGEMM_EINVAL, f"{what}: not contiguous")
     have = a.numel() * a.element_size()
@@ -147,20 +167,19 @@ def _ptr(a, nbytes: int = 0, what: str = "argument") -> int:
     return a.data_ptr()
 
 
-def _rows(a, rows: int, row_bytes: int, stride, what: str, esize: int = 0):
+def _rows(a, rows: int, row_bytes: int, stride, what: str, types):
     """(address, row stride in bytes) of a matrix whose rows are `row_bytes` long
     and contiguous, `stride` bytes apart (None: as the tensor's own rows are, or
-    dense for an address). The tensor must be on the GPU, hold elements of
-    `esize` bytes (0: any) and reach to the end of the last row."""
+    dense for an address). The tensor must be on the GPU, hold elements of one
+    of `types` and reach to the end of the last row."""
     if stride is not None and stride < 0:
         raise SkgemmError(SKGEMM_EINVAL, f"{what}: a negative row stride")
     if a is None or isinstance(a, int):
         return a or 0, row_bytes if stride is None else stride
     if not a.is_cuda:
         raise SkgemmError(SKGEMM_EINVAL, f"{what}: a tensor on {a.device}, not on the GPU")
+    _check_type(a, types, what)
     size = a.element_size()
-    if esize and size != esize:
-        raise SkgemmError(SKGEMM_EINVAL, f"{what}: elements of {size} bytes, the call's have {esize}")
     if stride is None and a.numel() * size == rows * row_bytes and a.is_contiguous():
         return a.data_ptr(), row_bytes  # dense
     n = a.numel() * size
@@ -320,32 +339,37 @@ def skgemm_mxfp8_batched(Wq8, Wscale, X, C, T: int, N: int, K: int, split_k: int
 def skgemm_rmsnorm(X, R, G, R_out, Y, y_scale, T: int, H: int, eps: float, out_format="bf16", x_stride=None,
                    r_stride=None, r_out_stride=None, y_stride=None, stream=None) -> None:
     """Y = (X + R) / rms(X + R) * G as bf16, or as "i8" / "e4m3" codes with a
-    scale for each row; R_out = bf16(X + R). R, G and R_out may be None."""
+    scale for each row; R_out = bf16(X + R). R, G and R_out may be None. X, R, G
+    and R_out are bfloat16, y_scale float32, Y bfloat16, for "i8" int8 or uint8,
+    for "e4m3" float8_e4m3fn or uint8."""
     f = _format(out_format)
+    ty = _types()
+    bf16 = ty["bf16"]
     ysize = 2 if f == 0 else 1
-    x, xs = _rows(X, T, 2 * H, x_stride, "X", 2)
-    r, rs = _rows(R, T, 2 * H, r_stride, "R", 2)
-    ro, ros = _rows(R_out, T, 2 * H, r_out_stride, "R_out", 2)
-    y, ys = _rows(Y, T, ysize * H, y_stride, "Y", ysize)
-    code = lib().skgemm_rmsnorm(x, r, _ptr(G, 2 * _n(H), "G"), ro, y, _ptr(y_scale, 4 * _n(T), "y_scale"), T, H, eps, f,
-                                xs, rs, ros, ys, _stream(stream))
+    x, xs = _rows(X, T, 2 * H, x_stride, "X", bf16)
+    r, rs = _rows(R, T, 2 * H, r_stride, "R", bf16)
+    ro, ros = _rows(R_out, T, 2 * H, r_out_stride, "R_out", bf16)
+    y, ys = _rows(Y, T, ysize * H, y_stride, "Y", bf16 if f == 0 else ty["i8_out"] if f == 1 else ty["e4m3_out"])
+    code = lib().skgemm_rmsnorm(x, r, _ptr(G, 2 * _n(H), "G", bf16), ro, y, _ptr(y_scale, 4 * _n(T), "y_scale", ty["f32"]),
+                                T, H, eps, f, xs, rs, ros, ys, _stream(stream))
     _check(code, "skgemm_rmsnorm")
 
 
 def skgemm_i8(Wq, w_scale, Xq, x_scale, C, T: int, N: int, K: int, out_format=None, w_stride=None, x_stride=None,
               c_stride=None, stream=None) -> None:
     """C[t, n] = x_scale[t] * w_scale[n] * (Xq . Wq^T)[t, n] with exact integer
-    sums; C is bf16 or float (out_format "bf16" / "f32"; None: as C's elements
-    are, bf16 for an address)."""
+    sums of int8 codes and float32 scales; C is bfloat16 or float32 (out_format
+    "bf16" / "f32"; None: as C's elements are, bf16 for an address)."""
     if out_format is None:
         out_format = 3 if not isinstance(C, int) and C is not None and C.element_size() == 4 else 0
     f = _format(out_format)
+    ty = _types()
     size = 4 if f == 3 else 2
-    w, ws = _rows(Wq, N, K, w_stride, "Wq", 1)
-    x, xs = _rows(Xq, T, K, x_stride, "Xq", 1)
-    c, cs = _rows(C, T, size * N, c_stride, "C", size)
-    code = lib().skgemm_i8(w, _ptr(w_scale, 4 * _n(N), "w_scale"), x, _ptr(x_scale, 4 * _n(T), "x_scale"), c, T, N, K, f,
-                           ws, xs, cs, _stream(stream))
+    w, ws = _rows(Wq, N, K, w_stride, "Wq", ty["i8"])
+    x, xs = _rows(Xq, T, K, x_stride, "Xq", ty["i8"])
+    c, cs = _rows(C, T, size * N, c_stride, "C", ty["f32"] if f == 3 else ty["bf16"])
+    code = lib().skgemm_i8(w, _ptr(w_scale, 4 * _n(N), "w_scale", ty["f32"]), x, _ptr(x_scale, 4 * _n(T), "x_scale", ty["f32"]),
+                           c, T, N, K, f, ws, xs, cs, _stream(stream))
     _check(code, "skgemm_i8")
 
 
@@ -359,30 +383,38 @@ def skgemm_logprobs(logits, tokens, logprob, entropy, lse, top_logprob, top_ids,
                     scale: float = 1.0, logits_format=None, stride=None, stream=None) -> None:
     """Of each row of scale * logits: the log probability of its token, the
     entropy, the log of the sum of exponentials, and the top_k best tokens with
-    their log probabilities. Outputs may be None; tokens and ids are int64.
-    logits_format "bf16" / "f32" (None: as the elements are, bf16 for an address)."""
+    their log probabilities. Outputs may be None and are float32; tokens and ids
+    are int64. logits are bfloat16 or float32 (logits_format "bf16" / "f32";
+    None: as the elements are, bf16 for an address)."""
     f = _logits_format(logits, logits_format)
+    ty = _types()
+    f32, i64 = ty["f32"], ty["i64"]
     size = 4 if f == 3 else 2
-    z, zs = _rows(logits, T, size * V, stride, "logits", size)
-    code = lib().skgemm_logprobs(z, _ptr(tokens, 8 * _n(T), "tokens"), _ptr(logprob, 4 * _n(T), "logprob"),
-                                 _ptr(entropy, 4 * _n(T), "entropy"), _ptr(lse, 4 * _n(T), "lse"),
-                                 _ptr(top_logprob, 4 * _n(T, top_k), "top_logprob"),
-                                 _ptr(top_ids, 8 * _n(T, top_k), "top_ids"), T, V, top_k, scale, f, zs, _stream(stream))
+    z, zs = _rows(logits, T, size * V, stride, "logits", f32 if f == 3 else ty["bf16"])
+    code = lib().skgemm_logprobs(z, _ptr(tokens, 8 * _n(T), "tokens", i64), _ptr(logprob, 4 * _n(T), "logprob", f32),
+                                 _ptr(entropy, 4 * _n(T), "entropy", f32), _ptr(lse, 4 * _n(T), "lse", f32),
+                                 _ptr(top_logprob, 4 * _n(T, top_k), "top_logprob", f32),
+                                 _ptr(top_ids, 8 * _n(T, top_k), "top_ids", i64), T, V, top_k, scale, f, zs,
+                                 _stream(stream))
     _check(code, "skgemm_logprobs")
 
 
 def skgemm_logprobs_grad(logits, tokens, lse, entropy, g_logprob, g_entropy, d_logits, T: int, V: int,
                          scale: float = 1.0, logits_format=None, stride=None, d_stride=None, stream=None) -> None:
     """The gradient of sum(g_logprob * logprob) + sum(g_entropy * entropy) to the
-    logits, from the lse and entropy that skgemm_logprobs gave; d_logits may be
-    the logits themselves. g_logprob or g_entropy may be None (zeros)."""
+    logits, from the lse and entropy that skgemm_logprobs gave; d_logits has the
+    logits' type and may be the logits themselves. g_logprob or g_entropy may be
+    None (zeros); they, lse and entropy are float32, tokens int64."""
     f = _logits_format(logits, logits_format)
+    ty = _types()
+    f32 = ty["f32"]
     size = 4 if f == 3 else 2
-    z, zs = _rows(logits, T, size * V, stride, "logits", size)
-    d, ds = _rows(d_logits, T, size * V, d_stride, "d_logits", size)
-    code = lib().skgemm_logprobs_grad(z, _ptr(tokens, 8 * _n(T), "tokens"), _ptr(lse, 4 * _n(T), "lse"),
-                                      _ptr(entropy, 4 * _n(T), "entropy"), _ptr(g_logprob, 4 * _n(T), "g_logprob"),
-                                      _ptr(g_entropy, 4 * _n(T), "g_entropy"), d, T, V, scale, f, zs, ds, _stream(stream))
+    z, zs = _rows(logits, T, size * V, stride, "logits", f32 if f == 3 else ty["bf16"])
+    d, ds = _rows(d_logits, T, size * V, d_stride, "d_logits", f32 if f == 3 else ty["bf16"])
+    code = lib().skgemm_logprobs_grad(z, _ptr(tokens, 8 * _n(T), "tokens", ty["i64"]), _ptr(lse, 4 * _n(T), "lse", f32),
+                                      _ptr(entropy, 4 * _n(T), "entropy", f32), _ptr(g_logprob, 4 * _n(T), "g_logprob", f32),
+                                      _ptr(g_entropy, 4 * _n(T), "g_entropy", f32), d, T, V, scale, f, zs, ds,
+                                      _stream(stream))
     _check(code, "skgemm_logprobs_grad")
 
 

@@ -1,0 +1,87 @@
+"""The operators' binding refuses tensors whose elements are of another type than
+the call's, also where the width is the same and the bytes would suffice."""
+
+import pytest
+
+import split_reduction_amd as sk
+from tests.gpu_util import DEV, torch
+
+A = 1 << 20  # an address; every call below is refused before any is used
+
+
+class OnGpu:
+    """A host tensor that says it is on the GPU: what the binding looks at."""
+
+    is_cuda = True
+
+    def __init__(self, a):
+        self.a = a
+
+    def __getattr__(self, name):
+        return getattr(self.a, name)
+
+
+def norm(Y=A, fmt="i8", **kw):
+    a = {"X": A, "R": A, "G": A, "R_out": A, "y_scale": A, **kw}
+    sk.skgemm_rmsnorm(a["X"], a["R"], a["G"], a["R_out"], Y, a["y_scale"], 4, 64, 1e-6, fmt)
+
+
+def i8(fmt=None, **kw):
+    a = {"Wq": A, "w_scale": A, "Xq": A, "x_scale": A, "C": A, **kw}
+    sk.skgemm_i8(a["Wq"], a["w_scale"], a["Xq"], a["x_scale"], a["C"], 4, 64, 64, fmt)
+
+
+def logprobs(fmt=None, **kw):
+    names = ("logits", "tokens", "logprob", "entropy", "lse", "top_logprob", "top_ids")
+    sk.skgemm_logprobs(*[({n: A for n in names} | kw)[n] for n in names], 4, 64, 16, logits_format=fmt)
+
+
+def grad(fmt=None, **kw):
+    names = ("logits", "tokens", "lse", "entropy", "g_logprob", "g_entropy", "d_logits")
+    sk.skgemm_logprobs_grad(*[({n: A for n in names} | kw)[n] for n in names], 4, 64, logits_format=fmt)
+
+
+# (call, argument, the wrong element type, arguments beside it)
+WRONG = [
+    *[(norm, n, ty, {}) for n in ("X", "R", "G", "R_out") for ty in ("float16", "int16", "float32")],
+    *[(norm, "Y", ty, {"fmt": f}) for f, tys in (("bf16", ("float16", "int16", "uint8")), ("i8", ("float8_e4m3fn", "bfloat16")),
+                                                 ("e4m3", ("int8", "float8_e5m2", "bfloat16"))) for ty in tys],
+    *[(norm, "y_scale", ty, {}) for ty in ("float64", "int32", "bfloat16")],
+    *[(i8, n, ty, {}) for n in ("Wq", "Xq") for ty in ("uint8", "float8_e4m3fn", "bfloat16")],
+    *[(i8, n, ty, {}) for n in ("w_scale", "x_scale") for ty in ("float64", "int32")],
+    *[(i8, "C", ty, {"fmt": f}) for ty in ("float16", "int32", "float64") for f in (None, "bf16", "f32")],
+    (i8, "C", "float32", {"fmt": "bf16"}), (i8, "C", "bfloat16", {"fmt": "f32"}),
+    *[(c, "logits", ty, {"fmt": f}) for c in (logprobs, grad) for ty in ("float16", "int32", "float64") for f in (None, "bf16", "f32")],
+    *[(c, "tokens", ty, {}) for c in (logprobs, grad) for ty in ("int32", "float64")],
+    *[(logprobs, n, ty, {}) for n in ("logprob", "entropy", "lse", "top_logprob") for ty in ("float64", "int32")],
+    (logprobs, "top_ids", "float64", {}), (logprobs, "top_ids", "int32", {}),
+    *[(grad, n, ty, {}) for n in ("lse", "entropy", "g_logprob", "g_entropy") for ty in ("float64", "int32")],
+    (grad, "d_logits", "float16", {}), (grad, "d_logits", "float32", {}), (grad, "d_logits", "bfloat16", {"fmt": "f32"}),
+]
+
+
+@pytest.mark.parametrize("call,name,ty,more", WRONG)
+def test_other_element_types_refused(call, name, ty, more):
+    t = torch()
+    a = t.zeros(4 * 64 * 8, dtype=t.uint8).view(getattr(t, ty)).view(4, -1)[:, :64].contiguous()  # bytes enough for each argument
+    with pytest.raises(sk.SkgemmError) as e:
+        call(**{name: OnGpu(a)}, **more)
+    assert e.value.code == sk.SKGEMM_EINVAL and f"{name}: elements of torch.{ty}" in str(e.value), str(e.value)
+
+
+@pytest.mark.gpu
+def test_other_element_types_refused_on_the_gpu():
+    """With whole buffers, of the same width as the call's."""
+    t = torch()
+    new = lambda *s, ty=t.float32: t.zeros(*s, dtype=ty, device=DEV)  # noqa: E731
+    half, x, y, f = new(4, 64, ty=t.float16), new(4, 64, ty=t.bfloat16), new(4, 64, ty=t.int8), new(64)
+    w, tok = new(64, 64, ty=t.int8), new(4, ty=t.int64)
+    for call in (lambda: sk.skgemm_rmsnorm(half, None, None, None, y, f, 4, 64, 1e-6, "i8"),
+                 lambda: sk.skgemm_rmsnorm(x, None, None, None, y, f, 4, 64, 1e-6, "e4m3"),
+                 lambda: sk.skgemm_i8(w, f, y.view(t.float8_e4m3fn), f, x, 4, 64, 64),
+                 lambda: sk.skgemm_i8(w, f, y, f, half, 4, 64, 64),
+                 lambda: sk.skgemm_logprobs(half, tok, f, f, f, None, None, 4, 64),
+                 lambda: sk.skgemm_logprobs_grad(half, tok, f, f, f, f, half, 4, 64)):
+        with pytest.raises(sk.SkgemmError) as e:
+            call()
+        assert e.value.code == sk.SKGEMM_EINVAL and "elements of" in str(e.value)
