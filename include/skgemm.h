@@ -243,7 +243,8 @@ enum skgemm_format {
  *   Y = bf16(y), or the codes of y / y_scale[t] with y_scale[t] = max|y| / 127
  *   (I8, rounded to nearest even) or max|y| / 448 (E4M3).
  *   X, R, R_out  bf16 [T, H]; R null: h = X; R_out null: not stored. R_out may
- *                be X or R (same stride); other overlaps are not supported.
+ *                be X or R (same stride, else SKGEMM_EINVAL); other overlaps are
+ *                not supported.
  *   G            bf16 [H], null for ones.
  *   Y            bf16, int8 or uint8 [T, H]; y_scale float [T] (8-bit formats).
  *   H % 8 == 0, H <= SKGEMM_MAX_H (SKGEMM_ESHAPE); 1e-30 <= eps < inf.

@@ -120,6 +120,9 @@ SKGEMM_API int skgemm_rmsnorm(const void* X, const void* R, const void* G, void*
       return SKGEMM_EALIGN;
     // Inputs may share rows (stride 0); outputs must not overlap.
     if (y_stride < y_row || (R_out != nullptr && r_out_stride < row)) return SKGEMM_EINVAL;
+    // On top of an input, another stride would overwrite rows that other workgroups read.
+    if (R_out != nullptr && ((R_out == X && r_out_stride != x_stride) || (R_out == R && r_out_stride != r_stride)))
+      return SKGEMM_EINVAL;
   }
   skg::NormParams p{};
   p.x = static_cast<const uint8_t*>(X);

@@ -1,5 +1,7 @@
-"""The operators' binding refuses tensors whose elements are of another type than
-the call's, also where the width is the same and the bytes would suffice."""
+"""What the operators' entry points refuse beside the contracts of each call: in
+the binding, tensors whose elements are of another type than the call's, also where
+the width is the same and the bytes would suffice; in the C ABI, outputs on top of
+inputs that other rows are still to be read from."""
 
 import pytest
 
@@ -85,3 +87,15 @@ def test_other_element_types_refused_on_the_gpu():
         with pytest.raises(sk.SkgemmError) as e:
             call()
         assert e.value.code == sk.SKGEMM_EINVAL and "elements of" in str(e.value)
+
+
+def test_rmsnorm_sum_on_an_input_needs_its_stride():
+    """Refused before any device work: the addresses are made up."""
+    X, R, far = A, 1 << 24, 1 << 26
+
+    def call(R_out, x_stride, r_stride, r_out_stride, r=R, T=3):
+        return sk.lib().skgemm_rmsnorm(X, r, None, R_out, far, far, T, 64, 1e-6, 1, x_stride, r_stride, r_out_stride, 64, None)
+
+    assert call(X, 0, 128, 128) == call(X, 256, 128, 128) == call(X, 128, 128, 256) == sk.SKGEMM_EINVAL
+    assert call(R, 128, 0, 128) == call(R, 128, 256, 128) == call(R, 128, 128, 256) == sk.SKGEMM_EINVAL
+    assert call(X, 256, 128, 128, r=None) == sk.SKGEMM_EINVAL
