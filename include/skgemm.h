@@ -36,7 +36,9 @@
  *
  * Concurrency: calls on one stream are ordered by the stream. Each
  * (device, stream) pair owns its own split-K workspace, so calls on different
- * streams do not share partial buffers.
+ * streams do not share partial buffers. hipStreamPerThread counts as a stream of
+ * each thread that passes it; what such a thread leaves at its end is freed by
+ * skgemm_release.
  */
 #ifndef SKGEMM_H
 #define SKGEMM_H

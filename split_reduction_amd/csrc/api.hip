@@ -80,7 +80,7 @@ struct Workspace {
 };
 
 std::mutex g_ws_mu;
-std::map<std::pair<int, hipStream_t>, Workspace> g_ws;
+std::map<skg::StreamKey, Workspace> g_ws;
 // Workspaces replaced by larger ones, kept until skgemm_release: a HIP graph
 // captured earlier still names their addresses in its kernel arguments, so
 // freeing them would let a later replay write into memory handed out again.
@@ -91,11 +91,11 @@ std::vector<std::pair<int, Workspace>> g_retired;
 // ones (kept allocated until skgemm_release); under graph capture it refuses
 // instead.
 int ensure_workspace(hipStream_t stream, size_t part_bytes, size_t cnt_count, Workspace* out) {
-  int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
+  skg::StreamKey key;
+  hipError_t e = skg::stream_key(stream, &key);
   if (e != hipSuccess) return hip_fail(e);
   std::lock_guard<std::mutex> lock(g_ws_mu);
-  Workspace& w = g_ws[std::make_pair(dev, stream)];
+  Workspace& w = g_ws[key];
   // A new entry holds nothing yet (a call asking for no bytes still needs the
   // counter, health and synchronisation words).
   if (w.cnt != nullptr && w.part_bytes >= part_bytes && w.cnt_count >= cnt_count) {
@@ -124,7 +124,7 @@ int ensure_workspace(hipStream_t stream, size_t part_bytes, size_t cnt_count, Wo
     (void)hipFree(nw.cnt);
     return hip_fail(e);
   }
-  if (w.part != nullptr || w.cnt != nullptr) g_retired.emplace_back(dev, w);
+  if (w.part != nullptr || w.cnt != nullptr) g_retired.emplace_back(std::get<0>(key), w);
   w = nw;
   *out = w;
   return SKGEMM_OK;
@@ -294,6 +294,15 @@ int noalloc_workspace(hipStream_t stream, Workspace* out) {
 int skg::hip_fail(hipError_t e) {
   g_last_hip_error = (int)e;
   return SKGEMM_EHIP;
+}
+
+hipError_t skg::stream_key(hipStream_t stream, StreamKey* key) {
+  static std::atomic<uint64_t> threads{0};
+  static thread_local const uint64_t thread = ++threads;
+  int dev = 0;
+  const hipError_t e = hipGetDevice(&dev);
+  *key = StreamKey(dev, stream, stream == hipStreamPerThread ? thread : 0);
+  return e;
 }
 
 // Compute units of the current device (the owner wait is used only while the
@@ -466,7 +475,7 @@ SKGEMM_API int skgemm_release(void) {
   int caller_dev = -1;
   if (hipGetDevice(&caller_dev) != hipSuccess) caller_dev = -1;
   std::vector<std::pair<int, Workspace>> all(g_retired.begin(), g_retired.end());
-  for (auto& kv : g_ws) all.emplace_back(kv.first.first, kv.second);
+  for (auto& kv : g_ws) all.emplace_back(std::get<0>(kv.first), kv.second);
   for (auto& dw : all) {
     hipError_t e = hipSetDevice(dw.first);
     if (e == hipSuccess) e = hipDeviceSynchronize();
@@ -564,13 +573,13 @@ SKGEMM_API int skgemm_set_timeline(void* buf, size_t capacity) {
 SKGEMM_API int skgemm_health(uint32_t* words, size_t n_words, hipStream_t stream) {
   if (words == nullptr && n_words > 0) return SKGEMM_EINVAL;
   for (size_t i = 0; i < n_words; ++i) words[i] = 0;
-  int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
+  skg::StreamKey key;
+  hipError_t e = skg::stream_key(stream, &key);
   if (e != hipSuccess) return hip_fail(e);
   Workspace w;
   {
     std::lock_guard<std::mutex> lock(g_ws_mu);
-    auto it = g_ws.find(std::make_pair(dev, stream));
+    auto it = g_ws.find(key);
     if (it == g_ws.end() || it->second.cnt == nullptr) return SKGEMM_OK;  // nothing ran yet
     w = it->second;
   }

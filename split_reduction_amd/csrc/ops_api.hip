@@ -6,19 +6,19 @@
 
 #include <map>
 #include <mutex>
-#include <utility>
 
 #include "ops_internal.h"
 #include "skgemm.h"
+#include "skgemm_internal.h"
 
 namespace {
 
 bool aligned(const void* p, uintptr_t n) { return (uintptr_t)p % n == 0; }
 
-// ---- workspace: one of a fixed size per (device, stream) -------------------
+// ---- workspace: one of a fixed size per (device, stream), skg::StreamKey ----
 
 std::mutex g_mu;
-std::map<std::pair<int, hipStream_t>, uint8_t*> g_work;
+std::map<skg::StreamKey, uint8_t*> g_work;
 
 static_assert(skg::kOpsPartBytes + (size_t)skg::kOpsCounters * skg::kOpsCounterStride * 4 <= SKGEMM_OPS_WORKSPACE_BYTES,
               "partial results and counters fit");
@@ -27,11 +27,11 @@ static_assert(skg::kOpsPartBytes + (size_t)skg::kOpsCounters * skg::kOpsCounterS
 // It never grows or moves, so graphs captured with it stay valid until
 // skgemm_release. Under capture nothing can be allocated.
 int ops_workspace(hipStream_t stream, uint8_t** out) {
-  int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
+  skg::StreamKey key;
+  hipError_t e = skg::stream_key(stream, &key);
   if (e != hipSuccess) return skg::hip_fail(e);
   std::lock_guard<std::mutex> lock(g_mu);
-  auto it = g_work.find(std::make_pair(dev, stream));
+  auto it = g_work.find(key);
   if (it != g_work.end()) {
     *out = it->second;
     return SKGEMM_OK;
@@ -49,7 +49,7 @@ int ops_workspace(hipStream_t stream, uint8_t** out) {
     return skg::hip_fail(e);
   }
   try {
-    g_work[std::make_pair(dev, stream)] = static_cast<uint8_t*>(p);
+    g_work[key] = static_cast<uint8_t*>(p);
   } catch (...) {  // no exception leaves a C entry
     (void)hipFree(p);
     return SKGEMM_ENOMEM;
@@ -78,7 +78,7 @@ int skg::release_ops_workspaces() {
   int rc = SKGEMM_OK, caller_dev = -1;
   if (hipGetDevice(&caller_dev) != hipSuccess) caller_dev = -1;
   for (auto& kv : g_work) {
-    hipError_t e = hipSetDevice(kv.first.first);
+    hipError_t e = hipSetDevice(std::get<0>(kv.first));
     if (e == hipSuccess) e = hipDeviceSynchronize();
     if (e != hipSuccess) rc = hip_fail(e);
     (void)hipFree(kv.second);

@@ -4,7 +4,16 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <tuple>
+
 namespace skg {
+
+// What a workspace belongs to: the current device and a stream, as (device,
+// handle, thread). hipStreamPerThread is one handle for a stream of each host
+// thread, so there the calling thread counts too, by a number that no other
+// thread ever gets (0 for every other handle).
+typedef std::tuple<int, hipStream_t, uint64_t> StreamKey;
+hipError_t stream_key(hipStream_t stream, StreamKey* key);
 
 // Launch parameters of one split-K GEMM launch over at most 128 token rows.
 struct GemmParams {
