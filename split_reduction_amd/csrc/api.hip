@@ -119,6 +119,8 @@ int ensure_workspace(hipStream_t stream, size_t part_bytes, size_t cnt_count, Wo
   // Partials start zeroed: a mailbox tag is never 0, so no slot of a new
   // workspace can hold a value that passes for this launch's.
   if (e == hipSuccess) e = hipMemsetAsync(nw.part, 0, nw.part_bytes, stream);
+  // Waited for: a graph captured on this stream may be replayed on another.
+  if (e == hipSuccess) e = hipStreamSynchronize(stream);
   if (e != hipSuccess) {
     (void)hipFree(nw.part);
     (void)hipFree(nw.cnt);

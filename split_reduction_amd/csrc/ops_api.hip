@@ -23,8 +23,9 @@ std::map<skg::StreamKey, uint8_t*> g_work;
 static_assert(skg::kOpsPartBytes + (size_t)skg::kOpsCounters * skg::kOpsCounterStride * 4 <= SKGEMM_OPS_WORKSPACE_BYTES,
               "partial results and counters fit");
 
-// The stream's workspace, allocated and its counters zeroed on the first call.
-// It never grows or moves, so graphs captured with it stay valid until
+// The stream's workspace, allocated and its counters zeroed on the first call,
+// which waits for that: a graph captured on this stream may be replayed on
+// another. It never grows or moves, so graphs captured with it stay valid until
 // skgemm_release. Under capture nothing can be allocated.
 int ops_workspace(hipStream_t stream, uint8_t** out) {
   skg::StreamKey key;
@@ -44,6 +45,7 @@ int ops_workspace(hipStream_t stream, uint8_t** out) {
   if (hipMalloc(&p, SKGEMM_OPS_WORKSPACE_BYTES) != hipSuccess) return SKGEMM_ENOMEM;
   e = hipMemsetAsync(static_cast<uint8_t*>(p) + skg::kOpsPartBytes, 0, (size_t)skg::kOpsCounters * skg::kOpsCounterStride * 4,
                      stream);
+  if (e == hipSuccess) e = hipStreamSynchronize(stream);
   if (e != hipSuccess) {
     (void)hipFree(p);
     return skg::hip_fail(e);

@@ -78,3 +78,44 @@ def test_negative_stride_refused():
         with pytest.raises(sk.SkgemmError) as e:
             f()
         assert e.value.code == sk.SKGEMM_EINVAL
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("reserve", [sk.skgemm_reserve_ops, lambda s: sk.skgemm_reserve(64, 4096, 4, s)])
+def test_reserve_has_cleared_the_workspace(reserve):
+    """A reserve on a busy stream returns with the workspace's counters cleared:
+    what is captured there may be replayed on a stream that waits for nothing."""
+    t = torch()
+    sk.skgemm_release()
+    s = t.cuda.Stream()
+    t.cuda.synchronize()
+    with t.cuda.stream(s):
+        t.cuda._sleep(100_000_000)  # tens of milliseconds
+    assert not s.query()
+    reserve(s)
+    assert s.query()
+    sk.skgemm_release()
+
+
+@pytest.mark.gpu
+def test_replay_on_another_stream():
+    t = torch()
+    T, V, k = 1, 100000, 4
+    Z = t.randn(T, V, device=DEV)
+    out = [t.zeros(T, device=DEV), t.zeros(T, device=DEV), t.zeros(T, k, device=DEV), t.zeros(T, k, dtype=t.int64, device=DEV)]
+    sk.skgemm_release()
+    s, s2 = t.cuda.Stream(), t.cuda.Stream()
+    t.cuda.synchronize()
+    with t.cuda.stream(s):
+        t.cuda._sleep(50_000_000)
+    sk.skgemm_reserve_ops(s)
+    g = t.cuda.CUDAGraph()
+    with t.cuda.graph(g, stream=s):
+        call(Z, out, T, V, k, s)
+    with t.cuda.stream(s2):
+        for _ in range(3):
+            g.replay()
+    t.cuda.synchronize()
+    assert t.equal(out[3][0], t.topk(Z[0], k).indices)
+    del g
+    sk.skgemm_release()
