@@ -109,9 +109,13 @@ int ensure_workspace(hipStream_t stream, size_t part_bytes, size_t cnt_count, Wo
   Workspace nw;
   nw.part_bytes = std::max(part_bytes, (size_t)256);
   nw.cnt_count = std::max(cnt_count, (size_t)64);
-  if (hipMalloc((void**)&nw.part, nw.part_bytes) != hipSuccess) return SKGEMM_ENOMEM;
+  if (hipMalloc((void**)&nw.part, nw.part_bytes) != hipSuccess) {
+    (void)hipGetLastError();  // reported by the return code
+    return SKGEMM_ENOMEM;
+  }
   const size_t words = nw.cnt_count + skg::kHealthWords + skg::kSyncWords;
   if (hipMalloc((void**)&nw.cnt, words * sizeof(uint32_t)) != hipSuccess) {
+    (void)hipGetLastError();
     (void)hipFree(nw.part);
     return SKGEMM_ENOMEM;
   }
@@ -293,7 +297,10 @@ int noalloc_workspace(hipStream_t stream, Workspace* out) {
 
 }  // namespace
 
+// The error is kept for skgemm_last_hip_error and taken from HIP's own record,
+// where the caller's next check of a launch would find it.
 int skg::hip_fail(hipError_t e) {
+  (void)hipGetLastError();
   g_last_hip_error = (int)e;
   return SKGEMM_EHIP;
 }

@@ -378,8 +378,7 @@ namespace {
 
 template <int NT, int F, int WT, int C, int WF>
 hipError_t launch_cluster_one(const Tactic& t, const GemmParams& p, hipStream_t s) {
-  hipLaunchKernelGGL((splitk_cluster_kernel<NT, F, WT, C, WF>), dim3(t.grid, p.L), dim3(t.threads), 0, s, p);
-  return hipGetLastError();
+  return launch(splitk_cluster_kernel<NT, F, WT, C, WF>, dim3(t.grid, p.L), dim3(t.threads), 0, s, p);
 }
 
 template <int NT, int F, int C, int WF>

@@ -1271,8 +1271,7 @@ hipError_t launch_one(const Tactic& t, const GemmParams& p, hipStream_t s) {
     return hipErrorInvalidValue;  // not built: pick_tactic never selects it
   } else {
     auto kern = splitk_gemm_kernel<NT, sh.rg, sh.wk, sh.wn, sh.d, sh.c, WF>;
-    hipLaunchKernelGGL(kern, dim3(t.grid, p.L), dim3(t.threads), t.lds, s, p);
-    return hipGetLastError();
+    return launch(kern, dim3(t.grid, p.L), dim3(t.threads), t.lds, s, p);
   }
 }
 
@@ -1394,8 +1393,7 @@ template <int NT, int SH, int WF>
 hipError_t launch_stream_one(const Tactic& t, const GemmParams& p, hipStream_t s) {
   constexpr StreamShape sh = kStreamShapes[SH];
   auto kern = splitk_stream_kernel<NT, sh.wk, sh.wn, stream_depth(sh, NT, WF), sh.c, sh.mode, WF>;
-  hipLaunchKernelGGL(kern, dim3(t.grid, p.L), dim3(t.threads), t.lds, s, p);
-  return hipGetLastError();
+  return launch(kern, dim3(t.grid, p.L), dim3(t.threads), t.lds, s, p);
 }
 
 template <int NT, int WF>

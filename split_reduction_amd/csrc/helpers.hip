@@ -90,22 +90,19 @@ hipError_t launch_zero16(void* p, size_t bytes, hipStream_t s) {
   const size_t n = bytes / 16;
   if (n == 0) return hipSuccess;
   const unsigned blocks = blocks_for(n, kThreads) < 1024u ? blocks_for(n, kThreads) : 1024u;
-  hipLaunchKernelGGL(zero16_kernel, dim3(blocks), dim3(kThreads), 0, s, static_cast<u32x4*>(p), n);
-  return hipGetLastError();
+  return launch(zero16_kernel, dim3(blocks), dim3(kThreads), 0, s, static_cast<u32x4*>(p), n);
 }
 
 hipError_t launch_pack_bf16(const float* in, uint32_t* out, size_t n, hipStream_t s) {
   if (n == 0) return hipSuccess;
-  hipLaunchKernelGGL(pack_bf16_kernel, dim3(blocks_for(n, kThreads)), dim3(kThreads), 0, s, in,
-                     out, n);
-  return hipGetLastError();
+  return launch(pack_bf16_kernel, dim3(blocks_for(n, kThreads)), dim3(kThreads), 0, s, in,
+                out, n);
 }
 
 hipError_t launch_pack_e4m3(const float* in, uint32_t* out, size_t n, hipStream_t s) {
   if (n == 0) return hipSuccess;
-  hipLaunchKernelGGL(pack_e4m3_kernel, dim3(blocks_for(n, kThreads)), dim3(kThreads), 0, s, in,
-                     out, n);
-  return hipGetLastError();
+  return launch(pack_e4m3_kernel, dim3(blocks_for(n, kThreads)), dim3(kThreads), 0, s, in,
+                out, n);
 }
 
 // Reference stream: every byte of src read once with coalesced 16-byte
@@ -139,36 +136,32 @@ __global__ __launch_bounds__(kReadProbeThreads) void read_probe_kernel(const u32
 
 hipError_t launch_read_probe(const void* src, size_t bytes, uint32_t* sink, hipStream_t s) {
   if (bytes < 16) return hipSuccess;
-  hipLaunchKernelGGL(read_probe_kernel, dim3(kReadProbeBlocks), dim3(kReadProbeThreads), 0, s,
-                     static_cast<const u32x4*>(src), bytes / 16, sink);
-  return hipGetLastError();
+  return launch(read_probe_kernel, dim3(kReadProbeBlocks), dim3(kReadProbeThreads), 0, s,
+                static_cast<const u32x4*>(src), bytes / 16, sink);
 }
 
 hipError_t launch_wave_sum(const float* in, float* out, size_t n_waves, hipStream_t s) {
   if (n_waves == 0) return hipSuccess;
-  hipLaunchKernelGGL(wave_sum_kernel, dim3(blocks_for(n_waves, kThreads / 64)), dim3(kThreads), 0,
-                     s, in, out, n_waves);
-  return hipGetLastError();
+  return launch(wave_sum_kernel, dim3(blocks_for(n_waves, kThreads / 64)), dim3(kThreads), 0,
+                s, in, out, n_waves);
 }
 
 hipError_t launch_mxfp4_dequant(const void* wq, const void* ws, void* out, int N, int K,
                                 hipStream_t s) {
   const size_t n = (size_t)N * (size_t)(K / 8);
   if (n == 0) return hipSuccess;
-  hipLaunchKernelGGL(mxfp4_dequant_kernel, dim3(blocks_for(n, kThreads)), dim3(kThreads), 0, s,
-                     static_cast<const uint32_t*>(wq), static_cast<const uint8_t*>(ws),
-                     static_cast<u32x4*>(out), N, K);
-  return hipGetLastError();
+  return launch(mxfp4_dequant_kernel, dim3(blocks_for(n, kThreads)), dim3(kThreads), 0, s,
+                static_cast<const uint32_t*>(wq), static_cast<const uint8_t*>(ws),
+                static_cast<u32x4*>(out), N, K);
 }
 
 hipError_t launch_mxfp8_dequant(const void* wq, const void* ws, void* out, int N, int K,
                                 hipStream_t s) {
   const size_t n = (size_t)N * (size_t)(K / 8);
   if (n == 0) return hipSuccess;
-  hipLaunchKernelGGL(mxfp8_dequant_kernel, dim3(blocks_for(n, kThreads)), dim3(kThreads), 0, s,
-                     static_cast<const u32x2*>(wq), static_cast<const uint8_t*>(ws),
-                     static_cast<u32x4*>(out), N, K);
-  return hipGetLastError();
+  return launch(mxfp8_dequant_kernel, dim3(blocks_for(n, kThreads)), dim3(kThreads), 0, s,
+                static_cast<const u32x2*>(wq), static_cast<const uint8_t*>(ws),
+                static_cast<u32x4*>(out), N, K);
 }
 
 }  // namespace skg

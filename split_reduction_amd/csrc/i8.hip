@@ -454,15 +454,13 @@ constexpr float kStart = 0.41f, kJoinRank = 0.222f;    // us
 constexpr float kWeights = 10.69e6f, kSums = 4.56e6f;  // bytes a us
 constexpr int kShapeCount = (int)(sizeof(kShapes) / sizeof(kShapes[0]));
 template <int BT, int BN, int WT, int WN, int STG>
-void launch_tile(const I8Params& p, int grid, hipStream_t s) {
-  hipLaunchKernelGGL((i8_tile_kernel<BT, BN, WT, WN, STG>), dim3((unsigned)grid), dim3(64 * WT * WN), 0, s, p);
+hipError_t launch_tile(const I8Params& p, int grid, hipStream_t s) {
+  return launch(i8_tile_kernel<BT, BN, WT, WN, STG>, dim3((unsigned)grid), dim3(64 * WT * WN), 0, s, p);
 }
 
-void launch_shape(int shape, const I8Params& p, int grid, hipStream_t s) {
+hipError_t launch_shape(int shape, const I8Params& p, int grid, hipStream_t s) {
   switch (shape) {
-    case 0:
-      hipLaunchKernelGGL(i8_big_kernel, dim3((unsigned)grid), dim3(512), 0, s, p);
-      return;
+    case 0: return launch(i8_big_kernel, dim3((unsigned)grid), dim3(512), 0, s, p);
     case 1: return launch_tile<256, 128, 4, 2, 3>(p, grid, s);
     case 2: return launch_tile<128, 128, 4, 2, 2>(p, grid, s);
     case 3: return launch_tile<128, 128, 2, 4, 4>(p, grid, s);
@@ -472,16 +470,16 @@ void launch_shape(int shape, const I8Params& p, int grid, hipStream_t s) {
 }
 
 template <int NT, bool LOW, int RG, int WAVES, int U>
-void launch_rows(const I8Params& p, hipStream_t s) {
+hipError_t launch_rows(const I8Params& p, hipStream_t s) {
   const int ntiles = (p.N + 16 * RG - 1) / (16 * RG), ttiles = (p.T + 16 * NT - 1) / (16 * NT);
-  hipLaunchKernelGGL((i8_rows_kernel<NT, LOW, RG, WAVES, U>), dim3((unsigned)(ntiles * ttiles)), dim3(64 * WAVES), 0, s, p);
+  return launch(i8_rows_kernel<NT, LOW, RG, WAVES, U>, dim3((unsigned)(ntiles * ttiles)), dim3(64 * WAVES), 0, s, p);
 }
 
 // Units in flight: one load round of a wave where K is short (the workgroups of
 // a CU hide each other's latency), seven from K = 4096 on. Measured with U = 1 /
 // U = 7: T=1 N=4096 K=1024 3.4 / 4.7 us, T=1 N=16384 K=1024 5.5 / 11.5 us; T=8
 // N=4096 K=7168 8.9 / 7.9 us, T=8 N=K=16384 60.8 / 51.3 us.
-void launch_rows_for(const I8Params& p, hipStream_t s) {
+hipError_t launch_rows_for(const I8Params& p, hipStream_t s) {
   if (p.K < 4096) {
     if (p.T <= 8) return launch_rows<1, true, 1, 8, 1>(p, s);
     return launch_rows<1, false, 1, 8, 1>(p, s);
@@ -538,12 +536,8 @@ hipError_t launch_i8(const I8Params& q, const I8Tactic& tac, hipStream_t s) {
   p.whole = tac.whole;
   const int per = p.out_f32 ? 16 : 8;  // bytes of four outputs
   p.c_quads = p.c_stride % per == 0;
-  if (tac.shape < 0) {
-    launch_rows_for(p, s);
-  } else {
-    launch_shape(tac.shape, p, tac.whole + (tac.tiles - tac.whole) * tac.S, s);
-  }
-  return hipGetLastError();
+  if (tac.shape < 0) return launch_rows_for(p, s);
+  return launch_shape(tac.shape, p, tac.whole + (tac.tiles - tac.whole) * tac.S, s);
 }
 
 }  // namespace skg

@@ -22,6 +22,7 @@
 #include "device/pack.h"
 #include "ops_internal.h"
 #include "skgemm.h"
+#include "skgemm_internal.h"
 
 namespace skg {
 
@@ -697,15 +698,9 @@ int logprob_parts(int T, int V, bool f32, int* per) {
 
 hipError_t launch_logprobs(const LogprobParams& p, bool f32, hipStream_t s) {
   const dim3 grid((unsigned)p.T * (unsigned)p.parts);
-  if (f32 && p.k > 0)
-    hipLaunchKernelGGL((logprobs_kernel<true, true>), grid, dim3(kThreads), 0, s, p);
-  else if (f32)
-    hipLaunchKernelGGL((logprobs_kernel<true, false>), grid, dim3(kThreads), 0, s, p);
-  else if (p.k > 0)
-    hipLaunchKernelGGL((logprobs_kernel<false, true>), grid, dim3(kThreads), 0, s, p);
-  else
-    hipLaunchKernelGGL((logprobs_kernel<false, false>), grid, dim3(kThreads), 0, s, p);
-  return hipGetLastError();
+  if (f32)
+    return launch(p.k > 0 ? logprobs_kernel<true, true> : logprobs_kernel<true, false>, grid, dim3(kThreads), 0, s, p);
+  return launch(p.k > 0 ? logprobs_kernel<false, true> : logprobs_kernel<false, false>, grid, dim3(kThreads), 0, s, p);
 }
 
 hipError_t launch_logprobs_grad(LogprobGradParams p, bool f32, hipStream_t s) {
@@ -714,11 +709,7 @@ hipError_t launch_logprobs_grad(LogprobGradParams p, bool f32, hipStream_t s) {
   const unsigned steps = ((unsigned)p.V / (f32 ? 4 : 8) + 2 + kThreads - 1) / kThreads;
   p.parts = std::max(1u, std::min(steps, 16384u / (unsigned)p.T));
   const dim3 grid((unsigned)p.T * p.parts);
-  if (f32)
-    hipLaunchKernelGGL(logprobs_grad_kernel<true>, grid, dim3(kThreads), 0, s, p);
-  else
-    hipLaunchKernelGGL(logprobs_grad_kernel<false>, grid, dim3(kThreads), 0, s, p);
-  return hipGetLastError();
+  return launch(f32 ? logprobs_grad_kernel<true> : logprobs_grad_kernel<false>, grid, dim3(kThreads), 0, s, p);
 }
 
 }  // namespace skg

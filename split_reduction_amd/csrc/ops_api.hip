@@ -42,7 +42,10 @@ int ops_workspace(hipStream_t stream, uint8_t** out) {
   if (e != hipSuccess) return skg::hip_fail(e);
   if (st != hipStreamCaptureStatusNone) return SKGEMM_ENOMEM;
   void* p = nullptr;
-  if (hipMalloc(&p, SKGEMM_OPS_WORKSPACE_BYTES) != hipSuccess) return SKGEMM_ENOMEM;
+  if (hipMalloc(&p, SKGEMM_OPS_WORKSPACE_BYTES) != hipSuccess) {
+    (void)hipGetLastError();  // reported by the return code
+    return SKGEMM_ENOMEM;
+  }
   e = hipMemsetAsync(static_cast<uint8_t*>(p) + skg::kOpsPartBytes, 0, (size_t)skg::kOpsCounters * skg::kOpsCounterStride * 4,
                      stream);
   if (e == hipSuccess) e = hipStreamSynchronize(stream);

@@ -18,6 +18,7 @@
 #include "device/pack.h"
 #include "ops_internal.h"
 #include "skgemm.h"
+#include "skgemm_internal.h"
 
 namespace skg {
 
@@ -170,15 +171,12 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormParams p) {
 }
 
 template <int VPT, bool STREAM>
-void launch_vpt(const NormParams& p, int out_format, hipStream_t s) {
+hipError_t launch_vpt(const NormParams& p, int out_format, hipStream_t s) {
   const int nv = p.H / 8;
   const dim3 grid((unsigned)p.T), block((unsigned)((((nv + VPT - 1) / VPT) + 63) / 64 * 64));
-  if (out_format == SKGEMM_BF16)
-    hipLaunchKernelGGL((rmsnorm_kernel<VPT, SKGEMM_BF16, STREAM>), grid, block, 0, s, p);
-  else if (out_format == SKGEMM_I8)
-    hipLaunchKernelGGL((rmsnorm_kernel<VPT, SKGEMM_I8, STREAM>), grid, block, 0, s, p);
-  else
-    hipLaunchKernelGGL((rmsnorm_kernel<VPT, SKGEMM_E4M3, STREAM>), grid, block, 0, s, p);
+  if (out_format == SKGEMM_BF16) return launch(rmsnorm_kernel<VPT, SKGEMM_BF16, STREAM>, grid, block, 0, s, p);
+  if (out_format == SKGEMM_I8) return launch(rmsnorm_kernel<VPT, SKGEMM_I8, STREAM>, grid, block, 0, s, p);
+  return launch(rmsnorm_kernel<VPT, SKGEMM_E4M3, STREAM>, grid, block, 0, s, p);
 }
 
 }  // namespace
@@ -193,12 +191,9 @@ hipError_t launch_rmsnorm(const NormParams& p, int out_format, hipStream_t s) {
   const int nv = p.H / 8;  // at most 4096
   const bool stream = (size_t)p.T * (size_t)p.H * 7 > ((size_t)256 << 20);
   const int vpt = nv > 2048 || (nv > 512 && p.T > 1024) ? 4 : nv > 1024 ? 2 : 1;
-  if (vpt == 4 && stream) launch_vpt<4, true>(p, out_format, s);
-  else if (vpt == 4) launch_vpt<4, false>(p, out_format, s);
-  else if (vpt == 2) launch_vpt<2, false>(p, out_format, s);  // T <= 1024: below 256 MB
-  else if (stream) launch_vpt<1, true>(p, out_format, s);
-  else launch_vpt<1, false>(p, out_format, s);
-  return hipGetLastError();
+  if (vpt == 4) return stream ? launch_vpt<4, true>(p, out_format, s) : launch_vpt<4, false>(p, out_format, s);
+  if (vpt == 2) return launch_vpt<2, false>(p, out_format, s);  // T <= 1024: below 256 MB
+  return stream ? launch_vpt<1, true>(p, out_format, s) : launch_vpt<1, false>(p, out_format, s);
 }
 
 }  // namespace skg

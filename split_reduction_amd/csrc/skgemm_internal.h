@@ -5,8 +5,18 @@
 #include <stdint.h>
 
 #include <tuple>
+#include <type_traits>
 
 namespace skg {
+
+// Enqueues kernel(p...) and returns the status of that launch alone:
+// hipGetLastError would also report, and clear, an error that the caller's own
+// earlier HIP calls left.
+template <class... P>
+hipError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t lds, hipStream_t s, std::type_identity_t<P>... p) {
+  void* args[] = {const_cast<void*>(static_cast<const volatile void*>(&p))...};
+  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, args, lds, s);
+}
 
 // What a workspace belongs to: the current device and a stream, as (device,
 // handle, thread). hipStreamPerThread is one handle for a stream of each host

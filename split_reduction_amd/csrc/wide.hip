@@ -450,8 +450,7 @@ namespace {
 
 template <int NT, int WF>
 hipError_t launch_wide_one(const Tactic& t, const GemmParams& p, hipStream_t s) {
-  hipLaunchKernelGGL((splitk_wide_kernel<NT, WF>), dim3(t.grid, p.L), dim3(t.threads), t.lds, s, p);
-  return hipGetLastError();
+  return launch(splitk_wide_kernel<NT, WF>, dim3(t.grid, p.L), dim3(t.threads), t.lds, s, p);
 }
 
 template <int WF>
