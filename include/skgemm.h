@@ -254,6 +254,8 @@ enum skgemm_format {
  *   8-bit Y strides multiples of 8 (SKGEMM_EALIGN).
  * A row of zeros has scale 0 and codes 0. A row that holds an infinity or a NaN
  * (in h) has NaN outputs: bf16 NaN, or a NaN scale whose codes mean nothing.
+ * By an infinity or a NaN in G, bf16 outputs are infinite or NaN where y is; a
+ * scale is infinite or NaN with them, and its codes mean nothing.
  * Finite rows of any size are right: the sum of squares is rescaled where
  * FP32 would overflow.
  */

@@ -94,7 +94,8 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormParams p) {
     for (int e = 0; e < 4; ++e) {
       hg[8 * i + 2 * e] = h[8 * i + 2 * e] * bf16_lo(gv[i][e]);
       hg[8 * i + 2 * e + 1] = h[8 * i + 2 * e + 1] * bf16_hi(gv[i][e]);
-      top = fmaxf(top, fmaxf(fabsf(hg[8 * i + 2 * e]), fabsf(hg[8 * i + 2 * e + 1])));
+      // NaN counts: a NaN in G (h's own are in ss) must not leave a finite scale.
+      top = max_or_nan(top, max_or_nan(fabsf(hg[8 * i + 2 * e]), fabsf(hg[8 * i + 2 * e + 1])));
     }
   block_sum_max(ss, top, part);
   float eps = p.eps;
@@ -124,7 +125,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormParams p) {
           const uint32_t w = gv[i][e >> 1];
           hg[8 * i + e] = a * ((e & 1) ? bf16_hi(w) : bf16_lo(w));
           ss = fmaf(a, a, ss);
-          top = fmaxf(top, fabsf(hg[8 * i + e]));
+          top = max_or_nan(top, fabsf(hg[8 * i + e]));
         }
       __syncthreads();
       block_sum_max(ss, top, part);

@@ -135,6 +135,34 @@ def test_rmsnorm_far_values(H, fmt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["bf16", "i8", "e4m3"])
+@pytest.mark.parametrize("H,T", [(64, 9), (7168, 9), (7168, 1100), (16384, 3)])
+@pytest.mark.parametrize("gain", [float("nan"), float("inf"), float("-inf")])
+def test_rmsnorm_gain_not_finite(H, T, gain, fmt):
+    """An element of G that is no number shows: in bf16 where it is, else in the
+    scale. Rows whose squares pass FP32's range, and a row with a zero there."""
+    t = torch()
+    x, r, g = rows(T, H, seed=2, spread=False)
+    at = H - 5
+    g[at] = gain
+    x[1], r[1] = x[1] * 1e30, 0
+    x[2, at] = r[2, at] = 0  # 0 * inf is NaN
+    log(f"rmsnorm gain {gain} T={T} H={H} {fmt}")
+    ro, y, ys = run(x, r, g, fmt)
+    nan = np.isnan(gain) | (f64(x)[:, at] + f64(r)[:, at] == 0)  # row 2, and where a sum happens to be 0
+    assert nan[2]
+    if fmt == "bf16":
+        got = f64(y)
+        _, want = O.rmsnorm_ref(f64(x), f64(r), np.where(np.arange(H) == at, 0.0, f64(g)), 1e-6)
+        rest = np.arange(H) != at
+        assert np.all(np.abs(got - want)[:, rest] <= np.abs(want)[:, rest] * (O.EPS_BF16 + 40 * ULP) + 2.0**-133)
+        got = got[:, at]
+    else:
+        got = ys.double().cpu().numpy()
+    assert np.isnan(got[nan]).all() and np.isinf(got[~nan]).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("fmt", ["i8", "bf16"])
 def test_rmsnorm_strides_in_place_and_stream(fmt):
     """Rows inside wider matrices, R_out on top of R, another stream."""
