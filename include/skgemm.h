@@ -256,8 +256,8 @@ enum skgemm_format {
  * (in h) has NaN outputs: bf16 NaN, or a NaN scale whose codes mean nothing.
  * By an infinity or a NaN in G, bf16 outputs are infinite or NaN where y is; a
  * scale is infinite or NaN with them, and its codes mean nothing.
- * Finite rows of any size are right: the sum of squares is rescaled where
- * FP32 would overflow.
+ * Finite rows of any size are right: a row is rescaled where its squares or its
+ * products h G would pass FP32's range. Products below 2^-126 lose digits.
  */
 SKGEMM_API int skgemm_rmsnorm(const void* X, const void* R, const void* G, void* R_out, void* Y,
                               float* y_scale, int T, int H, float eps, int out_format,

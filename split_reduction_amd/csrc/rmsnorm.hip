@@ -112,16 +112,17 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormParams p) {
     if (m == kInf) {
       ss = __builtin_nanf("");
     } else {
-      const float f = __uint_as_float((255u - (__float_as_uint(m) >> 23)) << 23);  // m * f lies in 2..4
-      eps *= f;
-      eps *= f;
+      // m * f / 4 lies in 1/2..1, so that the products with G stay in range; f
+      // alone does for every finite m, f / 4 would pass below FP32's normals.
+      const float f = __uint_as_float((255u - (__float_as_uint(m) >> 23)) << 23);
+      eps = eps * f * f * 0.0625f;
       ss = 0.0f;
       top = 0.0f;
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float a = h[8 * i + e] * f;
+          const float a = h[8 * i + e] * f * 0.25f;
           const uint32_t w = gv[i][e >> 1];
           hg[8 * i + e] = a * ((e & 1) ? bf16_hi(w) : bf16_lo(w));
           ss = fmaf(a, a, ss);
@@ -134,7 +135,10 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(NormParams p) {
   const float rstd = 1.0f / sqrtf(ss / (float)p.H + eps);  // NaN where the row holds a NaN or infinity
   float mul = rstd;
   if constexpr (OUT != SKGEMM_BF16) {
-    const float scale = rstd * top / top_code<OUT>();  // in this order: top alone may be near FP32's smallest
+    // The product first, as top alone may be near FP32's smallest; last where it
+    // would pass FP32's range and the scale does not.
+    float scale = rstd * top;
+    scale = scale < kInf ? scale / top_code<OUT>() : rstd * (top / top_code<OUT>());
     if (threadIdx.x == 0) p.y_scale[t] = scale;
     // 127 / top would pass FP32's range for a tiny top: such a row is lifted
     // by a power of two first (exact). Zero rows get zero codes.

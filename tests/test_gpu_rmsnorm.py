@@ -163,6 +163,25 @@ def test_rmsnorm_gain_not_finite(H, T, gain, fmt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["bf16", "i8", "e4m3"])
+@pytest.mark.parametrize("H", [64, 7168])
+def test_rmsnorm_far_gain(H, fmt):
+    """G near the type's largest value, where h G passes FP32's range and y does
+    not; for codes also a y that passes it and a scale that does not."""
+    t = torch()
+    rng = np.random.default_rng(H)
+    x = rng.uniform(0.55, 0.65, (4, H)) * rng.choice([-1, 1], (4, H))
+    x *= np.array([1, 1e10, 3e38, 1e-3])[:, None]
+    g = np.where(rng.random(H) < 0.5, 3e38 * rng.choice([-1, 1], H), rng.standard_normal(H))
+    g[3] = 3e38
+    if fmt != "bf16":
+        x[:2, 3] *= 3
+    x, g = (t.from_numpy(a).to(t.bfloat16) for a in (x, g))
+    log(f"rmsnorm far gain H={H} {fmt}")
+    check(x, None, g, *run(x, None, g, fmt), 1e-6, fmt)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("fmt", ["i8", "bf16"])
 def test_rmsnorm_strides_in_place_and_stream(fmt):
     """Rows inside wider matrices, R_out on top of R, another stream."""
