@@ -647,8 +647,9 @@ __global__ __launch_bounds__(kThreads) void logprobs_grad_kernel(LogprobGradPara
     row.load(j, x, 0.0f);
 #pragma unroll
     for (int e = 0; e < kE; ++e) {
-      // Past -1e30 the exponential is 0 either way; -inf would make 0 * inf.
-      const float lp = fmaxf(fmaf(x[e], p.scale, -ref) * kLog2e, -1e30f);
+      // Past -150 the exponential is 0; -inf would make 0 * inf of it, and so would
+      // a bound whose product with c1 passes FP32's range.
+      const float lp = fmaxf(fmaf(x[e], p.scale, -ref) * kLog2e, -1024.0f);
       x[e] = exp2_hw(lp) * fmaf(c1, lp, c0);
     }
     if ((unsigned)(hit_at - j * kE) < (unsigned)kE) {

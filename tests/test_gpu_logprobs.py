@@ -414,3 +414,34 @@ def test_logprobs_rows_of_many_nan(T, V, k, kind):
     for name, a in got.items():
         assert np.array_equal(a, a[np.arange(T) % 24], equal_nan=True), name
     check_forward(Z[:n], tok[rows][:n], k, 1.0, got={name: a[:n] for name, a in got.items()})
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("scale,weight", [(1.0, 3e9), (256.0, 1e7), (0.5, 1e30)])
+def test_logprobs_grad_large_weights(kind, scale, weight):
+    """Banned tokens, and tokens far below the best, under large weights of the
+    entropy: zeros, not 0 * inf. The bound is check_backward's."""
+    t = torch()
+    T, V = 5, 3001
+    z, tok = make(T, V, seed=3, banned=0.5)
+    z[1, 7:] = float(t.finfo(t.float32 if kind == "f32" else t.bfloat16).min)
+    z[2] = -np.inf
+    z[2, [4, 9]] = 1.0, 1.5
+    tok[1], tok[2] = 3, 4
+    Z = dev_logits(z, kind)
+    raw = Z.double().cpu().numpy()
+    with np.errstate(invalid="ignore", over="ignore"):
+        f = O.logprobs_ref(raw, tok, 0, scale)
+        lse, ent = f["lse"].astype(np.float32), f["entropy"].astype(np.float32)
+        g, gh = np.full(T, weight, np.float32), np.linspace(-weight, weight, T).astype(np.float32)
+        got = backward(Z, tok, lse, ent, g, gh, scale)
+        h, g, gh = (a.astype(np.float64) for a in (ent, g, gh))
+        want, p, lp = O.logprobs_grad_ref(raw, tok, lse.astype(np.float64), h, g, gh, scale)
+    parts = np.abs(g)[:, None] + np.abs(gh)[:, None] * (np.abs(h)[:, None] + np.abs(lp))
+    tol = U * scale * p * ((3 * np.abs(lp) + 4) * parts + 6 * parts) + 4 * U * scale * np.abs(g)[:, None] * (
+        np.arange(V) == tok[:, None]) + 1e-36 * scale * (1 + parts)
+    if kind == "bf16":
+        tol = tol * (1 + O.EPS_BF16) + O.EPS_BF16 * np.abs(want)
+    assert np.all(got[~np.isfinite(z)] == 0)
+    near(got, want, tol, "gradient")
