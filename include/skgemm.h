@@ -238,6 +238,7 @@ enum skgemm_format {
 #define SKGEMM_MAX_ROW_STRIDE ((size_t)1 << 22) /* skgemm_i8: W and X, bytes */
 #define SKGEMM_MAX_V (1 << 20)    /* skgemm_logprobs, skgemm_logprobs_grad */
 #define SKGEMM_MAX_TOP 64
+#define SKGEMM_MAX_SCALE 2e38f
 
 /*
  * skgemm_rmsnorm: h = X + R (in FP32, from here on unrounded), R_out = bf16(h),
@@ -294,8 +295,8 @@ SKGEMM_API int skgemm_i8(const void* Wq, const float* w_scale, const void* Xq, c
  *   marks padding: its logprob is 0. An index >= V gives a NaN logprob.
  *   logprob, entropy, lse float [T], each may be null. top_logprob float and
  *   top_ids int64 [T, top_k], 0 <= top_k <= min(V, SKGEMM_MAX_TOP).
- *   0 <= V <= SKGEMM_MAX_V; scale finite and > 0 (1 / temperature). Sums are
- *   FP32.
+ *   0 <= V <= SKGEMM_MAX_V; 0 < scale <= SKGEMM_MAX_SCALE (1 / temperature,
+ *   SKGEMM_EINVAL otherwise). Sums are FP32.
  * A logit of -inf is a banned token: probability 0, nothing added to the
  * entropy, logprob -inf. A row of nothing but -inf has lse -inf, entropy 0 and
  * logprobs -inf. A row with a NaN or +inf has NaN for every float output and

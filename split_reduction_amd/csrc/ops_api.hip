@@ -63,10 +63,13 @@ int ops_workspace(hipStream_t stream, uint8_t** out) {
   return SKGEMM_OK;
 }
 
+// The kernels work with scale / log 2.
+static_assert(SKGEMM_MAX_SCALE * 1.4426950408889634 < 3.4e38, "in FP32's range");
+
 // The logits' (or their gradient's) own arguments.
 int check_logits(const void* logits, int T, int V, float scale, int format, size_t stride) {
   if (T < 0 || V < 0 || (format != SKGEMM_BF16 && format != SKGEMM_F32)) return SKGEMM_EINVAL;
-  if (!(scale > 0.0f) || !(scale < INFINITY)) return SKGEMM_EINVAL;
+  if (!(scale > 0.0f) || !(scale <= SKGEMM_MAX_SCALE)) return SKGEMM_EINVAL;
   if (V > SKGEMM_MAX_V || T > SKGEMM_MAX_ROWS) return SKGEMM_ESHAPE;
   if (T == 0 || V == 0) return SKGEMM_OK;
   if (logits == nullptr) return SKGEMM_EINVAL;

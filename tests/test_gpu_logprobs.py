@@ -445,3 +445,26 @@ def test_logprobs_grad_large_weights(kind, scale, weight):
         tol = tol * (1 + O.EPS_BF16) + O.EPS_BF16 * np.abs(want)
     assert np.all(got[~np.isfinite(z)] == 0)
     near(got, want, tol, "gradient")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [1e10, 2e38])
+def test_logprobs_near_zero_temperature(kind, scale):
+    """All probability with the best token, shared where it is not alone."""
+    V = 3001
+    z, tok = make(4, V, seed=6)
+    z = np.round(z * 4) / 4  # apart by 1/4 or equal
+    z[1, [5, 900]] = z[1].max() + 1
+    tok[1] = 900
+    z[2] = 0.0
+    z[3, 1:] = -np.inf
+    tok[3] = 0
+    Z = dev_logits(z, kind)
+    got = forward(Z, tok, 3, scale)
+    n = (z == z.max(1, keepdims=True)).sum(1)
+    assert np.allclose(got["entropy"], np.log(n), rtol=1e-6, atol=0)
+    assert np.allclose(got["logprob"][1:], -np.log(n[1:]), rtol=1e-6, atol=0)
+    best = np.argsort(-z, axis=1, kind="stable")[:, :3]
+    assert np.array_equal(got["ids"], best)
+    assert np.allclose(got["top"][:, 0], -np.log(n), rtol=1e-6, atol=0)

@@ -99,3 +99,11 @@ def test_rmsnorm_sum_on_an_input_needs_its_stride():
     assert call(X, 0, 128, 128) == call(X, 256, 128, 128) == call(X, 128, 128, 256) == sk.SKGEMM_EINVAL
     assert call(R, 128, 0, 128) == call(R, 128, 256, 128) == call(R, 128, 128, 256) == sk.SKGEMM_EINVAL
     assert call(X, 256, 128, 128, r=None) == sk.SKGEMM_EINVAL
+
+
+def test_scale_past_the_kernels_range_refused():
+    """scale / log 2 has to be in FP32's range: beyond, every output was NaN."""
+    f, b = sk.lib().skgemm_logprobs, sk.lib().skgemm_logprobs_grad
+    for scale in (2.1e38, 3e38, 3.4e38):
+        assert f(A, A, A, A, A, A, A, 2, 32, 4, scale, 0, 64, None) == sk.SKGEMM_EINVAL
+        assert b(A, A, A, A, A, A, A << 1, 2, 32, scale, 0, 64, 64, None) == sk.SKGEMM_EINVAL
