@@ -297,6 +297,8 @@ SKGEMM_API int skgemm_i8(const void* Wq, const float* w_scale, const void* Xq, c
  *   top_ids int64 [T, top_k], 0 <= top_k <= min(V, SKGEMM_MAX_TOP).
  *   0 <= V <= SKGEMM_MAX_V; 0 < scale <= SKGEMM_MAX_SCALE (1 / temperature,
  *   SKGEMM_EINVAL otherwise). Sums are FP32.
+ * lse is infinite where scale * max passes FP32's range; the other outputs are
+ * right there, as they are built from differences to the row's largest logit.
  * A logit of -inf is a banned token: probability 0, nothing added to the
  * entropy, logprob -inf. A row of nothing but -inf has lse -inf, entropy 0 and
  * logprobs -inf. A row with a NaN or +inf has NaN for every float output and
@@ -317,7 +319,8 @@ SKGEMM_API int skgemm_logprobs(const void* logits, const int64_t* tokens, float*
  *   stride); other overlaps are not supported. g_logprob or g_entropy null:
  *   zeros (tokens null only with g_logprob null; entropy null only with
  *   g_entropy null). A padding row (token < 0) has no logprob term. Rows of
- *   nothing but -inf get zeros; a NaN lse gives a NaN row.
+ *   nothing but -inf (lse -inf) get zeros; a NaN lse gives a NaN row, and so
+ *   does +inf, which a finite row has where scale * max passes FP32's range.
  */
 SKGEMM_API int skgemm_logprobs_grad(const void* logits, const int64_t* tokens, const float* lse,
                                     const float* entropy, const float* g_logprob,

@@ -636,8 +636,9 @@ __global__ __launch_bounds__(kThreads) void logprobs_grad_kernel(LogprobGradPara
   const float gh = p.g_entropy != nullptr ? p.g_entropy[t] : 0.0f;
   const float ent = p.g_entropy != nullptr ? p.entropy[t] : 0.0f;
   const float ref = empty ? 0.0f : lse;
-  // The clamp below would swallow a NaN lse, so it goes into c0.
-  const float c0 = lse == lse ? -p.scale * (g + gh * ent) : lse, c1 = -p.scale * gh * kLn2;
+  // The clamp below would swallow a NaN lse, so it goes into c0; an lse of +inf
+  // (scale * max past FP32's range) says nothing about the probabilities either.
+  const float c0 = lse < kInf ? -p.scale * (g + gh * ent) : __builtin_nanf(""), c1 = -p.scale * gh * kLn2;
   const float hit = empty ? 0.0f : p.scale * g;
   const bool same = row.head == out.head;
   uint8_t* const base = p.d_logits + t * p.d_stride - (size_t)out.head * Row<F32>::kSize;

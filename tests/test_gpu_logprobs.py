@@ -468,3 +468,25 @@ def test_logprobs_near_zero_temperature(kind, scale):
     best = np.argsort(-z, axis=1, kind="stable")[:, :3]
     assert np.array_equal(got["ids"], best)
     assert np.allclose(got["top"][:, 0], -np.log(n), rtol=1e-6, atol=0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_logprobs_scaled_past_the_range(kind):
+    """scale * max past FP32's range: an infinite lse, the other outputs right. The
+    gradient has no probabilities to work with: NaN, or zeros where lse is -inf."""
+    t = torch()
+    V = 1000
+    z = np.zeros((2, V), np.float32)
+    z[0, :7], z[0, 7:] = 3e38, 1e38
+    z[1] = -3e38
+    tok = np.array([3, 8])
+    Z = dev_logits(z, kind)
+    got = forward(Z, tok, 2, 2.0)
+    n = np.array([7, V])
+    assert np.array_equal(got["lse"], [np.inf, -np.inf])
+    for a in (got["entropy"], -got["logprob"], -got["top"][:, 0], -got["top"][:, 1]):
+        assert np.allclose(a, np.log(n), rtol=1e-6, atol=0)
+    assert np.array_equal(got["ids"], [[0, 1], [0, 1]])
+    d = backward(Z, tok, got["lse"], got["entropy"], np.ones(2), np.ones(2), 2.0)
+    assert np.isnan(d[0]).all() and not d[1].any()
