@@ -132,9 +132,8 @@ def _types() -> dict:
     return _torch_types
 
 
-def _check_type(a, types, what: str) -> None:
-    if a.dtype not in types:
-        raise SkgemmError(SKGEMM_EINVAL, f"{what}: elements of {a.dtype}, the call takes {' or '.join(map(str, types))}")
+def _wrong_type(a, types, what: str) -> SkgemmError:
+    return SkgemmError(SKGEMM_EINVAL, f"{what}: elements of {a.dtype}, the call takes {' or '.join(map(str, types))}")
 
 
 def _ptr(a, nbytes: int = 0, what: str = "argument", types=None) -> int:
@@ -157,8 +156,8 @@ def _ptr(a, nbytes: int = 0, what: str = "argument", types=None) -> int:
         on_gpu = a.device.type == "cuda"
     if not on_gpu:
         raise SkgemmError(SKGEMM_EINVAL, f"{what}: a tensor on {a.device}, not on the GPU")
-    if types is not None:
-        _check_type(a, types, what)
+    if types is not None and a.dtype not in types:
+        raise _wrong_type(a, types, what)
     if not a.is_contiguous():
         raise SkgemmError(SKGEMM_EINVAL, f"{what}: not contiguous")
     have = a.numel() * a.element_size()
@@ -178,7 +177,8 @@ def _rows(a, rows: int, row_bytes: int, stride, what: str, types):
         return a or 0, row_bytes if stride is None else stride
     if not a.is_cuda:
         raise SkgemmError(SKGEMM_EINVAL, f"{what}: a tensor on {a.device}, not on the GPU")
-    _check_type(a, types, what)
+    if a.dtype not in types:
+        raise _wrong_type(a, types, what)
     size = a.element_size()
     if stride is None and a.numel() * size == rows * row_bytes and a.is_contiguous():
         return a.data_ptr(), row_bytes  # dense
@@ -343,7 +343,7 @@ def skgemm_rmsnorm(X, R, G, R_out, Y, y_scale, T: int, H: int, eps: float, out_f
     and R_out are bfloat16, y_scale float32, Y bfloat16, for "i8" int8 or uint8,
     for "e4m3" float8_e4m3fn or uint8."""
     f = _format(out_format)
-    ty = _types()
+    ty = _torch_types or _types()
     bf16 = ty["bf16"]
     ysize = 2 if f == 0 else 1
     x, xs = _rows(X, T, 2 * H, x_stride, "X", bf16)
@@ -363,7 +363,7 @@ def skgemm_i8(Wq, w_scale, Xq, x_scale, C, T: int, N: int, K: int, out_format=No
     if out_format is None:
         out_format = 3 if not isinstance(C, int) and C is not None and C.element_size() == 4 else 0
     f = _format(out_format)
-    ty = _types()
+    ty = _torch_types or _types()
     size = 4 if f == 3 else 2
     w, ws = _rows(Wq, N, K, w_stride, "Wq", ty["i8"])
     x, xs = _rows(Xq, T, K, x_stride, "Xq", ty["i8"])
@@ -387,7 +387,7 @@ def skgemm_logprobs(logits, tokens, logprob, entropy, lse, top_logprob, top_ids,
     are int64. logits are bfloat16 or float32 (logits_format "bf16" / "f32";
     None: as the elements are, bf16 for an address)."""
     f = _logits_format(logits, logits_format)
-    ty = _types()
+    ty = _torch_types or _types()
     f32, i64 = ty["f32"], ty["i64"]
     size = 4 if f == 3 else 2
     z, zs = _rows(logits, T, size * V, stride, "logits", f32 if f == 3 else ty["bf16"])
@@ -406,7 +406,7 @@ def skgemm_logprobs_grad(logits, tokens, lse, entropy, g_logprob, g_entropy, d_l
     logits' type and may be the logits themselves. g_logprob or g_entropy may be
     None (zeros); they, lse and entropy are float32, tokens int64."""
     f = _logits_format(logits, logits_format)
-    ty = _types()
+    ty = _torch_types or _types()
     f32 = ty["f32"]
     size = 4 if f == 3 else 2
     z, zs = _rows(logits, T, size * V, stride, "logits", f32 if f == 3 else ty["bf16"])
