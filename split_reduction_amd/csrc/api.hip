@@ -41,7 +41,6 @@ uint32_t owner_wait_ticks() { return (uint32_t)skg::knob(skg::kKnobOwnerWait, 10
 std::atomic<uint64_t*> g_stamps{nullptr};
 std::atomic<size_t> g_stamps_cap{0};
 
-using skg::device_cus;
 using skg::hip_fail;
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
@@ -141,6 +140,22 @@ size_t part_bytes_for(int T, int N, int S) {
 }
 // Arrival counters, one per 16 output rows, kCntStride words apart.
 size_t counters_for(int N) { return (size_t)N / 16 * skg::kCntStride; }
+
+// Compute units of the current device (the owner wait is used only while the
+// whole grid fits on them).
+int device_cus() {
+  static std::mutex mu;
+  static std::map<int, int> cache;
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  auto it = cache.find(dev);
+  if (it != cache.end()) return it->second;
+  int n = 0;
+  if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) n = 0;
+  cache[dev] = n;
+  return n;
+}
 
 // A batch of L problems of one shape; strides in bytes (problem l of W at
 // w + l * bw, and so on).
@@ -312,22 +327,6 @@ hipError_t skg::stream_key(hipStream_t stream, StreamKey* key) {
   const hipError_t e = hipGetDevice(&dev);
   *key = StreamKey(dev, stream, stream == hipStreamPerThread ? thread : 0);
   return e;
-}
-
-// Compute units of the current device (the owner wait is used only while the
-// whole grid fits on them).
-int skg::device_cus() {
-  static std::mutex mu;
-  static std::map<int, int> cache;
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return 0;
-  std::lock_guard<std::mutex> lock(mu);
-  auto it = cache.find(dev);
-  if (it != cache.end()) return it->second;
-  int n = 0;
-  if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) n = 0;
-  cache[dev] = n;
-  return n;
 }
 
 int skg::knob(int k, int dflt) {

@@ -49,72 +49,63 @@ __device__ __forceinline__ void store_sums(const I8Params& p, int t, int n, i32x
   }
 }
 
-// Few tokens: the weights' stream is everything. A workgroup of WAVES waves
-// takes 16 RG features x 16 NT tokens, operands straight from memory into
-// registers; the waves take the row's 128-byte units in turn and their sums meet
-// in LDS, so K is split without a second pass.
+// Few tokens: the weights' stream is everything. A workgroup of eight waves takes
+// 16 features x 16 tokens, operands straight from memory into registers; the
+// waves take the row's 128-byte units in turn and their sums meet in LDS, so K is
+// split without a second pass.
 //
 // Both operands come as line pairs (device/types.h): 8 rows x 128 bytes a load,
 // whole lines; one DPP move a register makes the two 16-row operands. With at
-// most 8 tokens the second load of the activations' pair is left out. U units
-// are in flight in each wave: a slot is consumed, then refilled. Bound by the
+// most 8 tokens (LOW) the second load of the activations' pair is left out. U
+// units are in flight in each wave: a slot is consumed, then refilled. Bound by the
 // weights: T=1 N=18432 K=7168 23.5 us (5.6 TB/s), T=8 N=K=16384 51 us (5.2);
 // below about 30 MB by launch and latency (T=1 N=2048 K=7168 6.6 us).
-template <int NT, bool LOW, int RG, int WAVES, int U>
-__global__ __launch_bounds__(64 * WAVES) void i8_rows_kernel(I8Params p) {
+constexpr int kRowWaves = 8;
+template <bool LOW, int U>
+__global__ __launch_bounds__(64 * kRowWaves) void i8_rows_kernel(I8Params p) {
   constexpr int kXL = LOW ? 1 : 2;  // loads of 16 tokens
-  static_assert(!LOW || NT == 1, "at most 8 tokens are one half tile");
-  __shared__ i32x4 part[WAVES][RG * NT][64];
+  __shared__ i32x4 part[kRowWaves][64];
   const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int li = lane & 15, g = lane >> 4;
-  const int ntiles = (p.N + 16 * RG - 1) / (16 * RG);
+  const int ntiles = (p.N + 15) / 16;
   const int tt = (int)blockIdx.x / ntiles;
-  const int n0 = ((int)blockIdx.x - tt * ntiles) * 16 * RG, t0 = tt * 16 * NT;
-  const int rows = min(16 * RG, p.N - n0), tokens = min(16 * NT, p.T - t0);
+  const int n0 = ((int)blockIdx.x - tt * ntiles) * 16, t0 = tt * 16;
+  const int rows = min(16, p.N - n0), tokens = min(16, p.T - t0);
   const rsrc_t w = make_rsrc(p.w + (size_t)n0 * p.w_stride, (uint32_t)((rows - 1) * p.w_stride + p.K));
   const rsrc_t x = make_rsrc(p.x + (size_t)t0 * p.x_stride, (uint32_t)((tokens - 1) * p.x_stride + p.K));
   const int in_line = 64 * (li >> 3) + 16 * g;  // this lane's bytes of a unit
   // Rows past the tile's end read zeros.
-  uint32_t woff[2 * RG], xoff[kXL * NT];
+  uint32_t woff[2], xoff[kXL];
 #pragma unroll
-  for (int q = 0; q < 2 * RG; ++q) {
+  for (int q = 0; q < 2; ++q) {
     const int r = 8 * q + (li & 7);
     woff[q] = r < rows ? (uint32_t)(r * p.w_stride + in_line) : kOOB;
   }
 #pragma unroll
-  for (int q = 0; q < kXL * NT; ++q) {
+  for (int q = 0; q < kXL; ++q) {
     const int r = 8 * q + (li & 7);
     xoff[q] = r < tokens ? (uint32_t)(r * p.x_stride + in_line) : kOOB;
   }
-  u32x4 wv[U][2 * RG], xv[U][kXL * NT];
+  u32x4 wv[U][2], xv[U][kXL];
   auto fill = [&](int u, int k) {  // k past the row's end: zeros
     const uint32_t past = k + in_line < p.K ? 0u : kOOB;
 #pragma unroll
-    for (int q = 0; q < kXL * NT; ++q)
+    for (int q = 0; q < kXL; ++q)
       xv[u][q] = __builtin_amdgcn_raw_buffer_load_b128(x, xoff[q] | past, k, kPolicyDefault);
 #pragma unroll
-    for (int q = 0; q < 2 * RG; ++q)
+    for (int q = 0; q < 2; ++q)
       wv[u][q] = __builtin_amdgcn_raw_buffer_load_b128(w, woff[q] | past, k, kPolicyStream);
   };
-  i32x4 acc[RG * NT] = {};
-  constexpr int kStep = 128 * WAVES;
+  i32x4 acc = {};
+  constexpr int kStep = 128 * kRowWaves;
 #pragma unroll
   for (int u = 0; u < U; ++u) fill(u, 128 * wave + u * kStep);
   auto use = [&](int u) {
-    u32x4 x0[NT], x1[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-      line_pair_to_operands(xv[u][kXL * j], LOW ? u32x4{0, 0, 0, 0} : xv[u][kXL * j + kXL - 1], x0[j], x1[j]);
-#pragma unroll
-    for (int r = 0; r < RG; ++r) {
-      u32x4 w0, w1;
-      line_pair_to_operands(wv[u][2 * r], wv[u][2 * r + 1], w0, w1);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        acc[r * NT + j] = mfma_i8(w0, x0[j], acc[r * NT + j]);
-        acc[r * NT + j] = mfma_i8(w1, x1[j], acc[r * NT + j]);
-      }
-    }
+    u32x4 x0, x1, w0, w1;
+    line_pair_to_operands(xv[u][0], LOW ? u32x4{0, 0, 0, 0} : xv[u][kXL - 1], x0, x1);
+    line_pair_to_operands(wv[u][0], wv[u][1], w0, w1);
+    acc = mfma_i8(w0, x0, acc);
+    acc = mfma_i8(w1, x1, acc);
   };
   int k = 128 * wave;
   for (; k + U * kStep < p.K; k += U * kStep) {
@@ -126,19 +117,16 @@ __global__ __launch_bounds__(64 * WAVES) void i8_rows_kernel(I8Params p) {
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) use(u);
-#pragma unroll
-  for (int j = 0; j < RG * NT; ++j) part[wave][j][lane] = acc[j];
+  part[wave][lane] = acc;
   __syncthreads();
-  for (int j = wave; j < RG * NT; j += WAVES) {
-    i32x4 s = part[0][j][lane];
+  if (wave != 0) return;
 #pragma unroll
-    for (int v = 1; v < WAVES; ++v) s += part[v][j][lane];
-    const int t = t0 + 16 * (j % NT) + li, n = n0 + 16 * (j / NT) + 4 * g;
-    float ws[4];
+  for (int v = 1; v < kRowWaves; ++v) acc += part[v][lane];
+  const int t = t0 + li, n = n0 + 4 * g;
+  float ws[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) ws[e] = n + e < p.N ? p.w_scale[n + e] : 0.0f;
-    if (t < p.T) store_sums(p, t, n, s, p.x_scale[t], ws);
-  }
+  for (int e = 0; e < 4; ++e) ws[e] = n + e < p.N ? p.w_scale[n + e] : 0.0f;
+  if (t < p.T) store_sums(p, t, n, acc, p.x_scale[t], ws);
 }
 
 // A tile of BT tokens x BN features, K in steps of 128 bytes through LDS.
@@ -469,10 +457,10 @@ hipError_t launch_shape(int shape, const I8Params& p, int grid, hipStream_t s) {
   }
 }
 
-template <int NT, bool LOW, int RG, int WAVES, int U>
+template <bool LOW, int U>
 hipError_t launch_rows(const I8Params& p, hipStream_t s) {
-  const int ntiles = (p.N + 16 * RG - 1) / (16 * RG), ttiles = (p.T + 16 * NT - 1) / (16 * NT);
-  return launch(i8_rows_kernel<NT, LOW, RG, WAVES, U>, dim3((unsigned)(ntiles * ttiles)), dim3(64 * WAVES), 0, s, p);
+  const int ntiles = (p.N + 15) / 16, ttiles = (p.T + 15) / 16;
+  return launch(i8_rows_kernel<LOW, U>, dim3((unsigned)(ntiles * ttiles)), dim3(64 * kRowWaves), 0, s, p);
 }
 
 // Units in flight: one load round of a wave where K is short (the workgroups of
@@ -480,12 +468,8 @@ hipError_t launch_rows(const I8Params& p, hipStream_t s) {
 // U = 7: T=1 N=4096 K=1024 3.4 / 4.7 us, T=1 N=16384 K=1024 5.5 / 11.5 us; T=8
 // N=4096 K=7168 8.9 / 7.9 us, T=8 N=K=16384 60.8 / 51.3 us.
 hipError_t launch_rows_for(const I8Params& p, hipStream_t s) {
-  if (p.K < 4096) {
-    if (p.T <= 8) return launch_rows<1, true, 1, 8, 1>(p, s);
-    return launch_rows<1, false, 1, 8, 1>(p, s);
-  }
-  if (p.T <= 8) return launch_rows<1, true, 1, 8, 7>(p, s);
-  return launch_rows<1, false, 1, 8, 7>(p, s);
+  if (p.K < 4096) return p.T <= 8 ? launch_rows<true, 1>(p, s) : launch_rows<false, 1>(p, s);
+  return p.T <= 8 ? launch_rows<true, 7>(p, s) : launch_rows<false, 7>(p, s);
 }
 
 }  // namespace

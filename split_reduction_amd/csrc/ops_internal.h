@@ -83,6 +83,5 @@ hipError_t launch_rmsnorm(const NormParams& p, int out_format, hipStream_t s);
 int hip_fail(hipError_t e);
 // Frees the workspaces of ops_api.hip; part of skgemm_release.
 int release_ops_workspaces();
-int device_cus();
 
 }  // namespace skg
