@@ -417,29 +417,33 @@ __global__ __launch_bounds__(512) void i8_big_kernel(I8Params p) {
 
 namespace {
 
-// The tile shapes and what a call with each costs, fitted to the times of 7035
-// calls (T = 9..4096, N = 549..18432, K = 1024..16384, every shape, K split 1
-// to 8 ways) and then to the choices: a workgroup pays kStart and `alone` a step
+// The tile shapes and a score of each by which a call's shape and split are
+// ranked. It has the form of a cost (a workgroup pays kStart and `alone` a step
 // while the CU has room for it (`fit` at once), or `crowded` a step for each
-// workgroup of the CU where they queue; the weights pass at kWeights at most; K
-// split S ways adds kJoinRank S and the sums' traffic. Over those 216 sizes the
-// choice is 1.5 % slower on average than the fastest call found for each (T=128
-// N=16384 K=4096, the worst: 26.8 against 21.9 us).
-// Why these six, each against the best of the others (us): 256 x 256 T=N=4096
-// K=7168 111 / 122; 256 x 128 T=509 N=18432 K=7168 92 / 100; 128 x 128 two to a
-// CU T=384 N=18432 K=7168 66 / 80; 128 x 128 with four buffers T=128 N=16384
-// K=4096 21.9 / 26.8; 64 x 64 T=256 N=7168 K=2048 12.1 / 15.2; 32 x 64 T=64 N=6015
-// K=2736 10.3 / 12.4.
+// workgroup of the CU where they queue; the weights pass at kWeights; K split S
+// ways adds kJoinRank S and the sums' traffic), but its numbers are no times: they
+// were fitted to 7035 timed calls (T = 9..4096, N = 549..18432, K = 1024..16384) and
+// then moved until the choices came out best (T=32 N=18432 K=7168 scores 18.8 and
+// takes 31 us). Over those 216 sizes the choice is 1.9 % slower on average than the
+// fastest found for each, 29 % at most (T=384 N=4096 K=7168 33.0 against 25.6 us).
+// Nothing was fitted past them: at K=7168 with float output N=32001 takes 42.7 us
+// for 32 tokens (the best shape pinned 40.7) and 92 for 256 (best 92), N=131072
+// 168 (best 162) and 277 (best 277).
+// Why these five, each where it is chosen against the best of the others (us):
+// 256 x 256 T=N=4096 K=7168 119 / 134; 128 x 128 two to a CU T=800 N=18432 K=7168 132
+// / 155; 128 x 128 with four buffers T=1024 N=4096 K=4096 25.5 / 30.9; 64 x 64 T=256
+// N=7168 K=2048 13.1 / 14.6; 32 x 64 T=32 N=18432 K=7168 30.8 / 33.3. A shape of 256 x
+// 128 was chosen for short K only and no faster there (T=3872 N=9563 K=512 90 / 84).
 struct TileShape {
   unsigned bt, bn, fit;
-  float alone, crowded;  // us a step of 128 bytes of K
+  float alone, crowded;  // a step of 128 bytes of K
 };
 constexpr TileShape kShapes[] = {
-    {256, 256, 1, 2.081f, 1.922f}, {256, 128, 1, 0.301f, 1.116f}, {128, 128, 2, 0.956f, 0.532f},
-    {128, 128, 1, 0.499f, 0.634f}, {64, 64, 2, 0.324f, 0.204f},   {32, 64, 3, 0.226f, 0.179f},
+    {256, 256, 1, 2.081f, 1.922f}, {128, 128, 2, 0.956f, 0.532f}, {128, 128, 1, 0.499f, 0.634f},
+    {64, 64, 2, 0.324f, 0.204f},   {32, 64, 3, 0.226f, 0.179f},
 };
-constexpr float kStart = 0.41f, kJoinRank = 0.222f;    // us
-constexpr float kWeights = 10.69e6f, kSums = 4.56e6f;  // bytes a us
+constexpr float kStart = 0.41f, kJoinRank = 0.222f;
+constexpr float kWeights = 10.69e6f, kSums = 4.56e6f;  // bytes
 constexpr int kShapeCount = (int)(sizeof(kShapes) / sizeof(kShapes[0]));
 template <int BT, int BN, int WT, int WN, int STG>
 hipError_t launch_tile(const I8Params& p, int grid, hipStream_t s) {
@@ -449,10 +453,9 @@ hipError_t launch_tile(const I8Params& p, int grid, hipStream_t s) {
 hipError_t launch_shape(int shape, const I8Params& p, int grid, hipStream_t s) {
   switch (shape) {
     case 0: return launch(i8_big_kernel, dim3((unsigned)grid), dim3(512), 0, s, p);
-    case 1: return launch_tile<256, 128, 4, 2, 3>(p, grid, s);
-    case 2: return launch_tile<128, 128, 4, 2, 2>(p, grid, s);
-    case 3: return launch_tile<128, 128, 2, 4, 4>(p, grid, s);
-    case 4: return launch_tile<64, 64, 2, 4, 4>(p, grid, s);
+    case 1: return launch_tile<128, 128, 4, 2, 2>(p, grid, s);
+    case 2: return launch_tile<128, 128, 2, 4, 4>(p, grid, s);
+    case 3: return launch_tile<64, 64, 2, 4, 4>(p, grid, s);
     default: return launch_tile<32, 64, 1, 4, 4>(p, grid, s);
   }
 }
@@ -477,7 +480,11 @@ hipError_t launch_rows_for(const I8Params& p, hipStream_t s) {
 I8Tactic pick_i8(int T, int N, int K) {
   I8Tactic best;
   const int pinned = knob(kKnobI8Shape, -1), split = knob(kKnobI8Split, 0);
-  // Few tokens, or little work: straight into registers (shape -1).
+  // Few tokens, or little work: straight into registers (shape -1). Measured
+  // against the best tile (us): T=8 N=K=4096 6.5 / 7.3; T=16 N=2048 K=4096 6.7 / 7.0,
+  // past the border N=4096 K=8192 11.7 / 9.7; T=32 N=1024 K=2048 4.2 / 6.0, N=2048
+  // K=4096 6.9 / 7.3. The borders lie below where the two meet (T=32 N=K=2048 4.3 /
+  // 6.1), and for 8 tokens a very wide N is slower so (N=131072 K=7168 163 / 141).
   const long work = (long)N * K;
   const bool rows = T <= 8 || (T <= 16 && work <= 8L << 20) || (T <= 32 && work <= 2L << 20);
   if (pinned >= kShapeCount || (pinned < 0 && rows)) return best;
@@ -497,13 +504,13 @@ I8Tactic pick_i8(int T, int N, int K) {
       const unsigned rest = S > 1 ? split_rest : tiles, whole = tiles - rest;
       if (S > 1 && (rest == 0 || rest * S * bytes > kOpsPartBytes || rest > (unsigned)kOpsCounters)) continue;
       const unsigned m = (rest * S + 255) / 256, each = (steps + S - 1) / S;
-      float us = std::max((float)((m + sh.fit - 1) / sh.fit) * (kStart + (float)each * sh.alone),
-                          (float)m * (kStart + (float)each * sh.crowded));
-      us += (float)(whole / 256) * (kStart + (float)steps * sh.crowded);
-      us = std::max(us, ((float)N + (float)T) * (float)K / kWeights);
-      if (S > 1) us += kJoinRank * (float)S + 8.0f * (float)(S * rest) * (float)(sh.bt * sh.bn) / kSums;
-      if (best.shape < 0 || us < least) {
-        least = us;
+      float score = std::max((float)((m + sh.fit - 1) / sh.fit) * (kStart + (float)each * sh.alone),
+                             (float)m * (kStart + (float)each * sh.crowded));
+      score += (float)(whole / 256) * (kStart + (float)steps * sh.crowded);
+      score = std::max(score, ((float)N + (float)T) * (float)K / kWeights);
+      if (S > 1) score += kJoinRank * (float)S + 8.0f * (float)(S * rest) * (float)(sh.bt * sh.bn) / kSums;
+      if (best.shape < 0 || score < least) {
+        least = score;
         best.shape = i;
         best.S = (int)S;
         best.whole = (int)whole;
