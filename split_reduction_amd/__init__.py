@@ -122,18 +122,18 @@ def _check(code: int, name: str) -> None:
 
 
 def _types() -> dict:
-    """The element types of the operators' tensors. A type of the same width
-    would be read as the call's own: float16 logits as bf16, say."""
+    """The element types of the operators' tensors, with their size. A type of the
+    same width would be read as the call's own: float16 logits as bf16, say."""
     if not _torch_types:
         import torch as t
 
-        _torch_types.update(bf16=(t.bfloat16,), f32=(t.float32,), i64=(t.int64,), i8=(t.int8,),
-                            i8_out=(t.int8, t.uint8), e4m3_out=(t.uint8, t.float8_e4m3fn))
+        _torch_types.update(bf16=(2, (t.bfloat16,)), f32=(4, (t.float32,)), i64=(8, (t.int64,)), i8=(1, (t.int8,)),
+                            i8_out=(1, (t.int8, t.uint8)), e4m3_out=(1, (t.uint8, t.float8_e4m3fn)))
     return _torch_types
 
 
 def _wrong_type(a, types, what: str) -> SkgemmError:
-    return SkgemmError(SKGEMM_EINVAL, f"{what}: elements of {a.dtype}, the call takes {' or '.join(map(str, types))}")
+    return SkgemmError(SKGEMM_EINVAL, f"{what}: elements of {a.dtype}, the call takes {' or '.join(map(str, types[1]))}")
 
 
 def _ptr(a, nbytes: int = 0, what: str = "argument", types=None) -> int:
@@ -144,8 +144,8 @@ def _ptr(a, nbytes: int = 0, what: str = "argument", types=None) -> int:
     address, so a host tensor, a strided view or a short buffer would reach the
     device as a bad address. Such tensors raise SkgemmError(SKGEMM_EINVAL) here,
     before anything is launched, and so do elements of another type than `types`
-    (None: any). Integer addresses are passed through unchecked (the caller
-    vouches for them)."""
+    (one of _types; None: any). Integer addresses are passed through unchecked
+    (the caller vouches for them)."""
     if a is None:
         return 0
     if isinstance(a, int):
@@ -156,11 +156,15 @@ def _ptr(a, nbytes: int = 0, what: str = "argument", types=None) -> int:
         on_gpu = a.device.type == "cuda"
     if not on_gpu:
         raise SkgemmError(SKGEMM_EINVAL, f"{what}: a tensor on {a.device}, not on the GPU")
-    if types is not None and a.dtype not in types:
+    if types is None:
+        size = a.element_size()
+    elif a.dtype in types[1]:
+        size = types[0]
+    else:
         raise _wrong_type(a, types, what)
     if not a.is_contiguous():
         raise SkgemmError(SKGEMM_EINVAL, f"{what}: not contiguous")
-    have = a.numel() * a.element_size()
+    have = a.numel() * size
     if have < nbytes:
         raise SkgemmError(SKGEMM_EINVAL, f"{what}: holds {have} bytes, the call needs {nbytes}")
     return a.data_ptr()
@@ -169,20 +173,20 @@ def _ptr(a, nbytes: int = 0, what: str = "argument", types=None) -> int:
 def _rows(a, rows: int, row_bytes: int, stride, what: str, types):
     """(address, row stride in bytes) of a matrix whose rows are `row_bytes` long
     and contiguous, `stride` bytes apart (None: as the tensor's own rows are, or
-    dense for an address). The tensor must be on the GPU, hold elements of one
-    of `types` and reach to the end of the last row."""
+    dense for an address). The tensor must be on the GPU, hold elements of
+    `types` (one of _types) and reach to the end of the last row."""
     if stride is not None and stride < 0:
         raise SkgemmError(SKGEMM_EINVAL, f"{what}: a negative row stride")
     if a is None or isinstance(a, int):
         return a or 0, row_bytes if stride is None else stride
     if not a.is_cuda:
         raise SkgemmError(SKGEMM_EINVAL, f"{what}: a tensor on {a.device}, not on the GPU")
-    if a.dtype not in types:
+    if a.dtype not in types[1]:
         raise _wrong_type(a, types, what)
-    size = a.element_size()
-    if stride is None and a.numel() * size == rows * row_bytes and a.is_contiguous():
-        return a.data_ptr(), row_bytes  # dense
+    size = types[0]
     n = a.numel() * size
+    if stride is None and n == rows * row_bytes and a.is_contiguous():
+        return a.data_ptr(), row_bytes  # dense
     if a.is_contiguous():
         if stride is None:
             stride = a.stride(0) * size if a.dim() == 2 and rows > 1 and a.stride(0) * size >= row_bytes else row_bytes
