@@ -222,8 +222,10 @@ SKGEMM_API int skgemm_mxfp8_batched(const void* Wq8, const void* Wscale, const v
  * several workgroups meets in a workspace of the stream that is separate from
  * the split-K workspace above and of one fixed size: the first call on a stream
  * allocates it, skgemm_reserve_ops does so ahead of a graph capture, and
- * skgemm_release frees it. A captured call keeps the workspace of the stream it
- * was captured on: its replays must not overlap other calls that use that one.
+ * skgemm_release frees it. All of it, SKGEMM_OPS_WORKSPACE_BYTES, is allocated
+ * whatever the call needs (skgemm_logprobs at most 540 KB). A captured call keeps
+ * the workspace of the stream it was captured on: its replays must not overlap
+ * other calls that use that one.
  */
 #define SKGEMM_OPS_WORKSPACE_BYTES ((size_t)65 << 20)
 enum skgemm_format {
@@ -301,8 +303,8 @@ SKGEMM_API int skgemm_i8(const void* Wq, const float* w_scale, const void* Xq, c
  * right there, as they are built from differences to the row's largest logit.
  * A logit of -inf is a banned token: probability 0, nothing added to the
  * entropy, logprob -inf. A row of nothing but -inf has lse -inf, entropy 0 and
- * logprobs -inf. A row with a NaN or +inf has NaN for every float output and
- * -1 for every id.
+ * logprobs -inf. A row with a NaN or +inf has NaN for every float output (but
+ * the 0 of a padding token) and -1 for every id.
  */
 SKGEMM_API int skgemm_logprobs(const void* logits, const int64_t* tokens, float* logprob,
                                float* entropy, float* lse, float* top_logprob, int64_t* top_ids,
@@ -318,9 +320,10 @@ SKGEMM_API int skgemm_logprobs(const void* logits, const int64_t* tokens, float*
  *   d_logits has the logits' type and may be the logits themselves (same
  *   stride); other overlaps are not supported. g_logprob or g_entropy null:
  *   zeros (tokens null only with g_logprob null; entropy null only with
- *   g_entropy null). A padding row (token < 0) has no logprob term. Rows of
- *   nothing but -inf (lse -inf) get zeros; a NaN lse gives a NaN row, and so
- *   does +inf, which a finite row has where scale * max passes FP32's range.
+ *   g_entropy null). A padding row (token < 0) has no logprob term; a token >= V
+ *   gives a NaN row (with g_logprob). Rows of nothing but -inf (lse -inf) get
+ *   zeros; a NaN lse gives a NaN row, and so does +inf, which a finite row has
+ *   where scale * max passes FP32's range.
  */
 SKGEMM_API int skgemm_logprobs_grad(const void* logits, const int64_t* tokens, const float* lse,
                                     const float* entropy, const float* g_logprob,

@@ -144,10 +144,11 @@ __global__ __launch_bounds__(64 * kRowWaves) void i8_rows_kernel(I8Params p) {
 // landed and every wave has read the previous step's buffer, which the next
 // loads then fill.
 //
-// Bound by the products for large calls, by the weights' stream for few tokens
-// (T=32 N=18432 K=7168: 29.4 us, 4.5 TB/s) and in between by the loads into LDS,
-// up to 70 GB/s a CU (T=509 N=4100 K=7168: 30.4 us). Loads counted by hand: left
-// to the compiler, T=4096 N=18432 K=7168 took 664 instead of 582 us.
+// Bound by the weights' stream for few tokens (T=32 N=18432 K=7168: 29.4 us, 4.5
+// TB/s) and above that by the loads into LDS, up to 70 GB/s a CU (T=509 N=4100
+// K=7168: 31.5 us). Loads counted by hand: left
+// to the compiler, T=4096 N=18432 K=7168 took 664 instead of 582 us (before the
+// kernel below took such calls).
 //
 // S workgroups may split K of a tile: each stores its sums to the workspace and
 // the last to arrive adds the others' (integers: the order does not matter).
@@ -332,17 +333,21 @@ __global__ __launch_bounds__(64 * WT * WN) void i8_tile_kernel(I8Params p) {
   store_blocks<kNT, kMT>(p, t.t0 + wt * (BT / WT), t.n0 + wn * (BN / WN), acc, lane);
 }
 
-// The same tile for matrix-core bound calls: 256 x 256, two waves a SIMD that
+// The same tile for calls of many products: 256 x 256, two waves a SIMD that
 // take turns. A step is four phases, each closed by a barrier: operands of the
 // first 64 bytes of K from LDS (R0), their products (M0), the other 64 bytes
 // (R1, M1). Waves 4-7 (the second of each SIMD) run one phase behind waves 0-3,
 // so that while one wave of a SIMD multiplies the other reads, and only four
 // waves at a time share the LDS (all eight in step: 591 against 561 us at
 // T=N=K=8192).
-// T=4096 N=18432 K=7168: 507 us, 2.13 POP/s; the clock is then held at 1.85 of
-// 2.4 GHz by power. T=N=K=8192 took 560 us, without the loads 430, without loads
-// and LDS reads 404; the 32 x 32 x 32 instruction took 617 against 534 us, four
-// stages of 64 bytes 602 against 560.
+// T=4096 N=18432 K=7168: 508 us, 2.13 POP/s, at 2.25 GHz once the clock is steady
+// (the first twenty launches after a pause take about 575). The matrix units are
+// busy 45 % of the cycles: a phase has 512 cycles of products and takes about 1130.
+// Neither their rate nor the memory bounds it, then, but the phases, and most of
+// that is in barriers and products themselves: T=N=K=8192 took 560 us, without the
+// loads 430, without loads and LDS reads 404. What the waves wait for there has not
+// been shown. The 32 x 32 x 32 instruction took 617 against 534 us, four stages of
+// 64 bytes 602 against 560.
 // With A's step s in phases 4s .. 4s+3 and B's one later, the last reads of
 // step s - 1 are B's R1 in phase 4s - 1: from phase 4s on its buffer may be
 // filled for step s + 1 (A issues in its R0, B in its M1 before), and the loads
@@ -433,7 +438,9 @@ namespace {
 // 256 x 256 T=N=4096 K=7168 119 / 134; 128 x 128 two to a CU T=800 N=18432 K=7168 132
 // / 155; 128 x 128 with four buffers T=1024 N=4096 K=4096 25.5 / 30.9; 64 x 64 T=256
 // N=7168 K=2048 13.1 / 14.6; 32 x 64 T=32 N=18432 K=7168 30.8 / 33.3. A shape of 256 x
-// 128 was chosen for short K only and no faster there (T=3872 N=9563 K=512 90 / 84).
+// 128 was chosen for short K only and no faster there (T=3872 N=9563 K=512 90 / 84),
+// though it was the fastest at some sizes that were not given to it (T=1024 N=18432
+// K=7168 154 / 161).
 struct TileShape {
   unsigned bt, bn, fit;
   float alone, crowded;  // a step of 128 bytes of K

@@ -5,15 +5,19 @@
 //   s = sum 2^d, u = sum 2^d d,
 //   lse = scale m + log s,  entropy = (log2 s - u / s) log 2,
 //   logprob = scale (x[token] - m) - log s.
-// The difference is taken before the scaling, so the type's lowest value does
-// not become an infinity on the way, every term is built from d, so nothing
-// cancels against m, and two parts of a row join by moving one to the other's
-// reference:  with f = (m - m') c:  s' = s 2^f,  u' = 2^f (u + f s).
+// Every term is built from d, so nothing cancels against m, and two parts of a row
+// join by moving one to the other's reference:  with f = (m - m') c:  s' = s 2^f,
+// u' = 2^f (u + f s). The pass over the data takes d as x c - ref in one fused
+// operation a logit, with ref = m c rounded, and moves its sums from ref to m itself
+// at the end. Where a product passes FP32's range (the type's lowest value as a
+// mask, a large scale) a run's sums come out as 0 or not finite: it is then read
+// again, with the difference before the scaling.
 //
 // Bound by memory for float logits (T=2048 V=131072: 163 us without alternatives,
 // 6.6 TB/s) and by arithmetic for bf16: eight logits take about 80 vector slots,
 // 32 of them the exponentials at a quarter rate, nearly the time of their read
-// (T=4096 V=131072 with 8 alternatives 199 us, 5.4 TB/s, vector units nine tenths busy).
+// (T=4096 V=131072 with 8 alternatives 198 us, 5.4 TB/s, vector units nine tenths
+// busy; 228 in the first twenty launches after a pause).
 // The gradient reads and writes: T=4096 V=131072 bf16 400 us, 5.4 TB/s.
 
 #include <algorithm>

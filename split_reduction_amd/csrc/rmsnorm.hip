@@ -11,7 +11,7 @@
 // free of rstd: sum(h^2) and max|h g| meet in one reduction behind one barrier.
 //
 // Bound by memory: 7 bytes an element (x, r, R_out, codes) and about 10 vector
-// operations. T=8192 H=7168 with a residual and E4M3 codes: 70.6 us, 5.8 TB/s (a
+// operations. T=8192 H=7168 with a residual and E4M3 codes: 70.8 us, 5.8 TB/s (a
 // large copy reaches 5.1); T=1: 3.5 us.
 
 #include "device/block.h"
