@@ -84,7 +84,8 @@ enum skgemm_status {
  *            over the cluster ranks; shapes are validated, never padded).
  *   stream   HIP stream to enqueue on (0 = the null stream).
  * With split_k > 1 the first call on a stream allocates that stream's
- * workspace (see skgemm_reserve) unless one large enough exists.
+ * workspace (see skgemm_reserve) unless one large enough exists, and waits for
+ * the stream until it is cleared.
  */
 SKGEMM_API int skgemm_bf16(const void* W, const void* X, void* C, int T, int N, int K,
                            int split_k, hipStream_t stream);
@@ -221,7 +222,7 @@ SKGEMM_API int skgemm_mxfp8_batched(const void* Wq8, const void* Wscale, const v
  * rows in BYTES. Sizes of zero enqueue nothing and succeed. Work split over
  * several workgroups meets in a workspace of the stream that is separate from
  * the split-K workspace above and of one fixed size: the first call on a stream
- * allocates it, skgemm_reserve_ops does so ahead of a graph capture, and
+ * allocates it (and waits until it is cleared), skgemm_reserve_ops does so ahead of a graph capture, and
  * skgemm_release frees it. All of it, SKGEMM_OPS_WORKSPACE_BYTES, is allocated
  * whatever the call needs (skgemm_logprobs at most 540 KB). A captured call keeps
  * the workspace of the stream it was captured on: its replays must not overlap
