@@ -222,11 +222,12 @@ SKGEMM_API int skgemm_mxfp8_batched(const void* Wq8, const void* Wscale, const v
  * rows in BYTES. Sizes of zero enqueue nothing and succeed. Work split over
  * several workgroups meets in a workspace of the stream that is separate from
  * the split-K workspace above and of one fixed size: the first call on a stream
- * allocates it (and waits until it is cleared), skgemm_reserve_ops does so ahead of a graph capture, and
- * skgemm_release frees it. All of it, SKGEMM_OPS_WORKSPACE_BYTES, is allocated
- * whatever the call needs (skgemm_logprobs at most 540 KB). A captured call keeps
- * the workspace of the stream it was captured on: its replays must not overlap
- * other calls that use that one.
+ * allocates it (and waits until it is cleared), skgemm_reserve_ops does so ahead
+ * of a graph capture, and skgemm_release frees it. All of it,
+ * SKGEMM_OPS_WORKSPACE_BYTES, is allocated whatever the call needs
+ * (skgemm_logprobs at most 540 KB). A captured call keeps the workspace of the
+ * stream it was captured on: its replays must not overlap other calls that use
+ * that one.
  */
 #define SKGEMM_OPS_WORKSPACE_BYTES ((size_t)65 << 20)
 enum skgemm_format {
