@@ -243,6 +243,13 @@ enum skgemm_format {
 #define SKGEMM_MAX_V (1 << 20)    /* skgemm_logprobs, skgemm_logprobs_grad */
 #define SKGEMM_MAX_TOP 64
 #define SKGEMM_MAX_SCALE 2e38f
+#define SKGEMM_MAX_HEADS 4096     /* skgemm_rope and the two calls after it */
+#define SKGEMM_MAX_PAGE (1 << 15) /* tokens of a page */
+#define SKGEMM_MAX_LEN (1 << 30)  /* tokens of a sequence */
+enum skgemm_rope_layout {
+  SKGEMM_ROPE_HALF = 0,       /* pairs (i, i + rot / 2) */
+  SKGEMM_ROPE_INTERLEAVED = 1 /* pairs (2 i, 2 i + 1)   */
+};
 
 /*
  * skgemm_rmsnorm: h = X + R (in FP32, from here on unrounded), R_out = bf16(h),
@@ -332,6 +339,106 @@ SKGEMM_API int skgemm_logprobs_grad(const void* logits, const int64_t* tokens, c
                                     const float* g_entropy, void* d_logits, int T, int V,
                                     float scale, int logits_format, size_t stride, size_t d_stride,
                                     hipStream_t stream);
+
+/*
+ * skgemm_rope: norm of each head and rotation by position, both optional. Of the D
+ * values x of every head of every token, in FP32 and rounded once:
+ *   with G: x <- x / sqrt(mean(x^2) + eps) * G;
+ *   with rot > 0: the pairs (a, b) of the first rot values (which: layout) become
+ *   amplitude * (a cos w - b sin w, b cos w + a sin w), w = positions[t] *
+ *   inv_freq[i] for pair i. The angle is taken in FP64, so far positions keep it.
+ *   Scaled contexts are a matter of inv_freq and amplitude.
+ *   X, Y       bf16 [T, H, D], a token's heads one after another; rows as above.
+ *              Y may be X (same stride, else SKGEMM_EINVAL); other overlaps are
+ *              not supported.
+ *   G          bf16 [D], or null: no norm.
+ *   inv_freq   float [rot / 2], positions int64 [T]; may be null for rot 0.
+ *   D % 16 == 0, 16 <= D <= 256; rot % 16 == 0, 0 <= rot <= D; H <=
+ *   SKGEMM_MAX_HEADS (SKGEMM_ESHAPE). With G 1e-30 <= eps < inf; amplitude finite.
+ *   X, G, Y are 16-byte aligned, strides multiples of 16.
+ * With G a head that holds an infinity or a NaN is NaN throughout; finite heads of
+ * any size are right.
+ */
+SKGEMM_API int skgemm_rope(const void* X, const void* G, const float* inv_freq,
+                           const int64_t* positions, void* Y, int T, int H, int D, int rot,
+                           int layout, float eps, float amplitude, size_t x_stride,
+                           size_t y_stride, hipStream_t stream);
+
+/*
+ * The paged cache of the next two calls: page i, token j of it, key head h, D
+ * values at base + i * page_stride + j * slot_stride + h * head_stride (bytes), the
+ * same for K_cache and V_cache. Either order of a page's tokens and heads is a
+ * choice of strides. Elements are bf16, or E4M3 codes that stand for code * k_scale
+ * (v_scale); with bf16 both scales are 1 (SKGEMM_EINVAL). page_size is a power of
+ * two up to SKGEMM_MAX_PAGE; the caches are 16-byte aligned, strides multiples of
+ * 16, and one page spans less than 4 GiB (SKGEMM_ESHAPE). Caches of any total size.
+ *
+ * skgemm_rope_append: skgemm_rope of Q into Q_out and of K into the cache, and V as
+ * it is into the cache, in one launch: queries, keys and values as the layer's first
+ * product leaves them.
+ *   Q [T, Hq, D], K and V [T, Hkv, D] bf16, each with its own row stride (parts of
+ *   one product's rows, say); Gq, Gk as G above, each may be null. Q_out may be Q
+ *   (same stride). Hq 0: keys and values alone; Hkv 0: queries alone.
+ *   slots int64 [T]: token t goes to page slots[t] / page_size, token slots[t] %
+ *   page_size of it. A slot below 0 (padding) or past the cache's n_pages is not
+ *   stored. The same slot twice: one of the two, which is not said.
+ *   E4M3 codes are of value / k_scale (v_scale), saturated to +-448, to nearest
+ *   even; a NaN keeps its code. Outputs must not overlap (SKGEMM_EINVAL where the
+ *   strides say so).
+ */
+SKGEMM_API int skgemm_rope_append(const void* Q, const void* K, const void* V, const void* Gq,
+                                  const void* Gk, const float* inv_freq,
+                                  const int64_t* positions, const int64_t* slots, void* Q_out,
+                                  void* K_cache, void* V_cache, int T, int Hq, int Hkv, int D,
+                                  int n_pages, int page_size, int rot, int layout, float eps,
+                                  float amplitude, int cache_format, float k_scale, float v_scale,
+                                  size_t q_stride, size_t k_stride, size_t v_stride,
+                                  size_t q_out_stride, size_t page_stride, size_t slot_stride,
+                                  size_t head_stride, hipStream_t stream);
+
+/*
+ * skgemm_paged_attention: causal attention of each sequence's new tokens, whose
+ * keys and values the cache holds already, over all its tokens. Sequence b has
+ * kv_len[b] tokens; the last n = q_start[b+1] - q_start[b] are new, rows q_start[b]
+ * .. of Q. Row i of them sits at p = kv_len[b] - n + i and sees the tokens j <= p,
+ * with a window only those with j > p - window. For each of the Hq heads (head h
+ * reads key head h / (Hq / Hkv)):
+ *   s_j = scale * q . k_j,  lse = log sum_j exp(s_j),  O = sum_j exp(s_j - lse) v_j.
+ *   One call takes prompts, chunks of them and single tokens in any mixture.
+ *   Q, O        bf16 [T, Hq, D]; O may be Q (same stride).
+ *   page_table  int32 [B, max_pages] (rows table_stride bytes apart): the page of
+ *               tokens i * page_size .. of a sequence. What lies past its length is
+ *               not read.
+ *   kv_len      int32 [B], at most max_pages * page_size; q_start int32 [B + 1],
+ *               rising. Rows of Q before q_start[0] and from q_start[B] on are
+ *               padding: their outputs are left as they were.
+ *   lse         float [T, Hq], natural logarithm, or null.
+ *   max_q       at least every n: what the launch is sized for (a sequence's tokens
+ *               past it are left out). window 0: none.
+ *   D is 64, 128 or 256; Hq % Hkv == 0; max_pages * page_size <= SKGEMM_MAX_LEN; T
+ *   * (Hq / Hkv) <= 2^30, B <= 2^20, and B * Hkv * (max_pages * page_size / 64 + 1)
+ *   and (T * (Hq / Hkv) / 128 + B) * Hkv below 2^31 (SKGEMM_ESHAPE). 0 < scale <=
+ *   SKGEMM_MAX_SCALE, also times k_scale. Q and O are 16-byte aligned with strides
+ *   that are multiples of 16; arrays of int32 and float 4.
+ * The lengths are read on the device, so a captured call may be replayed with
+ * others. It uses the workspace above (skgemm_reserve_ops before a capture).
+ * Sums, maxima and O are FP32; the probabilities are rounded to bf16 for the product
+ * with V. A row that sees no token (p < 0) has O 0 and lse -inf, and so has one
+ * whose scores are all below -1e30. Tokens that a row does not see have no part in
+ * it, whatever their keys and values hold; an infinity or a NaN in a key that it
+ * sees makes the row NaN (a score of -inf: probability 0), in a value that output
+ * NaN or infinite. A page id outside 0 .. n_pages - 1 is not read; rows that see its
+ * tokens are NaN, and others of their sequence may be.
+ */
+SKGEMM_API int skgemm_paged_attention(const void* Q, const void* K_cache, const void* V_cache,
+                                      const int32_t* page_table, const int32_t* kv_len,
+                                      const int32_t* q_start, void* O, float* lse, int T, int B,
+                                      int max_q, int Hq, int Hkv, int D, int n_pages,
+                                      int page_size, int max_pages, float scale, int window,
+                                      int cache_format, float k_scale, float v_scale,
+                                      size_t q_stride, size_t o_stride, size_t table_stride,
+                                      size_t page_stride, size_t slot_stride, size_t head_stride,
+                                      hipStream_t stream);
 
 /* skgemm_reserve_ops: allocate the stream's workspace of the calls above now
  * (they cannot allocate it while the stream is captured: SKGEMM_ENOMEM). */

@@ -86,3 +86,55 @@ def logprobs_grad_ref(logits, tokens, lse, entropy, g, gh, scale):
     safe = np.where(p > 0, lp, 0.0)
     d = scale * (gg[:, None] * (hit - p) - gh[:, None] * np.where(p > 0, p * (safe + entropy[:, None]), 0.0))
     return d, p, safe
+
+
+def rope_ref(x, gain, freq, pos, rot, layout, eps=1e-6, amplitude=1.0):
+    """Heads [T, H, D]: normed with a gain (not None), then the first `rot` values of
+    each turned by pos * freq. Also the size of what each output sums: |a| + |b| of its
+    pair after the norm, |x| outside the rotated part."""
+    y = x.astype(np.float64)
+    if gain is not None:
+        big = np.maximum(np.abs(y).max(axis=2, keepdims=True), 1e-300)
+        z = y / big
+        y = z / np.sqrt(np.mean(z * z, axis=2, keepdims=True) + eps / big / big) * gain.astype(np.float64)
+    size = np.abs(y)
+    if rot == 0:
+        return y, size
+    w = pos.astype(np.float64)[:, None] * freq.astype(np.float64)[None, :]
+    c, s = amplitude * np.cos(w)[:, None, :], amplitude * np.sin(w)[:, None, :]
+    half = rot // 2
+    ia, ib = (np.arange(half), half + np.arange(half)) if layout == "half" else (2 * np.arange(half), 2 * np.arange(half) + 1)
+    out = y.copy()
+    out[..., ia] = y[..., ia] * c - y[..., ib] * s
+    out[..., ib] = y[..., ib] * c + y[..., ia] * s
+    both = abs(amplitude) * (size[..., ia] + size[..., ib])
+    size = size.copy()
+    size[..., ia] = size[..., ib] = both
+    return out, size
+
+
+def attention_ref(q, k, v, scale, window=0):
+    """One sequence: q [n, Hq, D] of its last n tokens, k and v [L, Hkv, D]. Returns o
+    [n, Hq, D], lse [n, Hq], A = sum p |v| and the largest sum |q_i k_i| * scale of
+    what a row sees. Keys that a row does not see are not multiplied at all; a row that
+    sees none has o 0 and lse -inf."""
+    n, Hq, D = q.shape
+    L, Hkv, _ = k.shape
+    o, A = np.zeros((n, Hq, D)), np.zeros((n, Hq, D))
+    lse, size = np.full((n, Hq), -np.inf), np.zeros((n, Hq))
+    for i in range(n):
+        p = L - n + i
+        lo = max(0, p + 1 - window) if window else 0
+        if p < lo:
+            continue
+        for h in range(Hq):
+            g = h // (Hq // Hkv)
+            kk, vv = k[lo : p + 1, g].astype(np.float64), v[lo : p + 1, g].astype(np.float64)
+            s = scale * (kk @ q[i, h].astype(np.float64))
+            m = s.max()
+            e = np.exp(s - m)
+            w = e / e.sum()
+            o[i, h], A[i, h] = w @ vv, w @ np.abs(vv)
+            lse[i, h] = m + np.log(e.sum())
+            size[i, h] = scale * (np.abs(kk) @ np.abs(q[i, h].astype(np.float64))).max()
+    return o, lse, A, size

@@ -34,6 +34,9 @@ KNOBS = {"kind": 0, "stream": 1, "shape": 2, "fold": 3, "cluster_c": 4, "wg_per_
 # Element formats (include/skgemm.h, enum skgemm_format)
 FORMATS = {"bf16": 0, "i8": 1, "e4m3": 2, "f32": 3}
 
+# Which values of a head turn together (include/skgemm.h, enum skgemm_rope_layout)
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+
 _lib = None
 _raw_stream = _device = None  # torch's functions, bound by the first call that asks for the stream
 _torch_types = {}  # torch's element types that an operator's argument may have, filled by the first call
@@ -46,7 +49,7 @@ class SkgemmError(RuntimeError):
 
 
 def _declare(lib):
-    vp, i, sz, st = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
+    vp, i, sz, st, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float
     sig = {
         "skgemm_bf16": [vp, vp, vp, i, i, i, i, st],
         "skgemm_mxfp4": [vp, vp, vp, vp, i, i, i, i, st],
@@ -75,12 +78,15 @@ def _declare(lib):
         "skgemm_logprobs": [vp, vp, vp, vp, vp, vp, vp, i, i, i, ctypes.c_float, i, sz, st],
         "skgemm_logprobs_grad": [vp, vp, vp, vp, vp, vp, vp, i, i, ctypes.c_float, i, sz, sz, st],
         "skgemm_reserve_ops": [st],
+        "skgemm_rope": [vp, vp, vp, vp, vp, i, i, i, i, i, f, f, sz, sz, st],
+        "skgemm_rope_append": [vp] * 11 + [i] * 8 + [f, f, i, f, f] + [sz] * 7 + [st],
+        "skgemm_paged_attention": [vp] * 8 + [i] * 9 + [f, i, i, f, f] + [sz] * 6 + [st],
         "skgemm_rmsnorm": [vp, vp, vp, vp, vp, vp, i, i, ctypes.c_float, i, sz, sz, sz, sz, st],
     }
     for name, args in sig.items():
-        f = getattr(lib, name)
-        f.argtypes = args
-        f.restype = ctypes.c_int
+        fn = getattr(lib, name)
+        fn.argtypes = args
+        fn.restype = ctypes.c_int
     lib.skgemm_strerror.argtypes = [ctypes.c_int]
     lib.skgemm_strerror.restype = ctypes.c_char_p
 
@@ -128,6 +134,7 @@ def _types() -> dict:
         import torch as t
 
         _torch_types.update(bf16=(2, (t.bfloat16,)), f32=(4, (t.float32,)), i64=(8, (t.int64,)), i8=(1, (t.int8,)),
+                            i32=(4, (t.int32,)),
                             i8_out=(1, (t.int8, t.uint8)), e4m3_out=(1, (t.uint8, t.float8_e4m3fn)))
     return _torch_types
 
@@ -420,6 +427,132 @@ def skgemm_logprobs_grad(logits, tokens, lse, entropy, g_logprob, g_entropy, d_l
                                       _ptr(g_entropy, 4 * _n(T), "g_entropy", f32), d, T, V, scale, f, zs, ds,
                                       _stream(stream))
     _check(code, "skgemm_logprobs_grad")
+
+
+def _heads(a, rows: int, heads: int, D: int, stride, what: str):
+    """_rows of bfloat16 heads [rows, heads, D] or [rows, heads * D]; a token's heads
+    lie one after another."""
+    if a is not None and not isinstance(a, int) and a.dim() == 3 and not a.is_contiguous():
+        if (a.stride(2) != 1 and a.shape[2] > 1) or (a.stride(1) != a.shape[2] and a.shape[1] > 1):
+            raise SkgemmError(SKGEMM_EINVAL, f"{what}: a token's heads are not contiguous")
+        a = a.as_strided((a.shape[0], a.shape[1] * a.shape[2]), (a.stride(0), 1))
+    return _rows(a, rows, 2 * heads * D, stride, what, (_torch_types or _types())["bf16"])
+
+
+def _layout(name) -> int:
+    if isinstance(name, str):
+        if name not in ROPE_LAYOUTS:
+            raise SkgemmError(SKGEMM_EINVAL, f"unknown layout {name!r}, one of {sorted(ROPE_LAYOUTS)}")
+        return ROPE_LAYOUTS[name]
+    return int(name)
+
+
+def _here(a, what: str) -> None:
+    """A tensor of another GPU than the current one, where the call is launched."""
+    if a is not None and not isinstance(a, int) and _device is not None and a.is_cuda and a.get_device() != _device():
+        raise SkgemmError(SKGEMM_EINVAL, f"{what}: a tensor on {a.device}, the current device is {_device()}")
+
+
+def _pages(K, V, n_pages: int, page_size: int, Hkv: int, D: int, fmt, strides):
+    """(addresses of K and V, format, page, token and head stride in bytes) of a paged
+    cache: 4-D tensors [pages, page_size, Hkv, D] of bfloat16, or float8_e4m3fn or
+    uint8 codes, in any order in memory as long as a head's values are contiguous and
+    both are laid out alike. `strides` are of addresses (None: dense in that order)."""
+    ty = _torch_types or _types()
+    if fmt is None:
+        fmt = 2 if K is not None and not isinstance(K, int) and K.element_size() == 1 else 0
+    fmt = _format(fmt)
+    types = ty["e4m3_out"] if fmt == 2 else ty["bf16"]
+    ptr = []
+    for a, what in ((K, "K_cache"), (V, "V_cache")):
+        if a is None or isinstance(a, int):
+            ptr.append(a or 0)
+            continue
+        if not a.is_cuda:
+            raise SkgemmError(SKGEMM_EINVAL, f"{what}: a tensor on {a.device}, not on the GPU")
+        if a.dtype not in types[1]:
+            raise _wrong_type(a, types, what)
+        n, p, h, d = a.shape if a.dim() == 4 else (0, 0, 0, 0)
+        if n < n_pages or p != page_size or h != Hkv or d != D:
+            raise SkgemmError(SKGEMM_EINVAL, f"{what}: {tuple(a.shape)}, the call needs {(n_pages, page_size, Hkv, D)}")
+        s = a.stride()
+        if s[3] != 1:
+            raise SkgemmError(SKGEMM_EINVAL, f"{what}: a head's values are not contiguous")
+        own = (s[0] * types[0], s[1] * types[0], s[2] * types[0])
+        if strides is None:
+            strides = own
+        elif any(i != j for i, j, size in zip(strides, own, (n_pages, p, h)) if size > 1):
+            raise SkgemmError(SKGEMM_EINVAL, f"{what}: strides {own} bytes, not {tuple(strides)}")
+        ptr.append(a.data_ptr())
+    if strides is None:
+        row = max(0, D) * types[0]
+        strides = (max(0, page_size) * max(0, Hkv) * row, max(0, Hkv) * row, row)
+    if min(strides) < 0:
+        raise SkgemmError(SKGEMM_EINVAL, "cache: a negative stride")
+    return ptr[0], ptr[1], fmt, *strides
+
+
+def skgemm_rope(X, G, inv_freq, positions, Y, T: int, H: int, D: int, rot: int, layout="half", eps: float = 1e-6,
+                amplitude: float = 1.0, x_stride=None, y_stride=None, stream=None) -> None:
+    """Y = X with each head normed (G not None) and its first `rot` values rotated by
+    positions[t] * inv_freq (rot > 0), amplitude times. X, Y (may be X) and G are
+    bfloat16, inv_freq float32, positions int64; layout "half" or "interleaved"."""
+    ty = _torch_types or _types()
+    x, xs = _heads(X, T, H, D, x_stride, "X")
+    y, ys = _heads(Y, T, H, D, y_stride, "Y")
+    st = _stream(stream)
+    _here(X, "X")
+    code = lib().skgemm_rope(x, _ptr(G, 2 * _n(D), "G", ty["bf16"]), _ptr(inv_freq, 2 * _n(rot), "inv_freq", ty["f32"]),
+                             _ptr(positions, 8 * _n(T), "positions", ty["i64"]), y, T, H, D, rot, _layout(layout), eps,
+                             amplitude, xs, ys, st)
+    _check(code, "skgemm_rope")
+
+
+def skgemm_rope_append(Q, K, V, Gq, Gk, inv_freq, positions, slots, Q_out, K_cache, V_cache, T: int, Hq: int, Hkv: int,
+                       D: int, n_pages: int, page_size: int, rot: int, layout="half", eps: float = 1e-6,
+                       amplitude: float = 1.0, k_scale: float = 1.0, v_scale: float = 1.0, cache_format=None, q_stride=None,
+                       k_stride=None, v_stride=None, q_out_stride=None, cache_strides=None, stream=None) -> None:
+    """skgemm_rope of Q into Q_out and of K into the paged cache at slots[t], and V as
+    it is into the cache. The caches are bfloat16, or E4M3 codes of value / k_scale
+    (v_scale); see _pages for their layout (cache_strides: page, token and head stride
+    in bytes). slots is int64, below 0: not stored."""
+    ty = _torch_types or _types()
+    bf16, i64 = ty["bf16"], ty["i64"]
+    q, qs = _heads(Q, T, Hq, D, q_stride, "Q")
+    k, ks = _heads(K, T, Hkv, D, k_stride, "K")
+    v, vs = _heads(V, T, Hkv, D, v_stride, "V")
+    o, os_ = _heads(Q_out, T, Hq, D, q_out_stride, "Q_out")
+    kc, vc, f, page, slot, head = _pages(K_cache, V_cache, n_pages, page_size, Hkv, D, cache_format, cache_strides)
+    st = _stream(stream)
+    _here(K, "K")
+    code = lib().skgemm_rope_append(q, k, v, _ptr(Gq, 2 * _n(D), "Gq", bf16), _ptr(Gk, 2 * _n(D), "Gk", bf16),
+                                    _ptr(inv_freq, 2 * _n(rot), "inv_freq", ty["f32"]),
+                                    _ptr(positions, 8 * _n(T), "positions", i64), _ptr(slots, 8 * _n(T), "slots", i64), o, kc,
+                                    vc, T, Hq, Hkv, D, n_pages, page_size, rot, _layout(layout), eps, amplitude, f, k_scale,
+                                    v_scale, qs, ks, vs, os_, page, slot, head, st)
+    _check(code, "skgemm_rope_append")
+
+
+def skgemm_paged_attention(Q, K_cache, V_cache, page_table, kv_len, q_start, O, lse, T: int, B: int, max_q: int, Hq: int,  # noqa: E741
+                           Hkv: int, D: int, n_pages: int, page_size: int, max_pages: int, scale: float, window: int = 0,
+                           k_scale: float = 1.0, v_scale: float = 1.0, cache_format=None, q_stride=None, o_stride=None,
+                           table_stride=None, cache_strides=None, stream=None) -> None:
+    """Causal attention of the new tokens q_start[b] .. q_start[b + 1] of each sequence
+    over its kv_len[b] tokens in the paged cache (which holds them already); O is
+    bfloat16 (may be Q), lse float32 or None. page_table, kv_len and q_start are int32."""
+    ty = _torch_types or _types()
+    i32 = ty["i32"]
+    q, qs = _heads(Q, T, Hq, D, q_stride, "Q")
+    o, os_ = _heads(O, T, Hq, D, o_stride, "O")
+    t, ts = _rows(page_table, B, 4 * max_pages, table_stride, "page_table", i32)
+    kc, vc, f, page, slot, head = _pages(K_cache, V_cache, n_pages, page_size, Hkv, D, cache_format, cache_strides)
+    st = _stream(stream)
+    _here(Q, "Q")
+    code = lib().skgemm_paged_attention(q, kc, vc, t, _ptr(kv_len, 4 * _n(B), "kv_len", i32),
+                                        _ptr(q_start, 4 * _n(B + 1), "q_start", i32), o,
+                                        _ptr(lse, 4 * _n(T, Hq), "lse", ty["f32"]), T, B, max_q, Hq, Hkv, D, n_pages, page_size,
+                                        max_pages, scale, window, f, k_scale, v_scale, qs, os_, ts, page, slot, head, st)
+    _check(code, "skgemm_paged_attention")
 
 
 def skgemm_mxfp8_dequant(Wq8, Wscale, W_out, N: int, K: int, stream=None) -> None:

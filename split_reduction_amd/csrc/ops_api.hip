@@ -79,6 +79,66 @@ int check_logits(const void* logits, int T, int V, float scale, int format, size
   return SKGEMM_OK;
 }
 
+// Rows of heads: `needed` and, with more than one row, their stride.
+int check_heads(const void* a, int T, size_t row, size_t stride, bool written) {
+  if (a == nullptr) return SKGEMM_EINVAL;
+  if (!aligned(a, 16) || (T > 1 && stride % 16 != 0)) return SKGEMM_EALIGN;
+  return written && T > 1 && stride < row ? SKGEMM_EINVAL : SKGEMM_OK;
+}
+
+// The rotation's and the norm's own arguments.
+int check_turn(int D, int rot, int layout, bool norm, float eps, float amplitude) {
+  if (layout != SKGEMM_ROPE_HALF && layout != SKGEMM_ROPE_INTERLEAVED) return SKGEMM_EINVAL;
+  if (rot < 0 || D < 0 || !(amplitude > -INFINITY) || !(amplitude < INFINITY)) return SKGEMM_EINVAL;
+  if (norm && (!(eps >= 1e-30f) || !(eps < INFINITY))) return SKGEMM_EINVAL;
+  if (D % 16 != 0 || D < 16 || D > 256 || rot % 16 != 0 || rot > D) return SKGEMM_ESHAPE;
+  return SKGEMM_OK;
+}
+
+// A paged cache's own arguments.
+int check_cache(const void* K, const void* V, int Hkv, int D, int n_pages, int page_size, int format, float k_scale,
+                float v_scale, size_t page_stride, size_t slot_stride, size_t head_stride, bool written) {
+  if (format != SKGEMM_BF16 && format != SKGEMM_E4M3) return SKGEMM_EINVAL;
+  if (!(k_scale >= 1e-30f) || !(k_scale <= 1e30f) || !(v_scale >= 1e-30f) || !(v_scale <= 1e30f)) return SKGEMM_EINVAL;
+  if (format == SKGEMM_BF16 && (k_scale != 1.0f || v_scale != 1.0f)) return SKGEMM_EINVAL;
+  if (n_pages < 1 || page_size < 1 || K == nullptr || V == nullptr) return SKGEMM_EINVAL;
+  if ((page_size & (page_size - 1)) != 0 || page_size > SKGEMM_MAX_PAGE) return SKGEMM_ESHAPE;
+  if (!aligned(K, 16) || !aligned(V, 16)) return SKGEMM_EALIGN;
+  // (count, stride) of the axes that have more than one place.
+  struct Axis {
+    size_t count, stride;
+  } axes[3];
+  int n = 0;
+  const Axis all[3] = {{(size_t)n_pages, page_stride}, {(size_t)page_size, slot_stride}, {(size_t)Hkv, head_stride}};
+  for (const Axis& a : all) {
+    if (a.count < 2) continue;
+    if (a.stride % 16 != 0) return SKGEMM_EALIGN;
+    axes[n++] = a;
+  }
+  const size_t row = (size_t)D * (format == SKGEMM_BF16 ? 2 : 1);
+  const size_t limit = (size_t)1 << 32;
+  if ((page_size > 1 && slot_stride >= limit) || (Hkv > 1 && head_stride >= limit) ||
+      (n_pages > 1 && page_stride >= ((size_t)1 << 44)))
+    return SKGEMM_ESHAPE;
+  if ((page_size > 1 ? (size_t)(page_size - 1) * slot_stride : 0) + (Hkv > 1 ? (size_t)(Hkv - 1) * head_stride : 0) + row >= limit)
+    return SKGEMM_ESHAPE;
+  if (!written) return SKGEMM_OK;
+  for (int i = 1; i < n; ++i)
+    for (int j = i; j > 0 && axes[j].stride < axes[j - 1].stride; --j) {
+      const Axis a = axes[j];
+      axes[j] = axes[j - 1];
+      axes[j - 1] = a;
+    }
+  size_t span = row;
+  for (int i = 0; i < n; ++i) {
+    if (axes[i].stride < span) return SKGEMM_EINVAL;
+    span += (axes[i].count - 1) * axes[i].stride;
+  }
+  return SKGEMM_OK;
+}
+
+int log2_of(int v) { return __builtin_ctz((unsigned)v); }
+
 }  // namespace
 
 int skg::release_ops_workspaces() {
@@ -258,6 +318,175 @@ SKGEMM_API int skgemm_logprobs_grad(const void* logits, const int64_t* tokens, c
   p.V = V;
   p.scale = scale;
   const hipError_t e = skg::launch_logprobs_grad(p, logits_format == SKGEMM_F32, stream);
+  return e == hipSuccess ? SKGEMM_OK : skg::hip_fail(e);
+}
+
+SKGEMM_API int skgemm_rope(const void* X, const void* G, const float* inv_freq,
+                           const int64_t* positions, void* Y, int T, int H, int D, int rot,
+                           int layout, float eps, float amplitude, size_t x_stride,
+                           size_t y_stride, hipStream_t stream) {
+  if (T < 0 || H < 0) return SKGEMM_EINVAL;
+  int rc = check_turn(D, rot, layout, G != nullptr, eps, amplitude);
+  if (rc != SKGEMM_OK) return rc;
+  if (T > SKGEMM_MAX_ROWS || H > SKGEMM_MAX_HEADS) return SKGEMM_ESHAPE;
+  if (T == 0 || H == 0) return SKGEMM_OK;
+  const size_t row = (size_t)H * D * 2;
+  if ((rc = check_heads(X, T, row, x_stride, false)) != SKGEMM_OK) return rc;
+  if ((rc = check_heads(Y, T, row, y_stride, true)) != SKGEMM_OK) return rc;
+  if (rot > 0 && (inv_freq == nullptr || positions == nullptr)) return SKGEMM_EINVAL;
+  if (!aligned(G, 16) || !aligned(inv_freq, 4) || !aligned(positions, 8)) return SKGEMM_EALIGN;
+  if (Y == X && T > 1 && x_stride != y_stride) return SKGEMM_EINVAL;
+  skg::RopeParams p{};
+  p.q = static_cast<const uint8_t*>(X);
+  p.gq = static_cast<const uint8_t*>(G);
+  p.freq = inv_freq;
+  p.pos = positions;
+  p.q_out = static_cast<uint8_t*>(Y);
+  p.q_stride = x_stride;
+  p.q_out_stride = y_stride;
+  p.T = T;
+  p.Hq = H;
+  p.D = D;
+  p.rot = rot;
+  p.eps = eps;
+  p.amplitude = amplitude;
+  const hipError_t e = skg::launch_rope(p, layout == SKGEMM_ROPE_INTERLEAVED, false, stream);
+  return e == hipSuccess ? SKGEMM_OK : skg::hip_fail(e);
+}
+
+SKGEMM_API int skgemm_rope_append(const void* Q, const void* K, const void* V, const void* Gq,
+                                  const void* Gk, const float* inv_freq,
+                                  const int64_t* positions, const int64_t* slots, void* Q_out,
+                                  void* K_cache, void* V_cache, int T, int Hq, int Hkv, int D,
+                                  int n_pages, int page_size, int rot, int layout, float eps,
+                                  float amplitude, int cache_format, float k_scale, float v_scale,
+                                  size_t q_stride, size_t k_stride, size_t v_stride,
+                                  size_t q_out_stride, size_t page_stride, size_t slot_stride,
+                                  size_t head_stride, hipStream_t stream) {
+  if (T < 0 || Hq < 0 || Hkv < 0) return SKGEMM_EINVAL;
+  int rc = check_turn(D, rot, layout, (Gq != nullptr && Hq > 0) || (Gk != nullptr && Hkv > 0), eps, amplitude);
+  if (rc != SKGEMM_OK) return rc;
+  if (T > SKGEMM_MAX_ROWS || Hq > SKGEMM_MAX_HEADS || Hkv > SKGEMM_MAX_HEADS) return SKGEMM_ESHAPE;
+  if (T == 0 || (Hq == 0 && Hkv == 0)) return SKGEMM_OK;
+  if (Hq > 0) {
+    const size_t row = (size_t)Hq * D * 2;
+    if ((rc = check_heads(Q, T, row, q_stride, false)) != SKGEMM_OK) return rc;
+    if ((rc = check_heads(Q_out, T, row, q_out_stride, true)) != SKGEMM_OK) return rc;
+    if (Q_out == Q && T > 1 && q_stride != q_out_stride) return SKGEMM_EINVAL;
+  }
+  if (Hkv > 0) {
+    const size_t row = (size_t)Hkv * D * 2;
+    if ((rc = check_heads(K, T, row, k_stride, false)) != SKGEMM_OK) return rc;
+    if ((rc = check_heads(V, T, row, v_stride, false)) != SKGEMM_OK) return rc;
+    rc = check_cache(K_cache, V_cache, Hkv, D, n_pages, page_size, cache_format, k_scale, v_scale, page_stride, slot_stride,
+                     head_stride, true);
+    if (rc != SKGEMM_OK) return rc;
+    if (slots == nullptr || K_cache == V_cache) return SKGEMM_EINVAL;
+  }
+  if (rot > 0 && (inv_freq == nullptr || positions == nullptr)) return SKGEMM_EINVAL;
+  if (!aligned(Gq, 16) || !aligned(Gk, 16) || !aligned(inv_freq, 4) || !aligned(positions, 8) || !aligned(slots, 8))
+    return SKGEMM_EALIGN;
+  skg::RopeParams p{};
+  p.q = static_cast<const uint8_t*>(Q);
+  p.k = static_cast<const uint8_t*>(K);
+  p.v = static_cast<const uint8_t*>(V);
+  p.gq = static_cast<const uint8_t*>(Gq);
+  p.gk = static_cast<const uint8_t*>(Gk);
+  p.freq = inv_freq;
+  p.pos = positions;
+  p.slots = slots;
+  p.q_out = static_cast<uint8_t*>(Q_out);
+  p.kc = static_cast<uint8_t*>(K_cache);
+  p.vc = static_cast<uint8_t*>(V_cache);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_out_stride = q_out_stride;
+  p.page_stride = page_stride;
+  p.slot_stride = slot_stride;
+  p.head_stride = head_stride;
+  p.T = T;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.rot = rot;
+  p.eps = eps;
+  p.amplitude = amplitude;
+  if (Hkv > 0) {
+    p.n_slots = (int64_t)n_pages * page_size;
+    p.page_shift = log2_of(page_size);
+    p.k_inv = 1.0f / k_scale;
+    p.v_inv = 1.0f / v_scale;
+  }
+  const hipError_t e = skg::launch_rope(p, layout == SKGEMM_ROPE_INTERLEAVED, Hkv > 0 && cache_format == SKGEMM_E4M3, stream);
+  return e == hipSuccess ? SKGEMM_OK : skg::hip_fail(e);
+}
+
+SKGEMM_API int skgemm_paged_attention(const void* Q, const void* K_cache, const void* V_cache,
+                                      const int32_t* page_table, const int32_t* kv_len,
+                                      const int32_t* q_start, void* O, float* lse, int T, int B,
+                                      int max_q, int Hq, int Hkv, int D, int n_pages,
+                                      int page_size, int max_pages, float scale, int window,
+                                      int cache_format, float k_scale, float v_scale,
+                                      size_t q_stride, size_t o_stride, size_t table_stride,
+                                      size_t page_stride, size_t slot_stride, size_t head_stride,
+                                      hipStream_t stream) {
+  if (T < 0 || B < 0 || max_q < 0 || Hq < 0 || Hkv < 0 || D < 0 || n_pages < 0 || max_pages < 0 || window < 0) return SKGEMM_EINVAL;
+  if (!(scale > 0.0f) || !(scale <= SKGEMM_MAX_SCALE)) return SKGEMM_EINVAL;
+  if (D != 64 && D != 128 && D != 256) return SKGEMM_ESHAPE;
+  if (T == 0 || B == 0 || max_q == 0 || Hq == 0) return SKGEMM_OK;
+  if (Hkv == 0 || Hq % Hkv != 0 || Hq > SKGEMM_MAX_HEADS || T > SKGEMM_MAX_ROWS || B > (1 << 20)) return SKGEMM_ESHAPE;
+  int rc = check_cache(K_cache, V_cache, Hkv, D, n_pages, page_size, cache_format, k_scale, v_scale, page_stride, slot_stride,
+                       head_stride, false);
+  if (rc != SKGEMM_OK) return rc;
+  const int64_t most = (int64_t)1 << 31, G = Hq / Hkv, len = (int64_t)max_pages * page_size;
+  if (len > SKGEMM_MAX_LEN || T * G > ((int64_t)1 << 30) || B * (int64_t)Hkv * (len / 64 + 1) >= most ||
+      (T * G / 128 + B) * Hkv >= most)
+    return SKGEMM_ESHAPE;
+  const float c = scale * k_scale;
+  if (!(c >= 1e-37f) || !(c <= SKGEMM_MAX_SCALE)) return SKGEMM_EINVAL;
+  const size_t row = (size_t)Hq * D * 2;
+  if ((rc = check_heads(Q, T, row, q_stride, false)) != SKGEMM_OK) return rc;
+  if ((rc = check_heads(O, T, row, o_stride, true)) != SKGEMM_OK) return rc;
+  if (O == Q && T > 1 && q_stride != o_stride) return SKGEMM_EINVAL;
+  if (kv_len == nullptr || q_start == nullptr || (page_table == nullptr && max_pages > 0)) return SKGEMM_EINVAL;
+  if (!aligned(page_table, 4) || !aligned(kv_len, 4) || !aligned(q_start, 4) || !aligned(lse, 4) || (B > 1 && table_stride % 4 != 0))
+    return SKGEMM_EALIGN;
+  skg::AttnParams p{};
+  p.q = static_cast<const uint8_t*>(Q);
+  p.kc = static_cast<const uint8_t*>(K_cache);
+  p.vc = static_cast<const uint8_t*>(V_cache);
+  p.table = page_table;
+  p.kv_len = kv_len;
+  p.q_start = q_start;
+  p.o = static_cast<uint8_t*>(O);
+  p.lse = lse;
+  p.q_stride = q_stride;
+  p.o_stride = o_stride;
+  p.table_stride = table_stride;
+  p.page_stride = page_stride;
+  p.slot_stride = (uint32_t)slot_stride;
+  p.head_stride = (uint32_t)head_stride;
+  p.T = T;
+  p.B = B;
+  p.max_q = max_q < T ? max_q : T;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = (int)G;
+  p.n_pages = n_pages;
+  p.page_shift = log2_of(page_size);
+  p.max_len = (int)len;
+  // One that no sequence is longer than hides nothing, and differences to a token's
+  // place stay inside 32 bits without it (place >= 1 - T).
+  p.window = window < len ? window : 0;
+  p.c = c * 1.4426950408889634f;
+  p.v_scale = v_scale;
+  uint8_t* w = nullptr;
+  rc = ops_workspace(stream, &w);
+  if (rc != SKGEMM_OK) return rc;
+  p.part = w;
+  p.cnt = reinterpret_cast<uint32_t*>(w + skg::kOpsPartBytes);
+  const hipError_t e = skg::launch_attention(p, D, cache_format == SKGEMM_E4M3, stream);
   return e == hipSuccess ? SKGEMM_OK : skg::hip_fail(e);
 }
 

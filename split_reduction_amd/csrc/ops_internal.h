@@ -74,6 +74,41 @@ struct LogprobGradParams {
   float scale;
 };
 
+struct RopeParams {
+  const uint8_t *q, *k, *v;  // bf16 rows of heads; k, v null where Hkv is 0
+  const uint8_t *gq, *gk;    // bf16 [D] or null: no norm
+  const float* freq;         // [rot / 2]
+  const int64_t* pos;        // [T]
+  const int64_t* slots;      // [T], below 0: not stored
+  uint8_t *q_out, *kc, *vc;
+  size_t q_stride, k_stride, v_stride, q_out_stride;   // bytes between tokens
+  size_t page_stride, slot_stride, head_stride;        // bytes, of both caches
+  int64_t n_slots;
+  int T, Hq, Hkv, D, rot, page_shift;
+  float eps, amplitude, k_inv, v_inv;
+  int tokens, per;  // tokens of a workgroup; heads of one (blockIdx.y takes the next)
+};
+
+struct AttnParams {
+  const uint8_t* q;        // bf16 [T, Hq, D]
+  const uint8_t *kc, *vc;  // bf16 or E4M3 pages
+  const int32_t* table;    // [B, max_pages]
+  const int32_t* kv_len;   // [B]
+  const int32_t* q_start;  // [B + 1]
+  uint8_t* o;              // bf16 [T, Hq, D]
+  float* lse;              // [T, Hq] or null
+  size_t q_stride, o_stride, table_stride, page_stride;  // bytes
+  uint32_t slot_stride, head_stride;
+  int T, B, max_q, Hq, Hkv, G, n_pages, page_shift, max_len, window;
+  float c, v_scale;  // scale * k_scale / log 2
+  int few;           // rows (new tokens x G) of a sequence that attn_few_kernel takes
+  int S;             // attn_rows_kernel: workgroups that split a tile's keys
+  uint8_t* part;     // their results
+  uint32_t* cnt;     // arrival counters, kOpsCounterStride words apart
+};
+
+hipError_t launch_rope(const RopeParams& p, bool inter, bool codes, hipStream_t s);
+hipError_t launch_attention(const AttnParams& p, int D, bool codes, hipStream_t s);
 hipError_t launch_logprobs(const LogprobParams& p, bool f32, hipStream_t s);
 hipError_t launch_logprobs_grad(LogprobGradParams p, bool f32, hipStream_t s);
 hipError_t launch_i8(const I8Params& p, const I8Tactic& t, hipStream_t s);
