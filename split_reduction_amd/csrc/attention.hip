@@ -54,9 +54,13 @@ __device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
 
 // 16 (4) bytes a lane from each lane's address into LDS at `lds` + 16 (4) l; see
 // ld16_to_lds for why in asm and who waits.
+template <bool STREAM>
 __device__ __forceinline__ void global16_to_lds(const uint8_t* p, uint32_t lds) {
 #ifdef __HIP_DEVICE_COMPILE__
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory", "m0");
+  if constexpr (STREAM)  // non-temporal
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt" ::"s"(lds), "v"(p) : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory", "m0");
 #endif
 }
 __device__ __forceinline__ void global4_to_lds(const uint8_t* p, uint32_t lds) {
@@ -113,34 +117,48 @@ __device__ __forceinline__ void issue_ids(const Pages& c, int base, int last, ui
   global4_to_lds(c.ids + 4 * (size_t)(uint32_t)(key >> c.shift), lds);
 }
 
-// Keys base .. base + KEYS - 1 and their values on their way into LDS, this wave's
-// share of WAVES. Past `last` that key is taken again. A page that does not exist
-// is not read (page 0 is) and reported.
+// This lane's part of keys base .. base + KEYS - 1, its wave's share of WAVES. Past
+// `last` that key is taken again. A page that does not exist is not read (page 0 is)
+// and reported.
 template <int D, bool F8, int KEYS, int WAVES>
-__device__ __forceinline__ bool issue_tile(const Pages& c, int base, int last, const uint32_t* ids, uint32_t lds, int wave, int lane) {
+struct Share {
   typedef Cache<D, F8> L;
-  constexpr int kLoads = KEYS / L::kRows / WAVES;
+  static constexpr int kLoads = KEYS / L::kRows / WAVES;
   static_assert(kLoads >= 1, "every wave has a share");
-  // The offsets below are the same for every tile; kept from one to the next they
-  // would take more registers than there are (D = 256: spills).
-  asm volatile("" : "+v"(lane));
-  bool bad = false;
+  uint32_t page[kLoads];
+  int base, last;
+
+  __device__ __forceinline__ bool find(const Pages& c, int first, int end, const uint32_t* ids, int wave, int lane) {
+    bool bad = false;
+    base = first;
+    last = end;
 #pragma unroll
-  for (int q = 0; q < kLoads; ++q) {
-    const int row = (wave * kLoads + q) * L::kRows + lane / L::kChunks, at = lane % L::kChunks;
-    const int key = min(base + row, last);
-    uint32_t id = ids[row];
-    if (id >= (uint32_t)c.n_pages) {
-      id = 0;
-      bad = true;
+    for (int q = 0; q < kLoads; ++q) {
+      page[q] = ids[(wave * kLoads + q) * L::kRows + lane / L::kChunks];
+      if (page[q] >= (uint32_t)c.n_pages) {
+        page[q] = 0;
+        bad = true;
+      }
     }
-    const size_t off = (size_t)id * c.page_stride + (size_t)((uint32_t)(key & ((1 << c.shift) - 1)) * c.slot_stride);
-    const uint32_t to = lds + (uint32_t)(wave * kLoads + q) * 1024u;
-    global16_to_lds(c.k + off + 16 * (at ^ L::key_swizzle(row)), to);
-    global16_to_lds(c.v + off + 16 * (at ^ L::value_swizzle(row)), to + KEYS * L::kRow);
+    return bad;
   }
-  return bad;
-}
+  // VALUES: the values, else the keys, to KEYS rows at `lds`. STREAM: nobody else
+  // reads them.
+  template <bool VALUES, bool STREAM>
+  __device__ __forceinline__ void issue(const Pages& c, uint32_t lds, int wave, int lane) const {
+    // What follows from the lane is the same for every tile; kept from one to the next
+    // it would take more registers than there are (D = 256: spills).
+    asm volatile("" : "+v"(lane));
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+      const int row = (wave * kLoads + q) * L::kRows + lane / L::kChunks, at = lane % L::kChunks;
+      const int chunk = at ^ (VALUES ? L::value_swizzle(row) : L::key_swizzle(row));
+      const uint32_t in_page = (uint32_t)(min(base + row, last) & ((1 << c.shift) - 1)) * c.slot_stride + 16u * (uint32_t)chunk;
+      global16_to_lds<STREAM>((VALUES ? c.v : c.k) + (size_t)page[q] * c.page_stride + in_page,
+                              lds + (uint32_t)(wave * kLoads + q) * 1024u);
+    }
+  }
+};
 
 // ---- a wave's rows ----
 
@@ -182,13 +200,13 @@ struct Rows {
     }
   }
 
-  // The steps of a product go in groups of four operands: a group is read from LDS
+  // The steps of a product go in groups of two or four operands: a group is read from LDS
   // while the one before is multiplied, and no further ahead (the compiler would
   // read everything at once and spill).
   static __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
 
   __device__ __forceinline__ void scores(f32x16 (&s)[RT][KB], const uint8_t* keys, int lane) const {
-    constexpr int kSteps = D / (F8 ? 32 : 16), kGroup = F8 ? 2 : 4, kGroups = KB * kSteps / kGroup;
+    constexpr int kSteps = D / (F8 ? 32 : 16), kGroup = F8 || D == 256 ? 2 : 4, kGroups = KB * kSteps / kGroup;
     const int r = lane & 31, h = lane >> 5, swz = L::key_swizzle(r);
     u32x4 w[2][kGroup];
     auto read = [&](int g) {
@@ -238,33 +256,35 @@ struct Rows {
     }
   }
 
-  // A tile of 32 KB keys from `base`. mask: some row does not see all of them. What
-  // it does not see has score -inf and probability 0; a value that is no number
-  // would still make a NaN of that 0. Such values are taken out of the tile, and the
+  // A tile of 32 KB keys from `base` of which some row does not see all: what it does
+  // not see has score -inf (hide) and probability 0. A value that is no number would
+  // still make a NaN of that 0. Such values are taken out of the tile, and the
   // outputs of rows that do see one are noted in `lost`. SHARE waves share the tile.
   template <int SHARE>
-  __device__ __forceinline__ void tile(const uint8_t* keys, uint32_t values, int base, bool mask, float c, int wave, int lane) {
-    const int h = lane >> 5;
-    f32x16 s[RT][KB];
-    scores(s, keys, lane);
-    if (mask) {
-#pragma unroll
-      for (int t = 0; t < RT; ++t)
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int key = base + 32 * kb + 8 * (e >> 2) + 4 * h + (e & 3);
-            s[t][kb][e] = key >= lo[t] && key < hi[t] ? s[t][kb][e] : -__builtin_inff();
-          }
-      if (any_not_finite(values, lane)) {  // the same in all waves that share the tile
-        note_lost(values, base, lane);
-        if constexpr (SHARE > 1) __syncthreads();
-        take_out(values, wave, SHARE, lane);
-        if constexpr (SHARE > 1) __syncthreads();
-      }
+  __device__ __forceinline__ void clean_values(uint32_t values, int base, int wave, int lane) {
+    if (any_not_finite(values, lane)) {  // the same in all waves that share the tile
+      note_lost(values, base, lane);
+      if constexpr (SHARE > 1) __syncthreads();
+      take_out(values, wave, SHARE, lane);
+      if constexpr (SHARE > 1) __syncthreads();
     }
-    bf16x8 p[RT][KB][2];
+  }
+
+  __device__ __forceinline__ void hide(f32x16 (&s)[RT][KB], int base, int lane) const {
+    const int h = lane >> 5;
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int key = base + 32 * kb + 8 * (e >> 2) + 4 * h + (e & 3);
+          s[t][kb][e] = key >= lo[t] && key < hi[t] ? s[t][kb][e] : -__builtin_inff();
+        }
+  }
+
+  // Scores to probabilities: maximum, sum and O rescaled where it grows.
+  __device__ __forceinline__ void softmax(f32x16 (&s)[RT][KB], bf16x8 (&p)[RT][KB][2], float c) {
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       float top = -__builtin_inff();
@@ -297,7 +317,6 @@ struct Rows {
         }
       }
     }
-    add_values(p, values, lane);
   }
 
   static constexpr int kTileLoads = 32 * KB * L::kRow / 1024;  // of 16 bytes a lane
@@ -372,7 +391,7 @@ struct Rows {
 
   // O += V^T P^T.
   __device__ __forceinline__ void add_values(const bf16x8 (&p)[RT][KB][2], uint32_t values, int lane) {
-    constexpr int kGroup = kDT < 4 ? kDT : 4, kGroups = 2 * KB * kDT / kGroup;
+    constexpr int kGroup = D == 128 ? 4 : 2, kGroups = 2 * KB * kDT / kGroup;
     bf16x8 v[2][kGroup];
     auto read = [&](int g) {
 #pragma unroll
@@ -549,11 +568,14 @@ __global__ __launch_bounds__(64 * W, W / 4) void attn_rows_kernel(AttnParams p) 
   const uint32_t data = lds_offset(lds), id_lds = lds_offset(&ids[wave][0][0]);
   bool bad = false;
   const int last = khi - 1;
+  Share<D, F8, 64, W> share;
   if (j0 < j1) {
     issue_ids<64>(c, kal + 64 * j0, last, id_lds, lane);
     issue_ids<64>(c, kal + 64 * (j0 + 1), last, id_lds + 256, lane);
     wait_vmem<0>();
-    bad = issue_tile<D, F8, 64, W>(c, kal + 64 * j0, last, ids[wave][0], data, wave, lane);
+    bad = share.find(c, kal + 64 * j0, last, ids[wave][0], wave, lane);
+    share.template issue<false, false>(c, data, wave, lane);
+    share.template issue<true, false>(c, data + kRowsKeys * L::kRow, wave, lane);
     issue_ids<64>(c, kal + 64 * (j0 + 2), last, id_lds, lane);
   }
   for (int j = j0; j < j1; ++j) {
@@ -561,12 +583,22 @@ __global__ __launch_bounds__(64 * W, W / 4) void attn_rows_kernel(AttnParams p) 
     wait_vmem<1>();  // this wave's share of tile j; the ids of j + 2 may be under way
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     if (j + 1 < j1) {
-      bad |= issue_tile<D, F8, 64, W>(c, base + 64, last, ids[wave][at ^ 1], data + (uint32_t)(at ^ 1) * kStage, wave, lane);
+      bad |= share.find(c, base + 64, last, ids[wave][at ^ 1], wave, lane);
+      share.template issue<false, false>(c, data + (uint32_t)(at ^ 1) * kStage, wave, lane);
+      share.template issue<true, false>(c, data + (uint32_t)(at ^ 1) * kStage + kRowsKeys * L::kRow, wave, lane);
       issue_ids<64>(c, base + 192, last, id_lds + (uint32_t)(at ^ 1) * 256, lane);
     }
     const uint8_t* const keys = lds + at * kStage;
     const uint32_t values = data + (uint32_t)at * kStage + kRowsKeys * L::kRow;
-    w.template tile<W>(keys, values, base, base + 64 > see_min || base < lo_max, p.c, wave, lane);
+    f32x16 s[1][2];
+    bf16x8 prob[1][2][2];
+    w.scores(s, keys, lane);
+    if (base + 64 > see_min || base < lo_max) {
+      w.hide(s, base, lane);
+      w.template clean_values<W>(values, base, wave, lane);
+    }
+    w.softmax(s, prob, p.c);
+    w.add_values(prob, values, lane);
   }
   wait_vmem<0>();
   w.lose();
@@ -637,12 +669,14 @@ __global__ __launch_bounds__(64 * W, W / 4) void attn_rows_kernel(AttnParams p) 
 // ---- few rows: at most 32 of a key head, the waves split the keys ----
 //
 // What counts is the cache's stream. Every sequence and key head is cut into units
-// of 32 keys a wave; the units of the whole call, one sequence after another, are
-// dealt out in equal runs to a fixed number of workgroups, whatever the lengths
-// are. A workgroup goes through its run head by head; its waves take the unit's
-// keys by 32, each through two buffers of its own with no barrier, and meet at the
-// head's end. A head that was cut between workgroups is joined by the last to
-// arrive, from slots in the workspace, in the order of its keys.
+// of 32 keys a wave, and one more for what a head costs beside its keys; the units
+// of the whole call, one sequence after another, are dealt out in equal runs to a
+// fixed number of workgroups, whatever the lengths are. A workgroup goes through
+// its run head by head; its waves take the unit's keys by 32, each through two
+// buffers of its own with no barrier, and meet at the head's end. The loads run two
+// tiles ahead of the products, into the next head where one ends. A head that was
+// cut between workgroups is joined by the last to arrive, from slots in the
+// workspace, in the order of its keys.
 
 constexpr int kFewRows = 32;
 
@@ -655,179 +689,320 @@ constexpr size_t few_slot() {
   return (size_t)kFewRows * (D + 2) * 4;
 }
 
-// Units of a sequence for each key head, and the first key.
-__device__ __forceinline__ int few_units(const AttnParams& p, const Seq& s, int unit, int* first) {
+constexpr uint32_t kHeadUnits = 3;  // what a head costs beside its keys, in units
+constexpr uint32_t kFewShare = 4;   // units of a workgroup at least: a join costs about as much
+
+// Units of keys of a sequence for each key head, and the first key.
+__device__ __forceinline__ uint32_t few_units(const AttnParams& p, const Seq& s, int unit, int* first) {
+  *first = 0;
   if (s.n == 0 || s.n * p.G > p.few) return 0;
   const int lo = p.window > 0 ? max(0, s.L - s.n + 1 - p.window) & ~31 : 0;
   *first = lo;
-  return s.L > lo ? (s.L - lo + unit - 1) / unit : 1;  // a row that sees no key is written too
+  return s.L > lo ? (uint32_t)(s.L - lo + unit - 1) / (uint32_t)unit : 1;  // a row that sees no key is written too
+}
+__device__ __forceinline__ uint32_t few_cost(uint32_t units) { return units == 0 ? 0 : units + kHeadUnits; }
+
+// Part of a head that a workgroup does: all lanes hold the same.
+struct FewPart {
+  int b, kvh;
+  uint32_t start, units;  // cost before the head's first unit of keys; its units
+  int k0, nu;             // of these, the workgroup's
+  int first;              // key of unit 0
+  Seq seq;
+};
+
+// A workgroup's way through its run.
+template <int KUNIT>
+struct FewCursor {
+  uint32_t u, ue;         // where it is, the run's end
+  int chunk = -64;        // 64 sequences that are looked at, one a lane:
+  uint32_t end = 0;       // the cost up to each one's end
+  uint32_t units = 0;
+
+  // To the next part of a head that has keys to do; false at the run's end.
+  __device__ __forceinline__ bool next(const AttnParams& p, int lane, FewPart* part) {
+    while (u < ue) {
+      const uint64_t past = __ballot(end > u);
+      if (past == 0) {
+        const uint32_t before = (uint32_t)uniform(__shfl((int)end, 63));
+        chunk += 64;
+        units = 0;
+        int lo;
+        if (chunk + lane < p.B) units = few_units(p, sequence(p, chunk + lane), KUNIT, &lo);
+        end = before + (uint32_t)wave_scan((int)few_cost(units), lane) * (uint32_t)p.Hkv;
+        continue;
+      }
+      const int who = __builtin_ctzll(past);
+      FewPart& x = *part;
+      x.units = (uint32_t)__builtin_amdgcn_readlane((int)units, who);
+      const uint32_t cost = x.units + kHeadUnits;
+      const uint32_t before = (uint32_t)__builtin_amdgcn_readlane((int)end, who) - cost * (uint32_t)p.Hkv;
+      x.kvh = (int)((u - before) / cost);
+      x.start = before + (uint32_t)x.kvh * cost + kHeadUnits;
+      const uint32_t from = max(u, x.start), to = min(ue, x.start + x.units);
+      if (from >= to) return false;  // the run ends before the head's first keys
+      u = to;
+      x.b = chunk + who;
+      x.k0 = (int)(from - x.start);
+      x.nu = (int)(to - from);
+      x.seq = sequence(p, x.b);
+      few_units(p, x.seq, KUNIT, &x.first);
+      return true;
+    }
+    return false;
+  }
+};
+
+// Tiles of one wave of a part, and the first one's first key.
+template <int KUNIT>
+__device__ __forceinline__ int few_tiles(const FewPart& x, int wave, int* key) {
+  *key = x.first + x.k0 * KUNIT + 32 * wave;
+  return x.seq.L > *key ? min(x.nu, (x.seq.L - *key + KUNIT - 1) / KUNIT) : 0;
 }
 
 template <int D, bool F8, int W>
 __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_few_kernel(AttnParams p) {
   typedef Cache<D, F8> L;
   typedef Rows<D, F8, 1, 1> R;
-  constexpr int kStage = 2 * 32 * L::kRow, kUnit = 32 * W, kLoads = 2 * 32 / L::kRows;
-  constexpr int kRing = 2 * W * kStage, kMeet = W * D * 128;  // the waves' values at a head's end
-  __shared__ __align__(1024) uint8_t lds[kRing > kMeet ? kRing : kMeet];
-  __shared__ __align__(256) uint32_t ids[W][2][64];
+  typedef Share<D, F8, 32, 1> S;
+  constexpr int kTile = 32 * L::kRow, kUnit = 32 * W, kLoads = S::kLoads, kThreads = 64 * W;
+  // Where the waves meet, as much as leaves two workgroups to a CU or is left of one.
+  constexpr int kMeet = 4 * W * kTile > 65536 ? 16384 : 8192;
+  constexpr uint32_t kPairs = kMeet / sizeof(float2);  // maxima and sums of parts that are joined at once
+  __shared__ __align__(1024) uint8_t lds[4 * W * kTile];
+  __shared__ __align__(1024) uint8_t meet_lds[kMeet];
+  __shared__ __align__(256) uint32_t ids[W][4][64];
   __shared__ float meet_m[W][64], meet_l[W][64];
   __shared__ uint32_t arrived;
-  const int lane = (int)threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), h = lane >> 5, r = lane & 31;
+  const int tid = (int)threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), h = lane >> 5, r = lane & 31;
 
   uint32_t total = 0;
   for (int at = 0; at < p.B; at += 64) {
-    int units = 0, lo;
+    uint32_t units = 0;
+    int lo;
     if (at + lane < p.B) units = few_units(p, sequence(p, at + lane), kUnit, &lo);
-    total += (uint32_t)uniform(__shfl(wave_scan(units, lane), 63));
+    total += (uint32_t)uniform(__shfl(wave_scan((int)few_cost(units), lane), 63));
   }
   total *= (uint32_t)p.Hkv;
-  const uint32_t share = (total + gridDim.x - 1) / gridDim.x;
-  uint32_t u = blockIdx.x * share;
-  const uint32_t ue = min(total, u + share);
-  uint32_t chunk_first = 0, chunk = 0;  // units before the 64 sequences that are looked at
-  const uint32_t data = lds_offset(lds) + (uint32_t)wave * 2 * kStage, id_lds = lds_offset(&ids[wave][0][0]);
-  const uint8_t* const my_lds = lds + wave * 2 * kStage;
+  const uint32_t share = max((total + gridDim.x - 1) / gridDim.x, kFewShare);
+  FewCursor<kUnit> at_head;
+  at_head.u = min(total, blockIdx.x * share);
+  at_head.ue = min(total, at_head.u + share);
+  FewCursor<kUnit> ahead = at_head;  // where the loads are
 
-  while (u < ue) {
-    // The sequence, key head and unit of u.
-    int b = -1;
-    uint32_t start = 0, units = 0;
-    for (;;) {
-      int mine = 0, lo;
-      if ((int)chunk + lane < p.B) mine = few_units(p, sequence(p, (int)chunk + lane), kUnit, &lo);
-      const uint32_t end = chunk_first + (uint32_t)wave_scan(mine, lane) * (uint32_t)p.Hkv;
-      const uint64_t past = __ballot(end > u);
-      if (past != 0) {
-        const int who = __builtin_ctzll(past);
-        b = (int)chunk + who;
-        units = (uint32_t)uniform(__shfl(mine, who));
-        start = (uint32_t)uniform(__shfl((int)end, who)) - units * (uint32_t)p.Hkv;
-        break;
-      }
-      chunk_first = (uint32_t)uniform(__shfl((int)end, 63));
-      chunk += 64;
+  // This wave's ring: two buffers of keys, two of values.
+  const uint32_t k_lds = lds_offset(lds) + (uint32_t)wave * 4 * kTile, v_lds = k_lds + 2 * kTile;
+  const uint8_t* const keys = lds + wave * 4 * kTile;
+  const uint32_t id_lds = lds_offset(&ids[wave][0][0]);
+  S at_keys;     // of the tile that is loaded
+  FewPart coming{};
+  Pages from{};
+  int left = 0, key = 0, slot_of = 0;  // its head's tiles left, its first key, its ids' place
+  bool bad_page = false, bad_tile[2] = {false, false};  // of the tile found; of the next two to multiply
+  // To the next tile of this wave, if there is one: its ids are there, those of the
+  // tile after the next are sent for.
+  auto find = [&]() {
+    while (left == 0) {
+      if (!ahead.next(p, lane, &coming)) return false;
+      left = few_tiles<kUnit>(coming, wave, &key);
+      if (left == 0) continue;
+      from = pages_of(p, coming.b, coming.kvh);
+      slot_of = 0;
+      issue_ids<32>(from, key, coming.seq.L - 1, id_lds, lane);
+      issue_ids<32>(from, key + kUnit, coming.seq.L - 1, id_lds + 256, lane);
+      wait_vmem<0>();
     }
-    b = uniform(b);
-    const int kvh = (int)((u - start) / units);
-    start += (uint32_t)kvh * units;
-    const int k0 = (int)(u - start), nu = (int)min(units - (uint32_t)k0, ue - u);
-    const Seq seq = sequence(p, b);
-    int kal;
-    few_units(p, seq, kUnit, &kal);
-    const int rows = seq.n * p.G, place = seq.L - seq.n + 1, khi = seq.L;
-    const int lo_max = p.window > 0 ? seq.L - p.window : 0;
+    bad_page = at_keys.find(from, key, coming.seq.L - 1, ids[wave][slot_of], 0, lane);
+    issue_ids<32>(from, key + 2 * kUnit, coming.seq.L - 1, id_lds + 256 * (uint32_t)((slot_of + 2) & 3), lane);
+    slot_of = (slot_of + 1) & 3;
+    key += kUnit;
+    --left;
+    return true;
+  };
+  int sent = 0;  // tiles on their way or there, not multiplied yet
+  uint32_t ring = 0;
+  while (sent < 2 && find()) {
+    at_keys.template issue<false, true>(from, k_lds + sent * kTile, 0, lane);
+    at_keys.template issue<true, true>(from, v_lds + sent * kTile, 0, lane);
+    bad_tile[sent] = bad_page;
+    ++sent;
+  }
 
-    R w;
-    w.clear();
-    const bool ok = r < rows;
-    const int i = r / p.G, tok = seq.first + i, head = kvh * p.G + (r - i * p.G);
+  R w;
+  FewPart now, then;
+  // The rows of a part's head, on their way while the waves meet over the last one's.
+  auto take_rows = [&](const FewPart& x) {
+    const int i = r / p.G, head = x.kvh * p.G + (r - i * p.G), place = x.seq.L - x.seq.n + 1;
+    const bool ok = r < x.seq.n * p.G;
     w.hi[0] = ok ? place + i : 0;
     w.lo[0] = p.window > 0 ? place + i - p.window : 0;
-    w.load_query(0, p.q + (size_t)tok * p.q_stride + (size_t)head * D * 2, ok, h);
-
-    const Pages c = pages_of(p, b, kvh);
-    const int first = kal + k0 * kUnit + 32 * wave, last = khi - 1;
-    const int nt = khi > first ? min(nu, (khi - first + kUnit - 1) / kUnit) : 0;
+    w.load_query(0, p.q + (size_t)(x.seq.first + i) * p.q_stride + (size_t)head * D * 2, ok, h);
+  };
+  constexpr bool kEarly = D < 256;  // there are no registers for it beside wide heads
+  bool any = at_head.next(p, lane, &now);
+  if (kEarly && any) take_rows(now);
+  while (any) {
+    if (!kEarly) take_rows(now);
+    const Seq seq = now.seq;
+    const int rows = seq.n * p.G, place = seq.L - seq.n + 1, kvh = now.kvh;
+    const int lo_max = p.window > 0 ? seq.L - p.window : 0;
+    int base;
+    const int nt = few_tiles<kUnit>(now, wave, &base);
+    w.clear();
     bool bad = false;
-    if (nt > 0) {
-      issue_ids<32>(c, first, last, id_lds, lane);
-      issue_ids<32>(c, first + kUnit, last, id_lds + 256, lane);
-      wait_vmem<0>();
-      bad = issue_tile<D, F8, 32, 1>(c, first, last, ids[wave][0], data, 0, lane);
-      issue_ids<32>(c, first + 2 * kUnit, last, id_lds, lane);
-    }
-    for (int j = 0; j < nt; ++j) {
-      const int at = j & 1, base = first + j * kUnit;
-      if (j + 1 < nt) {
-        wait_vmem<kLoads + 1>();  // the ids of j + 1; after them came tile j and the ids of j + 2
-        bad |= issue_tile<D, F8, 32, 1>(c, base + kUnit, last, ids[wave][at ^ 1], data + (uint32_t)(at ^ 1) * kStage, 0, lane);
-        issue_ids<32>(c, base + 3 * kUnit, last, id_lds + (uint32_t)(at ^ 1) * 256, lane);
-        wait_vmem<kLoads + 2>();  // tile j
+    // In order of issue: .., K(t) V(t), K(t+1) V(t+1), .. with ids between; loads
+    // that come after what is waited for may stay under way.
+    for (int j = 0; j < nt; ++j, base += kUnit) {
+      const uint32_t at = (ring & 1) * kTile;
+      bad |= bad_tile[0];
+      bad_tile[0] = bad_tile[1];
+      if (sent == 2)
+        wait_vmem<3 * kLoads>();  // K(t)
+      else
+        wait_vmem<kLoads>();
+      f32x16 s[1][1];
+      bf16x8 prob[1][1][2];
+      w.scores(s, keys + at, lane);
+      bool more = false;
+      if (sent == 2) {
+        more = find();
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // K(t) is read before K(t+2) lands there
+        if (more) {
+          at_keys.template issue<false, true>(from, k_lds + at, 0, lane);
+          bad_tile[1] = bad_page;
+          wait_vmem<3 * kLoads>();  // V(t)
+        } else {
+          wait_vmem<2 * kLoads>();
+        }
       } else {
         wait_vmem<0>();
       }
-      const uint8_t* const keys = my_lds + at * kStage;
-      const uint32_t values = data + (uint32_t)at * kStage + 32 * L::kRow;
-      w.template tile<1>(keys, values, base, base + 32 > place || base < lo_max, p.c, 0, lane);
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before tile j + 2 lands there
+      if (base + 32 > place || base < lo_max) {
+        w.hide(s, base, lane);
+        w.template clean_values<1>(v_lds + at, base, 0, lane);
+      }
+      w.softmax(s, prob, p.c);
+      w.add_values(prob, v_lds + at, lane);
+      if (more) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // V(t) is read before V(t+2) lands there
+        at_keys.template issue<true, true>(from, v_lds + at, 0, lane);
+      } else {
+        --sent;
+      }
+      ++ring;
     }
     w.lose();
-    bad = __syncthreads_or(bad);  // and no wave reads its ring any more
-    float l = xred_add<32>(w.l[0]);
-    if (bad) l = __builtin_nanf("");
+    const float own_l = xred_add<32>(w.l[0]);
     meet_m[wave][lane] = w.m[0];
-    meet_l[wave][lane] = l;
-    f32x4* const meet = reinterpret_cast<f32x4*>(lds);  // [wave][32 values][quad of elements][lane]
-#pragma unroll
-    for (int d = 0; d < R::kDT; ++d)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        meet[((wave * R::kDT + d) * 4 + e) * 64 + lane] =
-            f32x4{w.o[0][d][4 * e], w.o[0][d][4 * e + 1], w.o[0][d][4 * e + 2], w.o[0][d][4 * e + 3]};
-    __syncthreads();
-    float m = meet_m[0][lane], by[W];
-#pragma unroll
-    for (int v = 1; v < W; ++v) m = fmaxf(m, meet_m[v][lane]);
-    l = 0.0f;
-#pragma unroll
-    for (int v = 0; v < W; ++v) {
-      by[v] = __builtin_amdgcn_exp2f(meet_m[v][lane] - m);
-      l += by[v] * meet_l[v][lane];
+    meet_l[wave][lane] = __any(bad) ? __builtin_nanf("") : own_l;
+    if constexpr (kEarly) {
+      any = at_head.next(p, lane, &then);
+      if (any) take_rows(then);
     }
-    // Wave v goes on with values 32 v .. and those 32 W further.
-    const bool whole = (uint32_t)nu == units;
-    constexpr size_t kSlot = few_slot<D>() / 4;
-    const uint32_t wg0 = start / share, parts = (start + units - 1) / share - wg0 + 1;
-    auto slot = [&](uint32_t k) {
-      return reinterpret_cast<float*>(p.part) + (size_t)(2 * (wg0 + k) + (k == 0 ? 1 : 0)) * kSlot;
+
+    const bool whole = (uint32_t)now.nu == now.units;
+    const uint32_t wg0 = now.start / share, parts = (now.start + now.units - 1) / share - wg0 + 1;
+    constexpr size_t kSlot = few_slot<D>();
+    auto slot = [&](uint32_t k) { return p.part + (size_t)(2 * (wg0 + k) + (k == 0 ? 1 : 0)) * kSlot; };
+    // Four values 4 c4 .. of a row.
+    auto put = [&](int row, int c4, f32x4 o, float m, float l) {
+      const int i = row / p.G, head = kvh * p.G + (row - i * p.G);
+      const float f = over_sum(p.v_scale, l);
+      *reinterpret_cast<u32x2*>(p.o + (size_t)(seq.first + i) * p.o_stride + (size_t)head * D * 2 + 8 * c4) =
+          u32x2{bf16_pair_hw(o[0] * f, o[1] * f), bf16_pair_hw(o[2] * f, o[3] * f)};
+      if (c4 == 0 && p.lse != nullptr) p.lse[(size_t)(seq.first + i) * p.Hq + head] = lse_of(m, l);
     };
-    float* const to = slot(blockIdx.x - wg0);
-    uint8_t* const row = p.o + (size_t)tok * p.o_stride + (size_t)head * D * 2;
-    const int at = h * rows + r;  // in a slot: rows are packed
-    for (int d = wave; d < R::kDT; d += W) {
-      f32x16 o = {};
+    // The waves meet over as many times 16 values of the rows as fit, a power of two;
+    // a thread takes four of a row.
+    f32x4* const meet = reinterpret_cast<f32x4*>(meet_lds);  // [wave][16 values][quad][half][row]
+    int pass_log = 31 - __builtin_clz(kMeet / (W * 64 * rows));
+    if (pass_log > 2 + (D == 128) + 2 * (D == 256)) pass_log = 2 + (D == 128) + 2 * (D == 256);
+    const int pass = 1 << pass_log;
 #pragma unroll
-      for (int v = 0; v < W; ++v)
+    for (int d = 0; d < 2 * R::kDT; ++d) {
+      if (r < rows) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const f32x4 q = meet[((v * R::kDT + d) * 4 + e) * 64 + lane];
-#pragma unroll
-          for (int f = 0; f < 4; ++f) o[4 * e + f] = fmaf(q[f], by[v], o[4 * e + f]);
+        for (int e = 0; e < 2; ++e) {
+          const f32x16& o = w.o[0][d >> 1];
+          const int x = 8 * (d & 1) + 4 * e;
+          meet[(((wave << pass_log) + (d & (pass - 1))) * 4 + 2 * e + h) * rows + r] = f32x4{o[x], o[x + 1], o[x + 2], o[x + 3]};
         }
-      if (!ok) continue;
-      if (whole) {
-        store_values(row, d, h, o, over_sum(p.v_scale, l));
-      } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) coherent_store(to + (d * 16 + e) * 2 * rows + at, o[e]);
       }
-    }
-    bool write = whole;
-    if (!whole) {
-      if (ok && wave == 0) coherent_store(to + D * rows + at, h == 0 ? m : l);
-      write = arrive_last(p.cnt + (size_t)wg0 * kOpsCounterStride, parts, &arrived);
-      if (write && ok) {
-        m = kFloor;
-        for (uint32_t k = 0; k < parts; ++k) m = fmaxf(m, coherent_load(slot(k) + D * rows + r));
-        l = 0.0f;
-        for (uint32_t k = 0; k < parts; ++k)
-          l += __builtin_amdgcn_exp2f(coherent_load(slot(k) + D * rows + r) - m) * coherent_load(slot(k) + D * rows + rows + r);
-        for (int d = wave; d < R::kDT; d += W) {
-          f32x16 o = {};
-          for (uint32_t k = 0; k < parts; ++k) {
-            const float* const from = slot(k);
-            const float f = __builtin_amdgcn_exp2f(coherent_load(from + D * rows + r) - m);
+      if ((d & (pass - 1)) != pass - 1) continue;
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // the tiles on their way are not waited for
+      const int d0 = d - (pass - 1);
+      for (int v = tid; v < rows * 4 * pass; v += kThreads) {
+        const int row = v >> (2 + pass_log), c4 = v & (4 * pass - 1);  // quad 4 d0 + c4 of the row
+        float m = meet_m[0][row], l = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = fmaf(coherent_load(from + (d * 16 + e) * 2 * rows + at), f, o[e]);
+        for (int x = 1; x < W; ++x) m = fmaxf(m, meet_m[x][row]);
+        f32x4 o = {};
+#pragma unroll
+        for (int x = 0; x < W; ++x) {
+          const float by = __builtin_amdgcn_exp2f(meet_m[x][row] - m);
+          l += by * meet_l[x][row];
+          o += by * meet[((x << pass_log) * 4 + c4) * rows + row];
+        }
+        if (whole) {
+          put(row, 4 * d0 + c4, o, m, l);
+        } else {
+          uint8_t* const to = slot(blockIdx.x - wg0);
+          st16_coherent_if(true, __builtin_bit_cast(u32x4, o), make_rsrc(to, (uint32_t)kSlot),
+                           16u * (uint32_t)(row * (D / 4) + 4 * d0 + c4));
+          if (d0 == 0 && c4 == 0) {
+            float* const ml = reinterpret_cast<float*>(to) + rows * D + 2 * row;
+            coherent_store(ml, m);
+            coherent_store(ml + 1, l);
           }
-          store_values(row, d, h, o, over_sum(p.v_scale, l));
         }
       }
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     }
-    if (write && ok && p.lse != nullptr && h == 0 && wave == 0) p.lse[(size_t)tok * p.Hq + head] = lse_of(m, l);
-    u += (uint32_t)nu;
-    if (u < ue) __syncthreads();  // the meeting's LDS is the ring again
+    if (!whole && arrive_last(p.cnt + (size_t)wg0 * kOpsCounterStride, parts, &arrived)) {
+      // Maxima and sums of `some` parts at once through LDS; values as they come.
+      float2* const join_ml = reinterpret_cast<float2*>(meet_lds);
+      const uint32_t some = kPairs / (uint32_t)rows;
+      const int quads = rows * (D / 4);
+      for (int v0 = 0; v0 < quads; v0 += kThreads) {
+        const int v = v0 + tid, row = min(v, quads - 1) / (D / 4), c4 = v % (D / 4);
+        float m = kFloor, l = 0.0f;
+        f32x4 o = {};
+        for (uint32_t k0 = 0; k0 < parts; k0 += some) {
+          const uint32_t here = min(some, parts - k0);
+          if (v0 == 0 || parts > some) {
+            __syncthreads();
+            for (uint32_t x = (uint32_t)tid; x < here * (uint32_t)rows; x += kThreads) {
+              const float* const ml = reinterpret_cast<const float*>(slot(k0 + x / (uint32_t)rows)) + rows * D + 2 * (x % (uint32_t)rows);
+              join_ml[x] = float2{coherent_load(ml), coherent_load(ml + 1)};
+            }
+            __syncthreads();
+          }
+          float top = m;
+          for (uint32_t k = 0; k < here; ++k) top = fmaxf(top, join_ml[k * rows + row].x);
+          const float by = __builtin_amdgcn_exp2f(m - top);
+          m = top;
+          l *= by;
+          o *= by;
+          if (v < quads) {
+#pragma unroll 8
+            for (uint32_t k = 0; k < here; ++k) {
+              const f32x4 x = __builtin_bit_cast(f32x4, ld16_coherent_if(true, make_rsrc(slot(k0 + k), (uint32_t)kSlot), 16u * (uint32_t)v));
+              const float2 ml = join_ml[k * rows + row];
+              const float f = __builtin_amdgcn_exp2f(ml.x - m);
+              l = fmaf(f, ml.y, l);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[e] = fmaf(f, x[e], o[e]);
+            }
+          }
+        }
+        if (v < quads) put(row, c4, o, m, l);
+      }
+      __syncthreads();
+    }
+    if constexpr (kEarly)
+      now = then;
+    else
+      any = at_head.next(p, lane, &now);
   }
 }
 
@@ -846,12 +1021,16 @@ template <int D, bool F8>
 int rows_splits(const AttnParams& p) {
   const int64_t groups = tiles_bound<D, F8>(p) * p.Hkv;
   if (groups <= 0 || groups > kOpsCounters) return 1;
-  int64_t s = 2 * kChipCUs / groups;
-  const int64_t tiles = (p.max_len + kRowsKeys - 1) / kRowsKeys;
-  if (s > tiles / 4) s = tiles / 4;  // not below 256 keys each
+  // Rounds of one workgroup a CU: S that leaves the fewest CUs idle, the smallest of
+  // equal ones; not below 512 keys a workgroup.
+  int64_t most = (p.max_len + kRowsKeys - 1) / kRowsKeys / 8;
   const int64_t room = (int64_t)(kOpsPartBytes / rows_part<D, F8>()) / groups;
-  if (s > room) s = room;
-  return s < 1 ? 1 : s > 64 ? 64 : (int)s;
+  if (most > room) most = room;
+  int best = 1;
+  auto rounds = [&](int64_t s) { return (groups * s + kChipCUs - 1) / kChipCUs; };
+  for (int s = 2; s <= most && s <= 64; ++s)
+    if (rounds(s) * best < rounds(best) * s) best = s;
+  return best;
 }
 
 // Workgroups of the few kernel: as many as the chip holds at once.
@@ -873,7 +1052,7 @@ hipError_t launch_format(AttnParams p, hipStream_t s) {
     if (e != hipSuccess || !few) return e;
   }
   constexpr int W = few_waves<D, F8>(), kUnit = 32 * W;
-  const int64_t units = (int64_t)p.B * p.Hkv * (p.max_len / kUnit + 1);
+  const int64_t units = (int64_t)p.B * p.Hkv * (p.max_len / kUnit + 2);
   const unsigned grid = (unsigned)(units < few_grid<D, F8>() ? units : few_grid<D, F8>());
   return launch(attn_few_kernel<D, F8, W>, dim3(grid), dim3(64 * W), 0, s, p);
 }
