@@ -371,7 +371,7 @@ SKGEMM_API int skgemm_rope(const void* X, const void* G, const float* inv_freq,
  * choice of strides. Elements are bf16, or E4M3 codes that stand for code * k_scale
  * (v_scale); with bf16 both scales are 1 (SKGEMM_EINVAL). page_size is a power of
  * two up to SKGEMM_MAX_PAGE; the caches are 16-byte aligned, strides multiples of
- * 16, and one page spans less than 4 GiB (SKGEMM_ESHAPE). Caches of any total size.
+ * 16 and below 4 GiB, and so is a page's span (SKGEMM_ESHAPE). Caches of any total size.
  *
  * skgemm_rope_append: skgemm_rope of Q into Q_out and of K into the cache, and V as
  * it is into the cache, in one launch: queries, keys and values as the layer's first

@@ -91,12 +91,12 @@ struct Cache {
   // What a row's chunk numbers are exchanged with. Keys are read by 32 rows, the
   // same chunk of 8 neighbouring rows at once.
   __device__ static __forceinline__ int key_swizzle(int row) {
-    return kRow >= 128 ? row & 7 : (row >> 1) & 3;
+    return kRow >= 256 ? row & 15 : kRow >= 128 ? row & 7 : (row >> 1) & 3;
   }
   // Values are read by 4 rows x 32 bytes (bf16), or rows 0..3 and 8..11 of 16 x 16
   // bytes (E4M3).
   __device__ static __forceinline__ int value_swizzle(int row) {
-    if constexpr (!F8) return (row & 3) << 1;
+    if constexpr (!F8) return kRow >= 256 ? (row & 3) << 2 : (row & 3) << 1;
     return kRow >= 128 ? (row & 3) | ((row >> 1) & 4) : ((row >> 1) & 1) | ((row >> 2) & 2);
   }
 };
@@ -104,8 +104,7 @@ struct Cache {
 // One key head's pages and a sequence's table.
 struct Pages {
   const uint8_t *k, *v, *ids;
-  size_t page_stride;
-  uint32_t slot_stride;
+  uint32_t page_stride, slot_stride;
   int n_pages, shift;
 };
 
@@ -153,10 +152,23 @@ struct Share {
     for (int q = 0; q < kLoads; ++q) {
       const int row = (wave * kLoads + q) * L::kRows + lane / L::kChunks, at = lane % L::kChunks;
       const int chunk = at ^ (VALUES ? L::value_swizzle(row) : L::key_swizzle(row));
-      const uint32_t in_page = (uint32_t)(min(base + row, last) & ((1 << c.shift) - 1)) * c.slot_stride + 16u * (uint32_t)chunk;
-      global16_to_lds<STREAM>((VALUES ? c.v : c.k) + (size_t)page[q] * c.page_stride + in_page,
-                              lds + (uint32_t)(wave * kLoads + q) * 1024u);
+      global16_to_lds<STREAM>((VALUES ? c.v : c.k) + place(c, q, row) + 16 * chunk, lds + (uint32_t)(wave * kLoads + q) * 1024u);
     }
+  }
+  // Both.
+  __device__ __forceinline__ void issue_both(const Pages& c, uint32_t keys, uint32_t values, int wave, int lane) const {
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+      const int row = (wave * kLoads + q) * L::kRows + lane / L::kChunks, at = lane % L::kChunks;
+      const size_t off = place(c, q, row);
+      const uint32_t to = (uint32_t)(wave * kLoads + q) * 1024u;
+      global16_to_lds<false>(c.k + 16 * (at ^ L::key_swizzle(row)) + off, keys + to);
+      global16_to_lds<false>(c.v + 16 * (at ^ L::value_swizzle(row)) + off, values + to);
+    }
+  }
+  __device__ __forceinline__ size_t place(const Pages& c, int q, int row) const {
+    const uint32_t in_page = (uint32_t)(min(base + row, last) & ((1 << c.shift) - 1)) * c.slot_stride;
+    return (size_t)page[q] * c.page_stride + in_page;
   }
 };
 
@@ -205,16 +217,25 @@ struct Rows {
   // read everything at once and spill).
   static __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
 
-  __device__ __forceinline__ void scores(f32x16 (&s)[RT][KB], const uint8_t* keys, int lane) const {
+  // Where a lane reads: 16 bytes of chunk 2 k + h of key r lie at key_place ^ 32 k, 32
+  // keys on is 32 rows on. The swizzle only exchanges chunks inside a row, and tiles lie
+  // at multiples of 1024, so one register and an exclusive or a step do.
+  static __device__ __forceinline__ uint32_t key_place(int lane) {
+    const int r = lane & 31, h = lane >> 5;
+    return (uint32_t)(r * L::kRow + 16 * (h ^ L::key_swizzle(r)));
+  }
+  static __device__ __forceinline__ u32x4 read_key(uint32_t place, int k, int kb) {
+    return *(SKG_LDS const u32x4*)((place ^ (32u * (uint32_t)k)) + (uint32_t)(32 * kb * L::kRow));
+  }
+
+  __device__ __forceinline__ void scores(f32x16 (&s)[RT][KB], uint32_t keys, int lane) const {
     constexpr int kSteps = D / (F8 ? 32 : 16), kGroup = F8 || D == 256 ? 2 : 4, kGroups = KB * kSteps / kGroup;
-    const int r = lane & 31, h = lane >> 5, swz = L::key_swizzle(r);
+    const uint32_t place = keys + key_place(lane);
     u32x4 w[2][kGroup];
     auto read = [&](int g) {
 #pragma unroll
-      for (int i = 0; i < kGroup; ++i) {
-        const int kb = (g * kGroup + i) / kSteps, k = (g * kGroup + i) % kSteps;
-        w[g & 1][i] = *reinterpret_cast<const u32x4*>(keys + (32 * kb + r) * L::kRow + 16 * ((2 * k + h) ^ swz));
-      }
+      for (int i = 0; i < kGroup; ++i)  // neighbours do not wait for each other's sums
+        w[g & 1][i] = read_key(place, (g * kGroup + i) / KB, (g * kGroup + i) % KB);
     };
     read(0);
 #pragma unroll
@@ -222,7 +243,7 @@ struct Rows {
       if (g + 1 < kGroups) read(g + 1);
 #pragma unroll
       for (int i = 0; i < kGroup; ++i) {
-        const int kb = (g * kGroup + i) / kSteps, k = (g * kGroup + i) % kSteps;
+        const int kb = (g * kGroup + i) % KB, k = (g * kGroup + i) / KB;
         const u32x4 x = w[g & 1][i];
         if constexpr (F8) {
           const bf16x8 a = fp8x8_bf16(x[0], x[1], 1.0f), b = fp8x8_bf16(x[2], x[3], 1.0f);
@@ -239,21 +260,30 @@ struct Rows {
     }
   }
 
-  // Values 32 d .. 32 d + 31 of the 16 keys from `key`, as the product takes them.
-  __device__ __forceinline__ bf16x8 value_operand(uint32_t values, int key, int d, int lane) const {
+  // Values 32 d .. 32 d + 31 of the 16 keys of a step, as they lie in LDS and as the
+  // product takes them: at value_place ^ (32 values of a row), 16 keys on 16 rows on.
+  static __device__ __forceinline__ uint32_t value_place(int lane) {
     const int i = lane & 15, side = (lane >> 4) & 1, h = lane >> 5;
+    const int row = F8 ? 4 * h + ((i >> 1) & 3) + 8 * (i >> 3) : 4 * h + (i >> 2);
+    const int chunk = F8 ? side : 2 * side + ((i >> 1) & 1);
+    return (uint32_t)(row * L::kRow + 16 * (chunk ^ L::value_swizzle(row)) + 8 * (i & 1));
+  }
+  static __device__ __forceinline__ u32x4 read_values(uint32_t place, int step, int d) {
+    const uint32_t at = (place ^ (uint32_t)(d * (F8 ? 32 : 64))) + (uint32_t)(16 * step * L::kRow);
     if constexpr (F8) {
-      const int row = key + 4 * h + ((i >> 1) & 3) + 8 * (i >> 3);
-      const uint32_t at = values + row * L::kRow + 16 * ((2 * d + side) ^ L::value_swizzle(row)) + 8 * (i & 1);
       const i32x2 w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((SKG_LDS i32x2*)at);
-      return fp8x8_bf16((uint32_t)w[0], (uint32_t)w[1], 1.0f);
+      return u32x4{(uint32_t)w[0], (uint32_t)w[1], 0, 0};
     } else {
-      const int row = key + 4 * h + (i >> 2);
-      const uint32_t at = values + row * L::kRow + 16 * ((4 * d + 2 * side + ((i >> 1) & 1)) ^ L::value_swizzle(row)) + 8 * (i & 1);
       const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SKG_LDS s16x4*)at);
       const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SKG_LDS s16x4*)(at + 8 * L::kRow));
-      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+      return __builtin_bit_cast(u32x4, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
     }
+  }
+  static __device__ __forceinline__ bf16x8 value_operand(u32x4 w) {
+    if constexpr (F8)
+      return fp8x8_bf16(w[0], w[1], 1.0f);
+    else
+      return as_bf16x8(w);
   }
 
   // A tile of 32 KB keys from `base` of which some row does not see all: what it does
@@ -271,6 +301,7 @@ struct Rows {
   }
 
   __device__ __forceinline__ void hide(f32x16 (&s)[RT][KB], int base, int lane) const {
+    asm volatile("" : "+v"(lane));  // or the compiler does this for every tile and selects
     const int h = lane >> 5;
 #pragma unroll
     for (int t = 0; t < RT; ++t)
@@ -322,6 +353,7 @@ struct Rows {
   static constexpr int kTileLoads = 32 * KB * L::kRow / 1024;  // of 16 bytes a lane
 
   __device__ __forceinline__ bool any_not_finite(uint32_t values, int lane) const {
+    asm volatile("" : "+v"(lane));  // as in hide
     bool is = false;
 #pragma unroll
     for (int i = 0; i < kTileLoads; ++i) {
@@ -367,7 +399,7 @@ struct Rows {
         }
 #pragma unroll
         for (int d = 0; d < kDT; ++d) {
-          u32x4 w = __builtin_bit_cast(u32x4, value_operand(values, 16 * step, d, lane));
+          u32x4 w = __builtin_bit_cast(u32x4, value_operand(read_values(values + value_place(lane), step, d)));
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             w[e] = ((w[e] & 0x7F80u) == 0x7F80u ? 0x3F80u : 0u) | ((w[e] & 0x7F800000u) == 0x7F800000u ? 0x3F800000u : 0u);
@@ -392,12 +424,13 @@ struct Rows {
   // O += V^T P^T.
   __device__ __forceinline__ void add_values(const bf16x8 (&p)[RT][KB][2], uint32_t values, int lane) {
     constexpr int kGroup = D == 128 ? 4 : 2, kGroups = 2 * KB * kDT / kGroup;
+    const uint32_t place = values + value_place(lane);
     bf16x8 v[2][kGroup];
     auto read = [&](int g) {
 #pragma unroll
       for (int i = 0; i < kGroup; ++i) {
         const int at = g * kGroup + i;
-        v[g & 1][i] = value_operand(values, 16 * (at / kDT), at % kDT, lane);
+        v[g & 1][i] = value_operand(read_values(place, at / kDT, at % kDT));
       }
     };
     read(0);
@@ -508,8 +541,9 @@ __global__ __launch_bounds__(64 * W, W / 4) void attn_rows_kernel(AttnParams p) 
   typedef Cache<D, F8> L;
   constexpr int RT = 1;
   typedef Rows<D, F8, RT, 2> R;
-  constexpr int BM = 32 * W, kStage = 2 * kRowsKeys * L::kRow;
-  __shared__ __align__(1024) uint8_t lds[2 * kStage];
+  constexpr int BM = 32 * W, kHalf = kRowsKeys * L::kRow;  // bytes of a tile's keys
+  constexpr int kBuffers = 2;
+  __shared__ __align__(1024) uint8_t lds[2 * kBuffers * kHalf];  // keys, then values
   __shared__ __align__(256) uint32_t ids[W][2][64];
   __shared__ uint32_t arrived;
   const int lane = (int)threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), h = lane >> 5;
@@ -565,41 +599,48 @@ __global__ __launch_bounds__(64 * W, W / 4) void attn_rows_kernel(AttnParams p) 
   }
 
   const Pages c = pages_of(p, b, kvh);
-  const uint32_t data = lds_offset(lds), id_lds = lds_offset(&ids[wave][0][0]);
+  const uint32_t k_lds = lds_offset(lds), v_lds = k_lds + kBuffers * kHalf, id_lds = lds_offset(&ids[wave][0][0]);
   bool bad = false;
   const int last = khi - 1;
   Share<D, F8, 64, W> share;
-  if (j0 < j1) {
-    issue_ids<64>(c, kal + 64 * j0, last, id_lds, lane);
-    issue_ids<64>(c, kal + 64 * (j0 + 1), last, id_lds + 256, lane);
+
+  // Tiles j .. end - 1, all waves in step, two buffers; some may be hidden from some row.
+  auto in_step = [&](int j, int end) {
+    if (j >= end) return;
+    const int from = j;
+    issue_ids<64>(c, kal + 64 * j, last, id_lds, lane);
+    issue_ids<64>(c, kal + 64 * (j + 1), last, id_lds + 256, lane);
     wait_vmem<0>();
-    bad = share.find(c, kal + 64 * j0, last, ids[wave][0], wave, lane);
-    share.template issue<false, false>(c, data, wave, lane);
-    share.template issue<true, false>(c, data + kRowsKeys * L::kRow, wave, lane);
-    issue_ids<64>(c, kal + 64 * (j0 + 2), last, id_lds, lane);
-  }
-  for (int j = j0; j < j1; ++j) {
-    const int at = (j - j0) & 1, base = kal + 64 * j;
-    wait_vmem<1>();  // this wave's share of tile j; the ids of j + 2 may be under way
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (j + 1 < j1) {
-      bad |= share.find(c, base + 64, last, ids[wave][at ^ 1], wave, lane);
-      share.template issue<false, false>(c, data + (uint32_t)(at ^ 1) * kStage, wave, lane);
-      share.template issue<true, false>(c, data + (uint32_t)(at ^ 1) * kStage + kRowsKeys * L::kRow, wave, lane);
-      issue_ids<64>(c, base + 192, last, id_lds + (uint32_t)(at ^ 1) * 256, lane);
+    bad |= share.find(c, kal + 64 * j, last, ids[wave][0], wave, lane);
+    share.template issue<false, false>(c, k_lds, wave, lane);
+    share.template issue<true, false>(c, v_lds, wave, lane);
+    issue_ids<64>(c, kal + 64 * (j + 2), last, id_lds, lane);
+    for (; j < end; ++j) {
+      const int at = (j - from) & 1, base = kal + 64 * j;
+      wait_vmem<1>();  // this wave's share of tile j; the ids of j + 2 may be under way
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      const uint32_t values = v_lds + (uint32_t)at * kHalf;
+      f32x16 s[1][2];
+      bf16x8 prob[1][2][2];
+      w.scores(s, k_lds + (uint32_t)at * kHalf, lane);
+      if (j + 1 < end) {  // behind the products, so that a SIMD's other wave can multiply meanwhile
+        const uint32_t next = (uint32_t)(at ^ 1);
+        bad |= share.find(c, base + 64, last, ids[wave][next], wave, lane);
+        share.issue_both(c, k_lds + next * kHalf, v_lds + next * kHalf, wave, lane);
+        issue_ids<64>(c, base + 192, last, id_lds + next * 256, lane);
+      }
+      if (base + 64 > see_min || base < lo_max) {
+        w.hide(s, base, lane);
+        w.template clean_values<W>(values, base, wave, lane);
+      }
+      w.softmax(s, prob, p.c);
+      w.add_values(prob, values, lane);
     }
-    const uint8_t* const keys = lds + at * kStage;
-    const uint32_t values = data + (uint32_t)at * kStage + kRowsKeys * L::kRow;
-    f32x16 s[1][2];
-    bf16x8 prob[1][2][2];
-    w.scores(s, keys, lane);
-    if (base + 64 > see_min || base < lo_max) {
-      w.hide(s, base, lane);
-      w.template clean_values<W>(values, base, wave, lane);
-    }
-    w.softmax(s, prob, p.c);
-    w.add_values(prob, values, lane);
-  }
+    wait_vmem<0>();
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // the buffers are free again
+  };
+
+  in_step(j0, j1);
   wait_vmem<0>();
   w.lose();
   bad = __syncthreads_or(bad);
@@ -792,7 +833,6 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_few_kernel(Attn
 
   // This wave's ring: two buffers of keys, two of values.
   const uint32_t k_lds = lds_offset(lds) + (uint32_t)wave * 4 * kTile, v_lds = k_lds + 2 * kTile;
-  const uint8_t* const keys = lds + wave * 4 * kTile;
   const uint32_t id_lds = lds_offset(&ids[wave][0][0]);
   S at_keys;     // of the tile that is loaded
   FewPart coming{};
@@ -862,7 +902,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_few_kernel(Attn
         wait_vmem<kLoads>();
       f32x16 s[1][1];
       bf16x8 prob[1][1][2];
-      w.scores(s, keys + at, lane);
+      w.scores(s, k_lds + at, lane);
       bool more = false;
       if (sent == 2) {
         more = find();

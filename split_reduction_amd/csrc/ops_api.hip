@@ -118,7 +118,7 @@ int check_cache(const void* K, const void* V, int Hkv, int D, int n_pages, int p
   const size_t row = (size_t)D * (format == SKGEMM_BF16 ? 2 : 1);
   const size_t limit = (size_t)1 << 32;
   if ((page_size > 1 && slot_stride >= limit) || (Hkv > 1 && head_stride >= limit) ||
-      (n_pages > 1 && page_stride >= ((size_t)1 << 44)))
+      (n_pages > 1 && page_stride >= limit))
     return SKGEMM_ESHAPE;
   if ((page_size > 1 ? (size_t)(page_size - 1) * slot_stride : 0) + (Hkv > 1 ? (size_t)(Hkv - 1) * head_stride : 0) + row >= limit)
     return SKGEMM_ESHAPE;
@@ -464,7 +464,7 @@ SKGEMM_API int skgemm_paged_attention(const void* Q, const void* K_cache, const 
   p.q_stride = q_stride;
   p.o_stride = o_stride;
   p.table_stride = table_stride;
-  p.page_stride = page_stride;
+  p.page_stride = (uint32_t)page_stride;
   p.slot_stride = (uint32_t)slot_stride;
   p.head_stride = (uint32_t)head_stride;
   p.T = T;

@@ -97,8 +97,8 @@ struct AttnParams {
   const int32_t* q_start;  // [B + 1]
   uint8_t* o;              // bf16 [T, Hq, D]
   float* lse;              // [T, Hq] or null
-  size_t q_stride, o_stride, table_stride, page_stride;  // bytes
-  uint32_t slot_stride, head_stride;
+  size_t q_stride, o_stride, table_stride;  // bytes
+  uint32_t page_stride, slot_stride, head_stride;
   int T, B, max_q, Hq, Hkv, G, n_pages, page_shift, max_len, window;
   float c, v_scale;  // scale * k_scale / log 2
   int few;           // rows (new tokens x G) of a sequence that attn_few_kernel takes
