@@ -527,17 +527,18 @@ __device__ __forceinline__ bool arrive_last(uint32_t* cnt, uint32_t all, uint32_
 
 constexpr int kRowsKeys = 64;
 
+// Waves of the larger form; each has a 64th of a tile's bytes to load at least.
 template <int D, bool F8>
 constexpr int rows_waves() {
   return D == 256 || (D == 64 && F8) ? 4 : 8;
 }
-template <int D, bool F8>
-constexpr size_t rows_part() {  // bytes of a workgroup's results
-  return (size_t)64 * rows_waves<D, F8>() * 4 * (D / 32 * 16 + 2);
+template <int D>
+constexpr size_t rows_part(int waves) {  // bytes of a workgroup's results
+  return (size_t)64 * waves * 4 * (D / 32 * 16 + 2);
 }
 
 template <int D, bool F8, int W>
-__global__ __launch_bounds__(64 * W, W / 4) void attn_rows_kernel(AttnParams p) {
+__global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_rows_kernel(AttnParams p) {
   typedef Cache<D, F8> L;
   constexpr int RT = 1;
   typedef Rows<D, F8, RT, 2> R;
@@ -653,7 +654,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void attn_rows_kernel(AttnParams p) 
   if (p.S > 1) {
     constexpr int kQuads = RT * R::kDT * 4;
     const int group = flat * p.Hkv + kvh;
-    const uint32_t one = (uint32_t)rows_part<D, F8>();
+    const uint32_t one = (uint32_t)rows_part<D>(W);
     uint8_t* const base = p.part + (size_t)group * p.S * one;
     const rsrc_t part = make_rsrc(base, (uint32_t)p.S * one);
     const uint32_t mine = (uint32_t)split * one, at = threadIdx.x * 16u;
@@ -1048,23 +1049,22 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_few_kernel(Attn
 
 // Tiles of the rows kernel at most: it has a workgroup for each, and those past
 // what the lengths give end at once.
-template <int D, bool F8>
-int64_t tiles_bound(const AttnParams& p) {
-  const int64_t BM = 32 * rows_waves<D, F8>();
+int64_t tiles_bound(const AttnParams& p, int waves) {
+  const int64_t BM = 32 * waves;
   const int64_t by_rows = (int64_t)p.T * p.G / BM + p.B;
   const int64_t by_seq = (int64_t)p.B * (((int64_t)p.max_q * p.G + BM - 1) / BM);
   return by_rows < by_seq ? by_rows : by_seq;
 }
 
-// Workgroups that split the keys of each tile where the tiles alone leave CUs idle.
-template <int D, bool F8>
-int rows_splits(const AttnParams& p) {
-  const int64_t groups = tiles_bound<D, F8>(p) * p.Hkv;
+// Workgroups that split the keys of each tile where the tiles alone leave CUs idle:
+// rounds of one workgroup a CU, S that leaves the fewest idle, the smallest of equal
+// ones; not below 512 keys a workgroup.
+template <int D>
+int rows_splits(const AttnParams& p, int waves) {
+  const int64_t groups = tiles_bound(p, waves) * p.Hkv;
   if (groups <= 0 || groups > kOpsCounters) return 1;
-  // Rounds of one workgroup a CU: S that leaves the fewest CUs idle, the smallest of
-  // equal ones; not below 512 keys a workgroup.
   int64_t most = (p.max_len + kRowsKeys - 1) / kRowsKeys / 8;
-  const int64_t room = (int64_t)(kOpsPartBytes / rows_part<D, F8>()) / groups;
+  const int64_t room = (int64_t)(kOpsPartBytes / rows_part<D>(waves)) / groups;
   if (most > room) most = room;
   int best = 1;
   auto rounds = [&](int64_t s) { return (groups * s + kChipCUs - 1) / kChipCUs; };
@@ -1086,9 +1086,22 @@ hipError_t launch_format(AttnParams p, hipStream_t s) {
   const bool many = (int64_t)p.max_q * p.G > kFewRows, few = !many || p.B > 1;
   p.few = few ? kFewRows : 0;
   if (many) {
-    p.S = rows_splits<D, F8>(p);
-    const int64_t grid = tiles_bound<D, F8>(p) * p.Hkv * p.S;
-    const hipError_t e = launch(attn_rows_kernel<D, F8, rows_waves<D, F8>()>, dim3((unsigned)grid), dim3(64 * rows_waves<D, F8>()), 0, s, p);
+    // Eight waves of a workgroup share a tile's keys, which halves what comes from the
+    // L2; two workgroups of four fill a CU as well, go at their own pace and waste
+    // less on short work. 8192 tokens of 32 heads of 128: 563 against 588 us, 512 over
+    // 32768 cached, keys split: 279 / 300; but heads of 64 360 / 342, a window of 1024
+    // 199 / 183, 4 x 2048 of 16 heads 119 / 105, 500 tokens 24.7 / 19.6.
+    constexpr int kMost = rows_waves<D, F8>();
+    p.S = rows_splits<D>(p, kMost);
+    const bool large = kMost == 8 && (p.S > 1 || (D == 128 && p.window == 0 && tiles_bound(p, 8) * p.Hkv >= 4 * kChipCUs));
+    const int waves = large ? 8 : 4;
+    const unsigned grid = (unsigned)(tiles_bound(p, waves) * p.Hkv * p.S);
+    hipError_t e;
+    if constexpr (kMost == 8)
+      e = large ? launch(attn_rows_kernel<D, F8, 8>, dim3(grid), dim3(512), 0, s, p)
+                : launch(attn_rows_kernel<D, F8, 4>, dim3(grid), dim3(256), 0, s, p);
+    else
+      e = launch(attn_rows_kernel<D, F8, 4>, dim3(grid), dim3(256), 0, s, p);
     if (e != hipSuccess || !few) return e;
   }
   constexpr int W = few_waves<D, F8>(), kUnit = 32 * W;
