@@ -432,11 +432,21 @@ def skgemm_logprobs_grad(logits, tokens, lse, entropy, g_logprob, g_entropy, d_l
 def _heads(a, rows: int, heads: int, D: int, stride, what: str):
     """_rows of bfloat16 heads [rows, heads, D] or [rows, heads * D]; a token's heads
     lie one after another."""
-    if a is not None and not isinstance(a, int) and a.dim() == 3 and not a.is_contiguous():
-        if (a.stride(2) != 1 and a.shape[2] > 1) or (a.stride(1) != a.shape[2] and a.shape[1] > 1):
-            raise SkgemmError(SKGEMM_EINVAL, f"{what}: a token's heads are not contiguous")
-        a = a.as_strided((a.shape[0], a.shape[1] * a.shape[2]), (a.stride(0), 1))
-    return _rows(a, rows, 2 * heads * D, stride, what, (_torch_types or _types())["bf16"])
+    bf16 = (_torch_types or _types())["bf16"]
+    if a is not None and not isinstance(a, int):
+        if stride is None and a.is_cuda and a.dtype is bf16[1][0]:  # the common cases, in half the time
+            st, sh = a.stride(), a.shape
+            n = len(st)
+            if n == 2:
+                if st[1] == 1 and sh[0] >= rows and sh[1] >= heads * D and st[0] >= sh[1]:
+                    return a.data_ptr(), 2 * st[0]
+            elif n == 3 and st[2] == 1 and st[1] == sh[2] == D and sh[0] >= rows and sh[1] >= heads and st[0] >= sh[1] * D:
+                return a.data_ptr(), 2 * st[0]
+        if a.dim() == 3 and not a.is_contiguous():
+            if (a.stride(2) != 1 and a.shape[2] > 1) or (a.stride(1) != a.shape[2] and a.shape[1] > 1):
+                raise SkgemmError(SKGEMM_EINVAL, f"{what}: a token's heads are not contiguous")
+            a = a.as_strided((a.shape[0], a.shape[1] * a.shape[2]), (a.stride(0), 1))
+    return _rows(a, rows, 2 * heads * D, stride, what, bf16)
 
 
 def _layout(name) -> int:
@@ -463,6 +473,12 @@ def _pages(K, V, n_pages: int, page_size: int, Hkv: int, D: int, fmt, strides):
         fmt = 2 if K is not None and not isinstance(K, int) and K.element_size() == 1 else 0
     fmt = _format(fmt)
     types = ty["e4m3_out"] if fmt == 2 else ty["bf16"]
+    if strides is None and K is not None and not isinstance(K, int) and K.is_cuda and K.dtype in types[1]:
+        sh, s = K.shape, K.stride()  # the common case: both alike
+        if len(s) == 4 and s[3] == 1 and sh[0] >= n_pages and (sh[1], sh[2], sh[3]) == (page_size, Hkv, D) and min(s) >= 0:
+            if V is not None and not isinstance(V, int) and V.is_cuda and V.dtype is K.dtype and V.shape == sh and V.stride() == s:
+                size = types[0]
+                return K.data_ptr(), V.data_ptr(), fmt, s[0] * size, s[1] * size, s[2] * size
     ptr = []
     for a, what in ((K, "K_cache"), (V, "V_cache")):
         if a is None or isinstance(a, int):

@@ -714,7 +714,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_rows_kernel(Att
 // of 32 keys a wave, and one more for what a head costs beside its keys; the units
 // of the whole call, one sequence after another, are dealt out in equal runs to a
 // fixed number of workgroups, whatever the lengths are. A workgroup goes through
-// its run head by head; its waves take the unit's keys by 32, each through two
+// its run head by head; its waves take the unit's keys by 32, each through
 // buffers of its own with no barrier, and meet at the head's end. The loads run two
 // tiles ahead of the products, into the next head where one ends. A head that was
 // cut between workgroups is joined by the last to arrive, from slots in the
@@ -722,10 +722,12 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_rows_kernel(Att
 
 constexpr int kFewRows = 32;
 
+// Buffers of keys and of values of a wave: two, or where 160 KB hold only one.
 template <int D, bool F8>
-constexpr int few_waves() {
-  return D == 256 && !F8 ? 2 : 4;
+constexpr int few_buffers() {
+  return D == 256 && !F8 ? 1 : 2;
 }
+constexpr int kFewWaves = 4;
 template <int D>
 constexpr size_t few_slot() {
   return (size_t)kFewRows * (D + 2) * 4;
@@ -761,17 +763,22 @@ struct FewCursor {
   uint32_t end = 0;       // the cost up to each one's end
   uint32_t units = 0;
 
+  // To the next 64; the cost up to their end.
+  __device__ __forceinline__ uint32_t more(const AttnParams& p, int lane, uint32_t before) {
+    chunk += 64;
+    units = 0;
+    int lo;
+    if (chunk + lane < p.B) units = few_units(p, sequence(p, chunk + lane), KUNIT, &lo);
+    end = before + (uint32_t)wave_scan((int)few_cost(units), lane) * (uint32_t)p.Hkv;
+    return (uint32_t)__builtin_amdgcn_readlane((int)end, 63);
+  }
+
   // To the next part of a head that has keys to do; false at the run's end.
   __device__ __forceinline__ bool next(const AttnParams& p, int lane, FewPart* part) {
     while (u < ue) {
       const uint64_t past = __ballot(end > u);
       if (past == 0) {
-        const uint32_t before = (uint32_t)uniform(__shfl((int)end, 63));
-        chunk += 64;
-        units = 0;
-        int lo;
-        if (chunk + lane < p.B) units = few_units(p, sequence(p, chunk + lane), KUNIT, &lo);
-        end = before + (uint32_t)wave_scan((int)few_cost(units), lane) * (uint32_t)p.Hkv;
+        more(p, lane, (uint32_t)__builtin_amdgcn_readlane((int)end, 63));
         continue;
       }
       const int who = __builtin_ctzll(past);
@@ -802,38 +809,37 @@ __device__ __forceinline__ int few_tiles(const FewPart& x, int wave, int* key) {
   return x.seq.L > *key ? min(x.nu, (x.seq.L - *key + KUNIT - 1) / KUNIT) : 0;
 }
 
-template <int D, bool F8, int W>
-__global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_few_kernel(AttnParams p) {
+template <int D, bool F8>
+__global__ __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) void attn_few_kernel(AttnParams p) {
   typedef Cache<D, F8> L;
   typedef Rows<D, F8, 1, 1> R;
   typedef Share<D, F8, 32, 1> S;
+  constexpr int W = kFewWaves, NB = few_buffers<D, F8>();
   constexpr int kTile = 32 * L::kRow, kUnit = 32 * W, kLoads = S::kLoads, kThreads = 64 * W;
   // Where the waves meet, as much as leaves two workgroups to a CU or is left of one.
-  constexpr int kMeet = 4 * W * kTile > 65536 ? 16384 : 8192;
+  constexpr int kRing = 2 * NB * W * kTile, kMeet = kRing > 65536 ? 16384 : 8192;
   constexpr uint32_t kPairs = kMeet / sizeof(float2);  // maxima and sums of parts that are joined at once
-  __shared__ __align__(1024) uint8_t lds[4 * W * kTile];
+  __shared__ __align__(1024) uint8_t lds[kRing];
   __shared__ __align__(1024) uint8_t meet_lds[kMeet];
   __shared__ __align__(256) uint32_t ids[W][4][64];
   __shared__ float meet_m[W][64], meet_l[W][64];
   __shared__ uint32_t arrived;
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), h = lane >> 5, r = lane & 31;
 
-  uint32_t total = 0;
-  for (int at = 0; at < p.B; at += 64) {
-    uint32_t units = 0;
-    int lo;
-    if (at + lane < p.B) units = few_units(p, sequence(p, at + lane), kUnit, &lo);
-    total += (uint32_t)uniform(__shfl(wave_scan((int)few_cost(units), lane), 63));
-  }
-  total *= (uint32_t)p.Hkv;
-  const uint32_t share = max((total + gridDim.x - 1) / gridDim.x, kFewShare);
   FewCursor<kUnit> at_head;
+  uint32_t total = at_head.more(p, lane, 0);
+  if (p.B > 64) {
+    FewCursor<kUnit> rest = at_head;
+    while (rest.chunk + 64 < p.B) total = rest.more(p, lane, total);
+  }
+  const uint32_t share = max((total + gridDim.x - 1) / gridDim.x, kFewShare);
   at_head.u = min(total, blockIdx.x * share);
   at_head.ue = min(total, at_head.u + share);
+  if (at_head.u >= at_head.ue) return;
   FewCursor<kUnit> ahead = at_head;  // where the loads are
 
-  // This wave's ring: two buffers of keys, two of values.
-  const uint32_t k_lds = lds_offset(lds) + (uint32_t)wave * 4 * kTile, v_lds = k_lds + 2 * kTile;
+  // This wave's ring: NB buffers of keys, as many of values.
+  const uint32_t k_lds = lds_offset(lds) + (uint32_t)wave * 2 * NB * kTile, v_lds = k_lds + NB * kTile;
   const uint32_t id_lds = lds_offset(&ids[wave][0][0]);
   S at_keys;     // of the tile that is loaded
   FewPart coming{};
@@ -860,15 +866,6 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_few_kernel(Attn
     --left;
     return true;
   };
-  int sent = 0;  // tiles on their way or there, not multiplied yet
-  uint32_t ring = 0;
-  while (sent < 2 && find()) {
-    at_keys.template issue<false, true>(from, k_lds + sent * kTile, 0, lane);
-    at_keys.template issue<true, true>(from, v_lds + sent * kTile, 0, lane);
-    bad_tile[sent] = bad_page;
-    ++sent;
-  }
-
   R w;
   FewPart now, then;
   // The rows of a part's head, on their way while the waves meet over the last one's.
@@ -882,6 +879,14 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_few_kernel(Attn
   constexpr bool kEarly = D < 256;  // there are no registers for it beside wide heads
   bool any = at_head.next(p, lane, &now);
   if (kEarly && any) take_rows(now);
+  int sent = 0;  // tiles on their way or there, not multiplied yet
+  uint32_t ring = 0;
+  while (sent < NB && find()) {
+    at_keys.template issue<false, true>(from, k_lds + sent * kTile, 0, lane);
+    at_keys.template issue<true, true>(from, v_lds + sent * kTile, 0, lane);
+    bad_tile[sent] = bad_page;
+    ++sent;
+  }
   while (any) {
     if (!kEarly) take_rows(now);
     const Seq seq = now.seq;
@@ -894,26 +899,26 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_few_kernel(Attn
     // In order of issue: .., K(t) V(t), K(t+1) V(t+1), .. with ids between; loads
     // that come after what is waited for may stay under way.
     for (int j = 0; j < nt; ++j, base += kUnit) {
-      const uint32_t at = (ring & 1) * kTile;
+      const uint32_t at = (ring & (NB - 1)) * kTile;
       bad |= bad_tile[0];
       bad_tile[0] = bad_tile[1];
-      if (sent == 2)
-        wait_vmem<3 * kLoads>();  // K(t)
+      if (sent == NB)
+        wait_vmem<(2 * NB - 1) * kLoads>();  // K(t)
       else
         wait_vmem<kLoads>();
       f32x16 s[1][1];
       bf16x8 prob[1][1][2];
       w.scores(s, k_lds + at, lane);
       bool more = false;
-      if (sent == 2) {
+      if (sent == NB) {
         more = find();
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // K(t) is read before K(t+2) lands there
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // K(t) is read before K(t+NB) lands there
         if (more) {
           at_keys.template issue<false, true>(from, k_lds + at, 0, lane);
-          bad_tile[1] = bad_page;
-          wait_vmem<3 * kLoads>();  // V(t)
+          bad_tile[NB - 1] = bad_page;
+          wait_vmem<(2 * NB - 1) * kLoads>();  // V(t)
         } else {
-          wait_vmem<2 * kLoads>();
+          wait_vmem<(2 * NB - 2) * kLoads>();
         }
       } else {
         wait_vmem<0>();
@@ -925,7 +930,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_few_kernel(Attn
       w.softmax(s, prob, p.c);
       w.add_values(prob, v_lds + at, lane);
       if (more) {
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // V(t) is read before V(t+2) lands there
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // V(t) is read before V(t+NB) lands there
         at_keys.template issue<true, true>(from, v_lds + at, 0, lane);
       } else {
         --sent;
@@ -1063,7 +1068,8 @@ template <int D>
 int rows_splits(const AttnParams& p, int waves) {
   const int64_t groups = tiles_bound(p, waves) * p.Hkv;
   if (groups <= 0 || groups > kOpsCounters) return 1;
-  int64_t most = (p.max_len + kRowsKeys - 1) / kRowsKeys / 8;
+  const int64_t keys = p.window > 0 && p.window + 32 * waves < p.max_len ? p.window + 32 * waves : p.max_len;
+  int64_t most = (keys + kRowsKeys - 1) / kRowsKeys / 8;
   const int64_t room = (int64_t)(kOpsPartBytes / rows_part<D>(waves)) / groups;
   if (most > room) most = room;
   int best = 1;
@@ -1104,10 +1110,10 @@ hipError_t launch_format(AttnParams p, hipStream_t s) {
       e = launch(attn_rows_kernel<D, F8, 4>, dim3(grid), dim3(256), 0, s, p);
     if (e != hipSuccess || !few) return e;
   }
-  constexpr int W = few_waves<D, F8>(), kUnit = 32 * W;
+  constexpr int kUnit = 32 * kFewWaves;
   const int64_t units = (int64_t)p.B * p.Hkv * (p.max_len / kUnit + 2);
   const unsigned grid = (unsigned)(units < few_grid<D, F8>() ? units : few_grid<D, F8>());
-  return launch(attn_few_kernel<D, F8, W>, dim3(grid), dim3(64 * W), 0, s, p);
+  return launch(attn_few_kernel<D, F8>, dim3(grid), dim3(64 * kFewWaves), 0, s, p);
 }
 
 }  // namespace
