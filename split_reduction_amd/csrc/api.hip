@@ -623,7 +623,7 @@ SKGEMM_API const char* skgemm_strerror(int code) {
     case SKGEMM_OK: return "success";
     case SKGEMM_EINVAL: return "invalid argument (null pointer, negative size, split_k not in {1,2,4,8}, or a value the call does not take)";
     case SKGEMM_EALIGN: return "pointer or stride not aligned as the call needs (16 bytes unless stated)";
-    case SKGEMM_ESHAPE: return "unsupported shape (N % 16, K % (32*split_k) or K % (128*split_k) for MXFP4, K % 16 for 8-bit integers, H % 8 for the norm, or size limit)";
+    case SKGEMM_ESHAPE: return "unsupported shape (N % 16, K % (32*split_k) or K % (128*split_k) for MXFP4, K % 16 for 8-bit integers, H % 8 for the norm, the sizes of heads and pages, or size limit)";
     case SKGEMM_ENOMEM: return "workspace could not be allocated (or would be during stream capture: call skgemm_reserve or skgemm_reserve_ops first)";
     case SKGEMM_EHIP: return "HIP runtime error (see skgemm_last_hip_error)";
     case SKGEMM_ESCRATCH: return "the call needs more split-K partials than the fixed scratch of skgemm_bf16_noalloc holds (split_k * min(T,128) * N * 4 bytes; see SKGEMM_NOALLOC_SCRATCH_BYTES)";

@@ -526,6 +526,18 @@ __device__ __forceinline__ bool arrive_last(uint32_t* cnt, uint32_t all, uint32_
 // on its way while one is multiplied.
 
 constexpr int kRowsKeys = 64;
+constexpr int kFewRows = 32;  // of a sequence's key head, at most, for the other form
+
+// The workspace: the few rows' slots and counters first, then these.
+constexpr int kFewCounters = 2 * kChipCUs;
+template <int D>
+constexpr size_t few_slot() {
+  return (size_t)kFewRows * (D + 2) * 4;
+}
+template <int D>
+constexpr size_t few_part() {
+  return (size_t)2 * kFewCounters * few_slot<D>();
+}
 
 // Waves of the larger form; each has a 64th of a tile's bytes to load at least.
 template <int D, bool F8>
@@ -538,18 +550,23 @@ constexpr size_t rows_part(int waves) {  // bytes of a workgroup's results
 }
 
 template <int D, bool F8, int W>
-__global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_rows_kernel(AttnParams p) {
+constexpr int rows_lds() {
+  return 4 * kRowsKeys * Cache<D, F8>::kRow + W * 2 * 64 * 4 + 16;
+}
+
+// Workgroup `block` of these.
+template <int D, bool F8, int W>
+__device__ __forceinline__ void rows_body(const AttnParams& p, int block, uint8_t* lds) {
   typedef Cache<D, F8> L;
   constexpr int RT = 1;
   typedef Rows<D, F8, RT, 2> R;
   constexpr int BM = 32 * W, kHalf = kRowsKeys * L::kRow;  // bytes of a tile's keys
-  constexpr int kBuffers = 2;
-  __shared__ __align__(1024) uint8_t lds[2 * kBuffers * kHalf];  // keys, then values
-  __shared__ __align__(256) uint32_t ids[W][2][64];
-  __shared__ uint32_t arrived;
+  constexpr int kBuffers = 2;                              // of keys, then as many of values
+  uint32_t(*const ids)[2][64] = reinterpret_cast<uint32_t(*)[2][64]>(lds + 2 * kBuffers * kHalf);
+  uint32_t* const arrived = reinterpret_cast<uint32_t*>(ids + W);
   const int lane = (int)threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), h = lane >> 5;
 
-  int rest = (int)blockIdx.x;
+  int rest = block;
   const int kvh = rest % p.Hkv;
   rest /= p.Hkv;
   const int split = rest % p.S, flat = rest / p.S;
@@ -655,7 +672,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_rows_kernel(Att
     constexpr int kQuads = RT * R::kDT * 4;
     const int group = flat * p.Hkv + kvh;
     const uint32_t one = (uint32_t)rows_part<D>(W);
-    uint8_t* const base = p.part + (size_t)group * p.S * one;
+    uint8_t* const base = p.part + few_part<D>() + (size_t)group * p.S * one;
     const rsrc_t part = make_rsrc(base, (uint32_t)p.S * one);
     const uint32_t mine = (uint32_t)split * one, at = threadIdx.x * 16u;
 #pragma unroll
@@ -671,7 +688,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_rows_kernel(Att
       coherent_store(sums + split * step + 128 * W * t, w.m[t]);
       coherent_store(sums + split * step + 128 * W * t + 64 * W, w.l[t]);
     }
-    if (!arrive_last(p.cnt + (size_t)group * kOpsCounterStride, (uint32_t)p.S, &arrived)) return;
+    if (!arrive_last(p.cnt + (size_t)(kFewCounters + group) * kOpsCounterStride, (uint32_t)p.S, arrived)) return;
     float top[RT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
@@ -720,19 +737,12 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_rows_kernel(Att
 // cut between workgroups is joined by the last to arrive, from slots in the
 // workspace, in the order of its keys.
 
-constexpr int kFewRows = 32;
-
 // Buffers of keys and of values of a wave: two, or where 160 KB hold only one.
 template <int D, bool F8>
 constexpr int few_buffers() {
   return D == 256 && !F8 ? 1 : 2;
 }
 constexpr int kFewWaves = 4;
-template <int D>
-constexpr size_t few_slot() {
-  return (size_t)kFewRows * (D + 2) * 4;
-}
-
 constexpr uint32_t kHeadUnits = 3;  // what a head costs beside its keys, in units
 constexpr uint32_t kFewShare = 4;   // units of a workgroup at least: a join costs about as much
 
@@ -762,13 +772,18 @@ struct FewCursor {
   int chunk = -64;        // 64 sequences that are looked at, one a lane:
   uint32_t end = 0;       // the cost up to each one's end
   uint32_t units = 0;
+  int4* seqs;             // LDS: the first 64 sequences and their first keys
 
   // To the next 64; the cost up to their end.
   __device__ __forceinline__ uint32_t more(const AttnParams& p, int lane, uint32_t before) {
     chunk += 64;
     units = 0;
-    int lo;
-    if (chunk + lane < p.B) units = few_units(p, sequence(p, chunk + lane), KUNIT, &lo);
+    if (chunk + lane < p.B) {
+      const Seq s = sequence(p, chunk + lane);
+      int lo;
+      units = few_units(p, s, KUNIT, &lo);
+      if (chunk == 0) seqs[lane] = int4{s.first, s.n, s.L, lo};  // every wave writes, and reads back, the same
+    }
     end = before + (uint32_t)wave_scan((int)few_cost(units), lane) * (uint32_t)p.Hkv;
     return (uint32_t)__builtin_amdgcn_readlane((int)end, 63);
   }
@@ -794,8 +809,14 @@ struct FewCursor {
       x.b = chunk + who;
       x.k0 = (int)(from - x.start);
       x.nu = (int)(to - from);
-      x.seq = sequence(p, x.b);
-      few_units(p, x.seq, KUNIT, &x.first);
+      if (x.b < 64) {
+        const int4 s = seqs[x.b];
+        x.seq = Seq{uniform(s.x), uniform(s.y), uniform(s.z)};
+        x.first = uniform(s.w);
+      } else {
+        x.seq = sequence(p, x.b);
+        few_units(p, x.seq, KUNIT, &x.first);
+      }
       return true;
     }
     return false;
@@ -809,37 +830,52 @@ __device__ __forceinline__ int few_tiles(const FewPart& x, int wave, int* key) {
   return x.seq.L > *key ? min(x.nu, (x.seq.L - *key + KUNIT - 1) / KUNIT) : 0;
 }
 
-template <int D, bool F8>
-__global__ __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) void attn_few_kernel(AttnParams p) {
+// What the few rows' workgroups keep in LDS beside their ring of NB buffers.
+template <int D, bool F8, int NB>
+struct FewLds {
+  static constexpr int kRing = 2 * NB * kFewWaves * 32 * Cache<D, F8>::kRow;
+  // Where the waves meet, as much as leaves two workgroups to a CU or is left of one.
+  static constexpr int kMeet = kRing > 65536 ? 16384 : 8192;
+  uint8_t ring[kRing];
+  uint8_t meet[kMeet];
+  uint32_t ids[kFewWaves][4][64];
+  float m[kFewWaves][64], l[kFewWaves][64];
+  int4 seqs[64];
+  uint32_t arrived;
+};
+
+// Workgroup `block` of `blocks`.
+template <int D, bool F8, int NB>
+__device__ __forceinline__ void few_body(const AttnParams& p, uint32_t block, uint32_t blocks, uint8_t* lds_bytes) {
   typedef Cache<D, F8> L;
   typedef Rows<D, F8, 1, 1> R;
   typedef Share<D, F8, 32, 1> S;
-  constexpr int W = kFewWaves, NB = few_buffers<D, F8>();
-  constexpr int kTile = 32 * L::kRow, kUnit = 32 * W, kLoads = S::kLoads, kThreads = 64 * W;
-  // Where the waves meet, as much as leaves two workgroups to a CU or is left of one.
-  constexpr int kRing = 2 * NB * W * kTile, kMeet = kRing > 65536 ? 16384 : 8192;
+  typedef FewLds<D, F8, NB> M;
+  M& mem = *reinterpret_cast<M*>(lds_bytes);
+  constexpr int W = kFewWaves;
+  constexpr int kTile = 32 * L::kRow, kUnit = 32 * W, kLoads = S::kLoads, kThreads = 64 * W, kMeet = M::kMeet;
   constexpr uint32_t kPairs = kMeet / sizeof(float2);  // maxima and sums of parts that are joined at once
-  __shared__ __align__(1024) uint8_t lds[kRing];
-  __shared__ __align__(1024) uint8_t meet_lds[kMeet];
-  __shared__ __align__(256) uint32_t ids[W][4][64];
-  __shared__ float meet_m[W][64], meet_l[W][64];
-  __shared__ uint32_t arrived;
+  uint8_t* const meet_lds = mem.meet;
+  auto& ids = mem.ids;
+  auto& meet_m = mem.m;
+  auto& meet_l = mem.l;
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), h = lane >> 5, r = lane & 31;
 
   FewCursor<kUnit> at_head;
+  at_head.seqs = mem.seqs;
   uint32_t total = at_head.more(p, lane, 0);
   if (p.B > 64) {
     FewCursor<kUnit> rest = at_head;
     while (rest.chunk + 64 < p.B) total = rest.more(p, lane, total);
   }
-  const uint32_t share = max((total + gridDim.x - 1) / gridDim.x, kFewShare);
-  at_head.u = min(total, blockIdx.x * share);
+  const uint32_t share = max((total + blocks - 1) / blocks, kFewShare);
+  at_head.u = min(total, block * share);
   at_head.ue = min(total, at_head.u + share);
   if (at_head.u >= at_head.ue) return;
   FewCursor<kUnit> ahead = at_head;  // where the loads are
 
   // This wave's ring: NB buffers of keys, as many of values.
-  const uint32_t k_lds = lds_offset(lds) + (uint32_t)wave * 2 * NB * kTile, v_lds = k_lds + NB * kTile;
+  const uint32_t k_lds = lds_offset(mem.ring) + (uint32_t)wave * 2 * NB * kTile, v_lds = k_lds + NB * kTile;
   const uint32_t id_lds = lds_offset(&ids[wave][0][0]);
   S at_keys;     // of the tile that is loaded
   FewPart coming{};
@@ -992,7 +1028,7 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) void attn_few_ker
         if (whole) {
           put(row, 4 * d0 + c4, o, m, l);
         } else {
-          uint8_t* const to = slot(blockIdx.x - wg0);
+          uint8_t* const to = slot(block - wg0);
           st16_coherent_if(true, __builtin_bit_cast(u32x4, o), make_rsrc(to, (uint32_t)kSlot),
                            16u * (uint32_t)(row * (D / 4) + 4 * d0 + c4));
           if (d0 == 0 && c4 == 0) {
@@ -1004,7 +1040,7 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) void attn_few_ker
       }
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     }
-    if (!whole && arrive_last(p.cnt + (size_t)wg0 * kOpsCounterStride, parts, &arrived)) {
+    if (!whole && arrive_last(p.cnt + (size_t)wg0 * kOpsCounterStride, parts, &mem.arrived)) {
       // Maxima and sums of `some` parts at once through LDS; values as they come.
       float2* const join_ml = reinterpret_cast<float2*>(meet_lds);
       const uint32_t some = kPairs / (uint32_t)rows;
@@ -1052,6 +1088,38 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) void attn_few_ker
   }
 }
 
+template <int D, bool F8, int W>
+__global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attn_rows_kernel(AttnParams p) {
+  __shared__ __align__(1024) uint8_t lds[rows_lds<D, F8, W>()];
+  rows_body<D, F8, W>(p, (int)blockIdx.x, lds);
+}
+
+template <int D, bool F8>
+__global__ __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) void attn_few_kernel(AttnParams p) {
+  constexpr int NB = few_buffers<D, F8>();
+  __shared__ __align__(1024) uint8_t lds[sizeof(FewLds<D, F8, NB>)];
+  few_body<D, F8, NB>(p, blockIdx.x, gridDim.x, lds);
+}
+
+// Both at once, for batches that may hold sequences of either kind: the first
+// few_blocks workgroups take those of few rows. One launch, and the short work of one
+// kind hides under the other's (a mixed batch of 37: see launch_format). Heads of 128
+// have one buffer less than on their own, so that two workgroups fit a CU.
+template <int D, bool F8>
+constexpr int mixed_buffers() {
+  return D == 256 ? few_buffers<D, F8>() : D == 128 && !F8 ? 1 : 2;
+}
+template <int D, bool F8>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_mixed_kernel(AttnParams p, int few_blocks) {
+  constexpr int NB = mixed_buffers<D, F8>();
+  constexpr int kRows = rows_lds<D, F8, 4>(), kFew = (int)sizeof(FewLds<D, F8, NB>);
+  __shared__ __align__(1024) uint8_t lds[kRows > kFew ? kRows : kFew];
+  if ((int)blockIdx.x < few_blocks)
+    few_body<D, F8, NB>(p, blockIdx.x, (uint32_t)few_blocks, lds);
+  else
+    rows_body<D, F8, 4>(p, (int)blockIdx.x - few_blocks, lds);
+}
+
 // Tiles of the rows kernel at most: it has a workgroup for each, and those past
 // what the lengths give end at once.
 int64_t tiles_bound(const AttnParams& p, int waves) {
@@ -1067,10 +1135,10 @@ int64_t tiles_bound(const AttnParams& p, int waves) {
 template <int D>
 int rows_splits(const AttnParams& p, int waves) {
   const int64_t groups = tiles_bound(p, waves) * p.Hkv;
-  if (groups <= 0 || groups > kOpsCounters) return 1;
+  if (groups <= 0 || groups > kOpsCounters - kFewCounters) return 1;
   const int64_t keys = p.window > 0 && p.window + 32 * waves < p.max_len ? p.window + 32 * waves : p.max_len;
   int64_t most = (keys + kRowsKeys - 1) / kRowsKeys / 8;
-  const int64_t room = (int64_t)(kOpsPartBytes / rows_part<D>(waves)) / groups;
+  const int64_t room = (int64_t)((kOpsPartBytes - few_part<D>()) / rows_part<D>(waves)) / groups;
   if (most > room) most = room;
   int best = 1;
   auto rounds = [&](int64_t s) { return (groups * s + kChipCUs - 1) / kChipCUs; };
@@ -1087,10 +1155,13 @@ constexpr int few_grid() {
 
 template <int D, bool F8>
 hipError_t launch_format(AttnParams p, hipStream_t s) {
-  static_assert((size_t)2 * few_grid<D, F8>() * few_slot<D>() <= kOpsPartBytes && few_grid<D, F8>() <= kOpsCounters, "slots fit");
+  static_assert(few_grid<D, F8>() <= kFewCounters && few_part<D>() < kOpsPartBytes && kFewCounters < kOpsCounters, "slots fit");
   // A batch may hold sequences of both kinds; a single sequence goes by its bound.
   const bool many = (int64_t)p.max_q * p.G > kFewRows, few = !many || p.B > 1;
   p.few = few ? kFewRows : 0;
+  constexpr int kUnit = 32 * kFewWaves;
+  const int64_t units = (int64_t)p.B * p.Hkv * (p.max_len / kUnit + 2);
+  const unsigned few_blocks = !few ? 0 : (unsigned)(units < few_grid<D, F8>() ? units : few_grid<D, F8>());
   if (many) {
     // Eight waves of a workgroup share a tile's keys, which halves what comes from the
     // L2; two workgroups of four fill a CU as well, go at their own pace and waste
@@ -1102,18 +1173,16 @@ hipError_t launch_format(AttnParams p, hipStream_t s) {
     const bool large = kMost == 8 && (p.S > 1 || (D == 128 && p.window == 0 && tiles_bound(p, 8) * p.Hkv >= 4 * kChipCUs));
     const int waves = large ? 8 : 4;
     const unsigned grid = (unsigned)(tiles_bound(p, waves) * p.Hkv * p.S);
-    hipError_t e;
-    if constexpr (kMost == 8)
-      e = large ? launch(attn_rows_kernel<D, F8, 8>, dim3(grid), dim3(512), 0, s, p)
-                : launch(attn_rows_kernel<D, F8, 4>, dim3(grid), dim3(256), 0, s, p);
-    else
-      e = launch(attn_rows_kernel<D, F8, 4>, dim3(grid), dim3(256), 0, s, p);
-    if (e != hipSuccess || !few) return e;
+    if constexpr (kMost == 8) {
+      if (large) {
+        const hipError_t e = launch(attn_rows_kernel<D, F8, 8>, dim3(grid), dim3(512), 0, s, p);
+        if (e != hipSuccess || !few) return e;
+      }
+    }
+    if (!large && few) return launch(attn_mixed_kernel<D, F8>, dim3(few_blocks + grid), dim3(256), 0, s, p, (int)few_blocks);
+    if (!large) return launch(attn_rows_kernel<D, F8, 4>, dim3(grid), dim3(256), 0, s, p);
   }
-  constexpr int kUnit = 32 * kFewWaves;
-  const int64_t units = (int64_t)p.B * p.Hkv * (p.max_len / kUnit + 2);
-  const unsigned grid = (unsigned)(units < few_grid<D, F8>() ? units : few_grid<D, F8>());
-  return launch(attn_few_kernel<D, F8>, dim3(grid), dim3(64 * kFewWaves), 0, s, p);
+  return launch(attn_few_kernel<D, F8>, dim3(few_blocks), dim3(64 * kFewWaves), 0, s, p);
 }
 
 }  // namespace

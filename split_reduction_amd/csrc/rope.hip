@@ -16,6 +16,10 @@
 // into LDS, while its first heads are on their way. The angle is a product in
 // FP64, reduced to part of a turn there: FP32 has lost a position of 2^20 to 0.06
 // radians.
+//
+// Bound by memory (4 bytes an element of the queries, 6 or 8 of keys and values)
+// and below that by the launch. T=8192 of 64 heads of 128: 48.7 us, 5.5 TB/s (a large
+// copy reaches 5.1); T=1 of 16: 3.2 us, the call 7.4.
 
 #include "device/pack.h"
 #include "device/wave.h"
@@ -42,7 +46,8 @@ __device__ __forceinline__ float to_code_range(float v) {
   return v != v ? v : fminf(fmaxf(v, -448.0f), 448.0f);
 }
 
-template <int L, bool INTER, bool CODES>
+// STREAM: heads are loaded non-temporally.
+template <int L, bool INTER, bool CODES, bool STREAM>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p) {
   constexpr int kSlots = kThreads / L;  // heads at once
   extern __shared__ float2 turn[];      // [tokens of the workgroup][rot / 2]: cos, sin
@@ -73,8 +78,9 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p) {
       row = p.k + (size_t)it.t * p.k_stride + (size_t)(it.h - p.Hq) * p.D * 2;
     else
       row = p.v + (size_t)it.t * p.v_stride + (size_t)(it.h - p.Hq - p.Hkv) * p.D * 2;
-    it.a = reinterpret_cast<const u32x4*>(row)[va];
-    it.b = reinterpret_cast<const u32x4*>(row)[vb];
+    const u32x4* const vectors = reinterpret_cast<const u32x4*>(row);
+    it.a = STREAM ? __builtin_nontemporal_load(vectors + va) : vectors[va];
+    it.b = STREAM ? __builtin_nontemporal_load(vectors + vb) : vectors[vb];
     return it;
   };
 
@@ -178,6 +184,17 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p) {
   }
 }
 
+template <int L, bool STREAM>
+hipError_t launch_kind(const RopeParams& p, bool inter, bool codes, dim3 grid, size_t lds, hipStream_t s) {
+  const dim3 block(kThreads);
+  if (inter) {
+    if (codes) return launch(rope_kernel<L, true, true, STREAM>, grid, block, lds, s, p);
+    return launch(rope_kernel<L, true, false, STREAM>, grid, block, lds, s, p);
+  }
+  if (codes) return launch(rope_kernel<L, false, true, STREAM>, grid, block, lds, s, p);
+  return launch(rope_kernel<L, false, false, STREAM>, grid, block, lds, s, p);
+}
+
 template <int L>
 hipError_t launch_lanes(RopeParams p, bool inter, bool codes, hipStream_t s) {
   constexpr int kSlots = kThreads / L;
@@ -192,13 +209,13 @@ hipError_t launch_lanes(RopeParams p, bool inter, bool codes, hipStream_t s) {
     gy = (unsigned)((heads + kSlots - 1) / kSlots);
   }
   const size_t lds = (size_t)p.tokens * (size_t)(p.rot / 2) * sizeof(float2);  // at most 16 KB
-  const dim3 grid(gx, gy), block(kThreads);
-  if (inter) {
-    if (codes) return launch(rope_kernel<L, true, true>, grid, block, lds, s, p);
-    return launch(rope_kernel<L, true, false>, grid, block, lds, s, p);
-  }
-  if (codes) return launch(rope_kernel<L, false, true>, grid, block, lds, s, p);
-  return launch(rope_kernel<L, false, false>, grid, block, lds, s, p);
+  // More than the last cache holds is loaded non-temporally: T=8192 of 64 heads of
+  // 128 51.6 -> 48.7 us, with 8 key heads into E4M3 71.4 -> 68.5; T=4096 of 32 and 8
+  // heads, which it holds, 23.3 -> 26.1.
+  const size_t bytes = (size_t)p.T * p.D * (4 * (size_t)p.Hq + (codes ? 6 : 8) * (size_t)p.Hkv);
+  const dim3 grid(gx, gy);
+  if (bytes > ((size_t)256 << 20)) return launch_kind<L, true>(p, inter, codes, grid, lds, s);
+  return launch_kind<L, false>(p, inter, codes, grid, lds, s);
 }
 
 }  // namespace
