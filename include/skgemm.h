@@ -416,7 +416,7 @@ SKGEMM_API int skgemm_rope_append(const void* Q, const void* K, const void* V, c
  *   max_q       at least every n: what the launch is sized for (a sequence's tokens
  *               past it are left out). window 0: none.
  *   D is 64, 128 or 256; Hq % Hkv == 0; max_pages * page_size <= SKGEMM_MAX_LEN; T
- *   * (Hq / Hkv) <= 2^30, B <= 2^20, and B * Hkv * (max_pages * page_size / 64 + 1)
+ *   * (Hq / Hkv) <= 2^30, B <= 2^20, and B * Hkv * (max_pages * page_size / 64 + 8)
  *   and (T * (Hq / Hkv) / 128 + B) * Hkv below 2^31 (SKGEMM_ESHAPE). 0 < scale <=
  *   SKGEMM_MAX_SCALE, also times k_scale. Q and O are 16-byte aligned with strides
  *   that are multiples of 16; arrays of int32 and float 4.

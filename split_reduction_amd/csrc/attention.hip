@@ -141,9 +141,9 @@ struct Share {
     }
     return bad;
   }
-  // VALUES: the values, else the keys, to KEYS rows at `lds`. STREAM: nobody else
-  // reads them.
-  template <bool VALUES, bool STREAM>
+  // VALUES: the values, else the keys, to KEYS rows at `lds`, non-temporally: nobody
+  // else reads them (64 tokens over 213k cached: 214 -> 194 us).
+  template <bool VALUES>
   __device__ __forceinline__ void issue(const Pages& c, uint32_t lds, int wave, int lane) const {
     // What follows from the lane is the same for every tile; kept from one to the next
     // it would take more registers than there are (D = 256: spills).
@@ -152,10 +152,10 @@ struct Share {
     for (int q = 0; q < kLoads; ++q) {
       const int row = (wave * kLoads + q) * L::kRows + lane / L::kChunks, at = lane % L::kChunks;
       const int chunk = at ^ (VALUES ? L::value_swizzle(row) : L::key_swizzle(row));
-      global16_to_lds<STREAM>((VALUES ? c.v : c.k) + place(c, q, row) + 16 * chunk, lds + (uint32_t)(wave * kLoads + q) * 1024u);
+      global16_to_lds<true>((VALUES ? c.v : c.k) + place(c, q, row) + 16 * chunk, lds + (uint32_t)(wave * kLoads + q) * 1024u);
     }
   }
-  // Both.
+  // Both, for a key head that other workgroups read as well.
   __device__ __forceinline__ void issue_both(const Pages& c, uint32_t keys, uint32_t values, int wave, int lane) const {
 #pragma unroll
     for (int q = 0; q < kLoads; ++q) {
@@ -332,12 +332,13 @@ struct Rows {
 #pragma unroll
         for (int d = 0; d < kDT; ++d) o[t][d] *= by;
       }
+      float sum = 0.0f;  // the tile's, so that long rows add few numbers of unlike size
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           s[t][kb][e] = __builtin_amdgcn_exp2f(fmaf(s[t][kb][e], c, -m[t]));
-          l[t] += s[t][kb][e];
+          sum += s[t][kb][e];
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -347,6 +348,7 @@ struct Rows {
           p[t][kb][x] = as_bf16x8(w);
         }
       }
+      l[t] += sum;
     }
   }
 
@@ -451,14 +453,15 @@ struct Rows {
 // ---- sequences ----
 
 struct Seq {
-  int first, n, L;  // its first row of Q, new tokens, tokens in all
+  int first, n, L;  // its first row of Q, new tokens, tokens up to the last of them
 };
 // Whatever the arrays hold, rows stay inside Q and keys inside the table.
 __device__ __forceinline__ Seq sequence(const AttnParams& p, int b) {
   Seq s;
   s.first = min(max(p.q_start[b], 0), p.T);
-  s.n = min(min(max(p.q_start[b + 1], s.first), p.T) - s.first, p.max_q);
-  s.L = min(max(p.kv_len[b], 0), p.max_len);
+  const int all = min(max(p.q_start[b + 1], s.first), p.T) - s.first;
+  s.n = min(all, p.max_q);
+  s.L = min(max(p.kv_len[b], 0), p.max_len) - (all - s.n);
   return s;
 }
 
@@ -520,10 +523,15 @@ __device__ __forceinline__ bool arrive_last(uint32_t* cnt, uint32_t all, uint32_
   return mine;
 }
 
-// ---- many rows: a workgroup takes 256 rows of a key head (128 of wide heads) ----
+// ---- many rows: a workgroup takes 128 or 256 rows of a key head ----
 //
-// Waves of 32 rows share tiles of 64 keys, two buffers: the next tile is
-// on its way while one is multiplied.
+// Four or eight waves of 32 rows share tiles of 64 keys, two buffers: the next
+// tile is on its way while one is multiplied. The matrix units bound it, with the
+// softmax's vector instructions beside them (about 180 of them and 32 exponentials for 32
+// matrix instructions): 8192 tokens of 32 heads of 128 take 550 us, 1.0 PFLOP/s of visible
+// pairs, where a large library product reaches 1.22. Two waves of a SIMD in turns,
+// one multiplying while the other has the softmax, with two barriers a tile: 610
+// against 567 us; operands read six to nine ahead instead of four: no gain.
 
 constexpr int kRowsKeys = 64;
 constexpr int kFewRows = 32;  // of a sequence's key head, at most, for the other form
@@ -622,43 +630,35 @@ __device__ __forceinline__ void rows_body(const AttnParams& p, int block, uint8_
   const int last = khi - 1;
   Share<D, F8, 64, W> share;
 
-  // Tiles j .. end - 1, all waves in step, two buffers; some may be hidden from some row.
-  auto in_step = [&](int j, int end) {
-    if (j >= end) return;
-    const int from = j;
-    issue_ids<64>(c, kal + 64 * j, last, id_lds, lane);
-    issue_ids<64>(c, kal + 64 * (j + 1), last, id_lds + 256, lane);
+  if (j0 < j1) {
+    issue_ids<64>(c, kal + 64 * j0, last, id_lds, lane);
+    issue_ids<64>(c, kal + 64 * (j0 + 1), last, id_lds + 256, lane);
     wait_vmem<0>();
-    bad |= share.find(c, kal + 64 * j, last, ids[wave][0], wave, lane);
-    share.template issue<false, false>(c, k_lds, wave, lane);
-    share.template issue<true, false>(c, v_lds, wave, lane);
-    issue_ids<64>(c, kal + 64 * (j + 2), last, id_lds, lane);
-    for (; j < end; ++j) {
-      const int at = (j - from) & 1, base = kal + 64 * j;
-      wait_vmem<1>();  // this wave's share of tile j; the ids of j + 2 may be under way
-      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      const uint32_t values = v_lds + (uint32_t)at * kHalf;
-      f32x16 s[1][2];
-      bf16x8 prob[1][2][2];
-      w.scores(s, k_lds + (uint32_t)at * kHalf, lane);
-      if (j + 1 < end) {  // behind the products, so that a SIMD's other wave can multiply meanwhile
-        const uint32_t next = (uint32_t)(at ^ 1);
-        bad |= share.find(c, base + 64, last, ids[wave][next], wave, lane);
-        share.issue_both(c, k_lds + next * kHalf, v_lds + next * kHalf, wave, lane);
-        issue_ids<64>(c, base + 192, last, id_lds + next * 256, lane);
-      }
-      if (base + 64 > see_min || base < lo_max) {
-        w.hide(s, base, lane);
-        w.template clean_values<W>(values, base, wave, lane);
-      }
-      w.softmax(s, prob, p.c);
-      w.add_values(prob, values, lane);
+    bad = share.find(c, kal + 64 * j0, last, ids[wave][0], wave, lane);
+    share.issue_both(c, k_lds, v_lds, wave, lane);
+    issue_ids<64>(c, kal + 64 * (j0 + 2), last, id_lds, lane);
+  }
+  for (int j = j0; j < j1; ++j) {
+    const int at = (j - j0) & 1, base = kal + 64 * j;
+    wait_vmem<1>();  // this wave's share of tile j; the ids of j + 2 may be under way
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    const uint32_t values = v_lds + (uint32_t)at * kHalf;
+    f32x16 s[1][2];
+    bf16x8 prob[1][2][2];
+    w.scores(s, k_lds + (uint32_t)at * kHalf, lane);
+    if (j + 1 < j1) {  // behind the product, so that a SIMD's other wave can multiply meanwhile
+      const uint32_t next = (uint32_t)(at ^ 1);
+      bad |= share.find(c, base + 64, last, ids[wave][next], wave, lane);
+      share.issue_both(c, k_lds + next * kHalf, v_lds + next * kHalf, wave, lane);
+      issue_ids<64>(c, base + 192, last, id_lds + next * 256, lane);
     }
-    wait_vmem<0>();
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // the buffers are free again
-  };
-
-  in_step(j0, j1);
+    if (base + 64 > see_min || base < lo_max) {
+      w.hide(s, base, lane);
+      w.template clean_values<W>(values, base, wave, lane);
+    }
+    w.softmax(s, prob, p.c);
+    w.add_values(prob, values, lane);
+  }
   wait_vmem<0>();
   w.lose();
   bad = __syncthreads_or(bad);
@@ -736,6 +736,10 @@ __device__ __forceinline__ void rows_body(const AttnParams& p, int block, uint8_
 // tiles ahead of the products, into the next head where one ends. A head that was
 // cut between workgroups is joined by the last to arrive, from slots in the
 // workspace, in the order of its keys.
+//
+// Bound by the cache's stream: 64 tokens over 213k cached of 8 key heads of 128, 873
+// MB, take 142 us, 6.1 TB/s (a read alone reaches 6.9); below about 30 MB by the chain
+// of loads (lengths, page ids, keys) and one joining, 13 us.
 
 // Buffers of keys and of values of a wave: two, or where 160 KB hold only one.
 template <int D, bool F8>
@@ -743,8 +747,11 @@ constexpr int few_buffers() {
   return D == 256 && !F8 ? 1 : 2;
 }
 constexpr int kFewWaves = 4;
-constexpr uint32_t kHeadUnits = 3;  // what a head costs beside its keys, in units
-constexpr uint32_t kFewShare = 4;   // units of a workgroup at least: a join costs about as much
+// What a head costs beside its keys, in units (that batch: 207 us with 1, 153 with 2,
+// 145 with 3 and 4), and the units of a workgroup at least (one token over 1000 of 2 key
+// heads: 16.4 us with 4, 19.0 with 6, 23.7 with 8; over 257 13.1, 12.8, 13.0).
+constexpr uint32_t kHeadUnits = 3;
+constexpr uint32_t kFewShare = 4;
 
 // Units of keys of a sequence for each key head, and the first key.
 __device__ __forceinline__ uint32_t few_units(const AttnParams& p, const Seq& s, int unit, int* first) {
@@ -918,8 +925,8 @@ __device__ __forceinline__ void few_body(const AttnParams& p, uint32_t block, ui
   int sent = 0;  // tiles on their way or there, not multiplied yet
   uint32_t ring = 0;
   while (sent < NB && find()) {
-    at_keys.template issue<false, true>(from, k_lds + sent * kTile, 0, lane);
-    at_keys.template issue<true, true>(from, v_lds + sent * kTile, 0, lane);
+    at_keys.template issue<false>(from, k_lds + sent * kTile, 0, lane);
+    at_keys.template issue<true>(from, v_lds + sent * kTile, 0, lane);
     bad_tile[sent] = bad_page;
     ++sent;
   }
@@ -950,7 +957,7 @@ __device__ __forceinline__ void few_body(const AttnParams& p, uint32_t block, ui
         more = find();
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // K(t) is read before K(t+NB) lands there
         if (more) {
-          at_keys.template issue<false, true>(from, k_lds + at, 0, lane);
+          at_keys.template issue<false>(from, k_lds + at, 0, lane);
           bad_tile[NB - 1] = bad_page;
           wait_vmem<(2 * NB - 1) * kLoads>();  // V(t)
         } else {
@@ -967,7 +974,7 @@ __device__ __forceinline__ void few_body(const AttnParams& p, uint32_t block, ui
       w.add_values(prob, v_lds + at, lane);
       if (more) {
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // V(t) is read before V(t+NB) lands there
-        at_keys.template issue<true, true>(from, v_lds + at, 0, lane);
+        at_keys.template issue<true>(from, v_lds + at, 0, lane);
       } else {
         --sent;
       }
@@ -1102,8 +1109,9 @@ __global__ __launch_bounds__(64 * kFewWaves, D == 256 ? 1 : 2) void attn_few_ker
 }
 
 // Both at once, for batches that may hold sequences of either kind: the first
-// few_blocks workgroups take those of few rows. One launch, and the short work of one
-// kind hides under the other's (a mixed batch of 37: see launch_format). Heads of 128
+// few_blocks workgroups take those of few rows. The short work of one kind hides
+// under the other's: a mixed batch of 37 takes 32.5 us against 41.5 with two launches, 16
+// prompts of up to 500 tokens 27 against 37, 4 x 2048 of 16 heads 106 against 106. Heads of 128
 // have one buffer less than on their own, so that two workgroups fit a CU.
 template <int D, bool F8>
 constexpr int mixed_buffers() {

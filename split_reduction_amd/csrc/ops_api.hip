@@ -440,7 +440,7 @@ SKGEMM_API int skgemm_paged_attention(const void* Q, const void* K_cache, const 
                        head_stride, false);
   if (rc != SKGEMM_OK) return rc;
   const int64_t most = (int64_t)1 << 31, G = Hq / Hkv, len = (int64_t)max_pages * page_size;
-  if (len > SKGEMM_MAX_LEN || T * G > ((int64_t)1 << 30) || B * (int64_t)Hkv * (len / 64 + 1) >= most ||
+  if (len > SKGEMM_MAX_LEN || T * G > ((int64_t)1 << 30) || B * (int64_t)Hkv * (len / 64 + 8) >= most ||
       (T * G / 128 + B) * Hkv >= most)
     return SKGEMM_ESHAPE;
   const float c = scale * k_scale;

@@ -214,7 +214,7 @@ hipError_t launch_lanes(RopeParams p, bool inter, bool codes, hipStream_t s) {
   // heads, which it holds, 23.3 -> 26.1.
   const size_t bytes = (size_t)p.T * p.D * (4 * (size_t)p.Hq + (codes ? 6 : 8) * (size_t)p.Hkv);
   const dim3 grid(gx, gy);
-  if (bytes > ((size_t)256 << 20)) return launch_kind<L, true>(p, inter, codes, grid, lds, s);
+  if (bytes >= ((size_t)256 << 20)) return launch_kind<L, true>(p, inter, codes, grid, lds, s);
   return launch_kind<L, false>(p, inter, codes, grid, lds, s);
 }
 

@@ -366,6 +366,23 @@ def test_cache_past_4_gib():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("seqs,max_q", [([(5, 60), (3, 9)], 2), ([(90, 200), (40, 40), (1, 7)], 33)])
+def test_rows_past_max_q_are_left_out(seqs, max_q):
+    """The rows before them sit where they would, the others are left as they were."""
+    t = torch()
+    c = Case(seqs, 2, 4, 128, 16, "bf16", "token", seed=9)
+    want, wl = c.run()
+    o, lse = c.run(max_q=max_q)
+    for b, (n, _) in enumerate(seqs):
+        a = int(c.starts[b])
+        k = min(n, max_q)
+        err = np.abs(f64(o[a : a + k]) - f64(want[a : a + k]))  # both within the bound of c.check, of the same value
+        assert np.all(err <= 4 * O.EPS_BF16 * np.maximum(np.abs(f64(want[a : a + k])), np.abs(f64(c.values[1][b])).max()))
+        assert np.allclose(lse[a : a + k].cpu(), wl[a : a + k].cpu(), rtol=0, atol=1e-4)
+        assert (f64(o[a + k : a + n]) == 7.75).all() and (lse[a + k : a + n] == -55).all()
+
+
+@pytest.mark.gpu
 def test_attention_empty_calls():
     t = torch()
     x = t.zeros(0, 128, dtype=t.bfloat16, device=DEV)
