@@ -85,7 +85,7 @@ struct RopeParams {
   size_t page_stride, slot_stride, head_stride;        // bytes, of both caches
   int64_t n_slots;
   int T, Hq, Hkv, D, rot, page_shift;
-  float eps, amplitude, k_inv, v_inv;
+  float eps, amplitude, k_inv, v_inv, by_d;  // by_d: 1 / D
   int tokens, per;  // tokens of a workgroup; heads of one (blockIdx.y takes the next)
 };
 

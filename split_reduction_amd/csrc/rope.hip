@@ -43,17 +43,18 @@ __device__ __forceinline__ float lanes_sum(float v) {
 }
 // A value on its way to an E4M3 code: saturated, NaN kept.
 __device__ __forceinline__ float to_code_range(float v) {
-  return v != v ? v : fminf(fmaxf(v, -448.0f), 448.0f);
+  return __builtin_elementwise_minimum(__builtin_elementwise_maximum(v, -448.0f), 448.0f);
 }
 
-// STREAM: heads are loaded non-temporally.
-template <int L, bool INTER, bool CODES, bool STREAM>
+// STREAM: heads are loaded non-temporally. ONE: a workgroup has heads of one token, so
+// that what goes by the token is the same in all lanes.
+template <int L, bool INTER, bool CODES, bool STREAM, bool ONE>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p) {
   constexpr int kSlots = kThreads / L;  // heads at once
   extern __shared__ float2 turn[];      // [tokens of the workgroup][rot / 2]: cos, sin
   const int u = (int)threadIdx.x % L, slot = (int)threadIdx.x / L;
   const int heads = p.Hq + 2 * p.Hkv, half = p.rot >> 1;
-  const int t0 = (int)blockIdx.x * p.tokens, nt = min(p.tokens, p.T - t0);
+  const int t0 = ONE ? (int)blockIdx.x : (int)blockIdx.x * p.tokens, nt = ONE ? 1 : min(p.tokens, p.T - t0);
   const int first = (int)blockIdx.y * p.per, last = min(nt * heads, first + p.per);
   const bool in_head = u < (p.D >> 4), turns = u < (p.rot >> 4);
   // This lane's two vectors: past the rotated ones, neighbours in both layouts.
@@ -67,17 +68,18 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p) {
   auto load = [&](int i) {
     Item it{};
     if (i >= last) return it;
-    const int tl = p.tokens == 1 ? 0 : i / heads;
+    const int tl = ONE ? 0 : i / heads;
     it.h = i - tl * heads;
-    it.t = t0 + tl;
+    if constexpr (!ONE) it.t = t0 + tl;
+    const int t = ONE ? t0 : it.t;
     if (!in_head) return it;
     const uint8_t* row;
     if (it.h < p.Hq)
-      row = p.q + (size_t)it.t * p.q_stride + (size_t)it.h * p.D * 2;
+      row = p.q + (size_t)t * p.q_stride + (uint32_t)(it.h * p.D * 2);
     else if (it.h < p.Hq + p.Hkv)
-      row = p.k + (size_t)it.t * p.k_stride + (size_t)(it.h - p.Hq) * p.D * 2;
+      row = p.k + (size_t)t * p.k_stride + (uint32_t)((it.h - p.Hq) * p.D * 2);
     else
-      row = p.v + (size_t)it.t * p.v_stride + (size_t)(it.h - p.Hq - p.Hkv) * p.D * 2;
+      row = p.v + (size_t)t * p.v_stride + (uint32_t)((it.h - p.Hq - p.Hkv) * p.D * 2);
     const u32x4* const vectors = reinterpret_cast<const u32x4*>(row);
     it.a = STREAM ? __builtin_nontemporal_load(vectors + va) : vectors[va];
     it.b = STREAM ? __builtin_nontemporal_load(vectors + vb) : vectors[vb];
@@ -92,7 +94,7 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p) {
     if (p.gk != nullptr) gain[1][0] = reinterpret_cast<const u32x4*>(p.gk)[va], gain[1][1] = reinterpret_cast<const u32x4*>(p.gk)[vb];
   }
   for (int w = (int)threadIdx.x; w < nt * half; w += kThreads) {
-    const int tl = p.tokens == 1 ? 0 : w / half;
+    const int tl = ONE ? 0 : w / half;
     const double in_turns = (double)p.pos[t0 + tl] * (double)p.freq[w - tl * half] * 0.15915494309189533577;  // / 2 pi
     float s, c;
     sincospif(2.0f * (float)(in_turns - rint(in_turns)), &s, &c);
@@ -130,16 +132,22 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p) {
         ss = lanes_sum<L>(ss);
         if (ss == kInf) ss = __builtin_nanf("");  // the head holds an infinity
       }
-      const float rstd = 1.0f / sqrtf(ss / (float)p.D + eps);
+      const float rstd = __builtin_amdgcn_rsqf(ss * p.by_d + eps);
+      u32x4 ga, gb;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {  // by element: an index into the registers would cost 15 times this
+        ga[e] = part == 0 ? gain[0][0][e] : gain[1][0][e];
+        gb[e] = part == 0 ? gain[0][1][e] : gain[1][1][e];
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint32_t wa = gain[part][0][e >> 1], wb = gain[part][1][e >> 1];
+        const uint32_t wa = ga[e >> 1], wb = gb[e >> 1];
         a[e] = a[e] * rstd * ((e & 1) ? bf16_hi(wa) : bf16_lo(wa));
         b[e] = b[e] * rstd * ((e & 1) ? bf16_hi(wb) : bf16_lo(wb));
       }
     }
     if (part != 2 && turns) {
-      const float2* const cs = turn + (p.tokens == 1 ? 0 : it.t - t0) * half + 8 * u;
+      const float2* const cs = turn + (ONE ? 0 : it.t - t0) * half + 8 * u;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float2 w = cs[e];
@@ -150,12 +158,13 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p) {
       }
     }
     if (!in_head) continue;
+    const int t = ONE ? t0 : it.t;
     uint8_t* out;
     bool codes = false;
     if (part == 0) {
-      out = p.q_out + (size_t)it.t * p.q_out_stride + (size_t)it.h * p.D * 2;
+      out = p.q_out + (size_t)t * p.q_out_stride + (uint32_t)(it.h * p.D * 2);
     } else {
-      const int64_t at = p.slots[it.t];
+      const int64_t at = p.slots[t];
       if (at < 0 || at >= p.n_slots) continue;  // padding, or past the cache
       const int h = it.h - p.Hq - (part == 2 ? p.Hkv : 0);
       out = (part == 1 ? p.kc : p.vc) + (size_t)(at >> p.page_shift) * p.page_stride +
@@ -184,15 +193,15 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p) {
   }
 }
 
-template <int L, bool STREAM>
+template <int L, bool STREAM, bool ONE>
 hipError_t launch_kind(const RopeParams& p, bool inter, bool codes, dim3 grid, size_t lds, hipStream_t s) {
   const dim3 block(kThreads);
   if (inter) {
-    if (codes) return launch(rope_kernel<L, true, true, STREAM>, grid, block, lds, s, p);
-    return launch(rope_kernel<L, true, false, STREAM>, grid, block, lds, s, p);
+    if (codes) return launch(rope_kernel<L, true, true, STREAM, ONE>, grid, block, lds, s, p);
+    return launch(rope_kernel<L, true, false, STREAM, ONE>, grid, block, lds, s, p);
   }
-  if (codes) return launch(rope_kernel<L, false, true, STREAM>, grid, block, lds, s, p);
-  return launch(rope_kernel<L, false, false, STREAM>, grid, block, lds, s, p);
+  if (codes) return launch(rope_kernel<L, false, true, STREAM, ONE>, grid, block, lds, s, p);
+  return launch(rope_kernel<L, false, false, STREAM, ONE>, grid, block, lds, s, p);
 }
 
 template <int L>
@@ -214,8 +223,10 @@ hipError_t launch_lanes(RopeParams p, bool inter, bool codes, hipStream_t s) {
   // heads, which it holds, 23.3 -> 26.1.
   const size_t bytes = (size_t)p.T * p.D * (4 * (size_t)p.Hq + (codes ? 6 : 8) * (size_t)p.Hkv);
   const dim3 grid(gx, gy);
-  if (bytes >= ((size_t)256 << 20)) return launch_kind<L, true>(p, inter, codes, grid, lds, s);
-  return launch_kind<L, false>(p, inter, codes, grid, lds, s);
+  p.by_d = 1.0f / (float)p.D;
+  if (bytes >= ((size_t)256 << 20))
+    return p.tokens == 1 ? launch_kind<L, true, true>(p, inter, codes, grid, lds, s) : launch_kind<L, true, false>(p, inter, codes, grid, lds, s);
+  return p.tokens == 1 ? launch_kind<L, false, true>(p, inter, codes, grid, lds, s) : launch_kind<L, false, false>(p, inter, codes, grid, lds, s);
 }
 
 }  // namespace
