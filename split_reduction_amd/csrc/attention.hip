@@ -728,12 +728,12 @@ __device__ __forceinline__ void rows_body(const AttnParams& p, int block, uint8_
 // ---- few rows: at most 32 of a key head, the waves split the keys ----
 //
 // What counts is the cache's stream. Every sequence and key head is cut into units
-// of 32 keys a wave, and one more for what a head costs beside its keys; the units
+// of 32 keys a wave, and some more for what a head costs beside its keys; the units
 // of the whole call, one sequence after another, are dealt out in equal runs to a
 // fixed number of workgroups, whatever the lengths are. A workgroup goes through
 // its run head by head; its waves take the unit's keys by 32, each through
-// buffers of its own with no barrier, and meet at the head's end. The loads run two
-// tiles ahead of the products, into the next head where one ends. A head that was
+// buffers of its own with no barrier, and meet at the head's end. The loads run as many
+// tiles ahead of the products as there are buffers, into the next head where one ends. A head that was
 // cut between workgroups is joined by the last to arrive, from slots in the
 // workspace, in the order of its keys.
 //
@@ -800,6 +800,7 @@ struct FewCursor {
     while (u < ue) {
       const uint64_t past = __ballot(end > u);
       if (past == 0) {
+        if (chunk + 64 >= p.B) return false;  // only where the lengths change under the kernel
         more(p, lane, (uint32_t)__builtin_amdgcn_readlane((int)end, 63));
         continue;
       }
