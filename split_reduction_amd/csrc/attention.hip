@@ -1140,14 +1140,15 @@ int64_t tiles_bound(const AttnParams& p, int waves) {
 
 // Workgroups that split the keys of each tile where the tiles alone leave CUs idle:
 // rounds of one workgroup a CU, S that leaves the fewest idle, the smallest of equal
-// ones; not below 512 keys a workgroup.
+// ones; not below 512 keys a workgroup. A kernel of less waves takes the same S as one
+// of `most_waves`, which fills the chip with one workgroup a CU.
 template <int D>
-int rows_splits(const AttnParams& p, int waves) {
-  const int64_t groups = tiles_bound(p, waves) * p.Hkv;
-  if (groups <= 0 || groups > kOpsCounters - kFewCounters) return 1;
+int rows_splits(const AttnParams& p, int waves, int most_waves) {
+  const int64_t slots = tiles_bound(p, waves) * p.Hkv, groups = tiles_bound(p, most_waves) * p.Hkv;
+  if (groups <= 0 || slots > kOpsCounters - kFewCounters) return 1;
   const int64_t keys = p.window > 0 && p.window + 32 * waves < p.max_len ? p.window + 32 * waves : p.max_len;
   int64_t most = (keys + kRowsKeys - 1) / kRowsKeys / 8;
-  const int64_t room = (int64_t)((kOpsPartBytes - few_part<D>()) / rows_part<D>(waves)) / groups;
+  const int64_t room = (int64_t)((kOpsPartBytes - few_part<D>()) / rows_part<D>(waves)) / slots;
   if (most > room) most = room;
   int best = 1;
   auto rounds = [&](int64_t s) { return (groups * s + kChipCUs - 1) / kChipCUs; };
@@ -1178,8 +1179,13 @@ hipError_t launch_format(AttnParams p, hipStream_t s) {
     // 32768 cached, keys split: 279 / 300; but heads of 64 360 / 342, a window of 1024
     // 199 / 183, 4 x 2048 of 16 heads 119 / 105, 500 tokens 24.7 / 19.6.
     constexpr int kMost = rows_waves<D, F8>();
-    p.S = rows_splits<D>(p, kMost);
-    const bool large = kMost == 8 && (p.S > 1 || (D == 128 && p.window == 0 && tiles_bound(p, 8) * p.Hkv >= 4 * kChipCUs));
+    // A batch whose keys are split stays with four: beside the few kernel, not before it,
+    // 12 sequences of up to 64 tokens over up to 8000 cached take 43 us against 88, 4 of up
+    // to 500 over 30000 341 / 411, 37 of up to 301 and heads of 64 32 / 54; but 8 x 64 over
+    // 16384 184 / 171, 2 of up to 1000 over 60000 365 / 332.
+    const bool full = D == 128 && p.window == 0 && tiles_bound(p, 8) * p.Hkv >= 4 * kChipCUs;
+    p.S = rows_splits<D>(p, few && !full ? 4 : kMost, kMost);  // for the waves that are launched, or 1
+    const bool large = kMost == 8 && (full || (p.S > 1 && !few));
     const int waves = large ? 8 : 4;
     const unsigned grid = (unsigned)(tiles_bound(p, waves) * p.Hkv * p.S);
     if constexpr (kMost == 8) {

@@ -169,6 +169,16 @@ def test_long(seqs, G, D, fmt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D,fmt", [(64, "bf16"), (64, "e4m3"), (128, "bf16"), (128, "e4m3"), (256, "bf16")])
+@pytest.mark.parametrize("G,Hkv,window", [(4, 2, 0), (1, 3, 0), (16, 1, 0), (7, 1, 3000)])
+def test_chunks_over_long_caches(D, fmt, G, Hkv, window):
+    """Batches whose keys are split, beside sequences of few rows that are split as well."""
+    c = Case([(70, 5000), (1, 6100), (0, 40), (300, 301), (33, 4097), (1, 1), (5, 2049), (129, 100)], Hkv, G, D, 16, fmt, "head", pad=1, seed=D + G)
+    log(f"attention chunks over long caches D={D} {fmt} G={G} Hkv={Hkv} window={window}")
+    c.check(*c.run(window), window, rows=lambda n: sorted({0, n // 3, n - 1}))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("window", [1, 16, 100, 2000, 2**31 - 1])
 @pytest.mark.parametrize("D,fmt", [(128, "bf16"), (64, "e4m3"), (256, "e4m3")])
 def test_window(window, D, fmt):
