@@ -89,7 +89,7 @@ struct Cache {
   static constexpr int kChunks = kRow / 16;
   static constexpr int kRows = 64 / kChunks;     // rows of one wave's load
   // What a row's chunk numbers are exchanged with. Keys are read by 32 rows, the
-  // same chunk of 8 neighbouring rows at once.
+  // same chunk of each: 8 neighbouring rows (16 of 256 bytes and more) take theirs apart.
   __device__ static __forceinline__ int key_swizzle(int row) {
     return kRow >= 256 ? row & 15 : kRow >= 128 ? row & 7 : (row >> 1) & 3;
   }
