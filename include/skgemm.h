@@ -407,8 +407,9 @@ SKGEMM_API int skgemm_rope_append(const void* Q, const void* K, const void* V, c
  *   One call takes prompts, chunks of them and single tokens in any mixture.
  *   Q, O        bf16 [T, Hq, D]; O may be Q (same stride).
  *   page_table  int32 [B, max_pages] (rows table_stride bytes apart): the page of
- *               tokens i * page_size .. of a sequence. What lies past its length is
- *               not read.
+ *               tokens i * page_size .. of a sequence. Entries past its length are
+ *               not used, nor with a window those of pages that lie wholly before
+ *               the first token that its first new one sees (given back, say).
  *   kv_len      int32 [B], at most max_pages * page_size; q_start int32 [B + 1],
  *               rising. Rows of Q before q_start[0] and from q_start[B] on are
  *               padding: their outputs are left as they were.

@@ -604,8 +604,9 @@ __device__ __forceinline__ void rows_body(const AttnParams& p, int block, uint8_
   const int place = seq.L - seq.n + 1;  // keys before and at token 0
   const int khi = max(0, place + tok1), see_min = place + tok0;
   const int klo = p.window > 0 ? max(0, place + tok0 - p.window) : 0, lo_max = p.window > 0 ? place + tok1 - p.window : 0;
-  const int kal = klo & ~(kRowsKeys - 1);
-  const int nk = khi > kal ? (khi - kal + kRowsKeys - 1) / kRowsKeys : 0;
+  // Tiles of keys from klo on, not from a multiple of their size: a page that no row
+  // sees may have been given back, so its id is not looked up.
+  const int nk = khi > klo ? (khi - klo + kRowsKeys - 1) / kRowsKeys : 0;
   const int j0 = (int)((int64_t)nk * split / p.S), j1 = (int)((int64_t)nk * (split + 1) / p.S);
 
   R w;
@@ -631,15 +632,15 @@ __device__ __forceinline__ void rows_body(const AttnParams& p, int block, uint8_
   Share<D, F8, 64, W> share;
 
   if (j0 < j1) {
-    issue_ids<64>(c, kal + 64 * j0, last, id_lds, lane);
-    issue_ids<64>(c, kal + 64 * (j0 + 1), last, id_lds + 256, lane);
+    issue_ids<64>(c, klo + 64 * j0, last, id_lds, lane);
+    issue_ids<64>(c, klo + 64 * (j0 + 1), last, id_lds + 256, lane);
     wait_vmem<0>();
-    bad = share.find(c, kal + 64 * j0, last, ids[wave][0], wave, lane);
+    bad = share.find(c, klo + 64 * j0, last, ids[wave][0], wave, lane);
     share.issue_both(c, k_lds, v_lds, wave, lane);
-    issue_ids<64>(c, kal + 64 * (j0 + 2), last, id_lds, lane);
+    issue_ids<64>(c, klo + 64 * (j0 + 2), last, id_lds, lane);
   }
   for (int j = j0; j < j1; ++j) {
-    const int at = (j - j0) & 1, base = kal + 64 * j;
+    const int at = (j - j0) & 1, base = klo + 64 * j;
     wait_vmem<1>();  // this wave's share of tile j; the ids of j + 2 may be under way
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     const uint32_t values = v_lds + (uint32_t)at * kHalf;
@@ -753,11 +754,12 @@ constexpr int kFewWaves = 4;
 constexpr uint32_t kHeadUnits = 3;
 constexpr uint32_t kFewShare = 4;
 
-// Units of keys of a sequence for each key head, and the first key.
+// Units of keys of a sequence for each key head, and the first key: the first that a
+// row sees, as in rows_body.
 __device__ __forceinline__ uint32_t few_units(const AttnParams& p, const Seq& s, int unit, int* first) {
   *first = 0;
   if (s.n == 0 || s.n * p.G > p.few) return 0;
-  const int lo = p.window > 0 ? max(0, s.L - s.n + 1 - p.window) & ~31 : 0;
+  const int lo = p.window > 0 ? max(0, s.L - s.n + 1 - p.window) : 0;
   *first = lo;
   return s.L > lo ? (uint32_t)(s.L - lo + unit - 1) / (uint32_t)unit : 1;  // a row that sees no key is written too
 }
