@@ -19,7 +19,10 @@
 //
 // The softmax runs in one pass with the running maximum m (in powers of two) and
 // sum l in FP32; O and l are rescaled only where a maximum grows by more than 2^8
-// (P stays below 2^8, bf16 has the same relative step there). P is rounded to bf16
+// (P stays below 2^8, bf16 has the same relative step there). An exponent is taken as
+// s c - m, one fused operation; m is rounded, so past 2^24 that is off by more than
+// half a power of two, and the score's own difference to the row's largest is taken
+// (a branch that only a grown maximum can turn on). P is rounded to bf16
 // for the second product, 2^-9 of each probability; l sums the unrounded ones.
 //
 // Keys and values come straight from memory into LDS, 16 bytes a lane, each row
@@ -46,6 +49,7 @@ typedef int i32x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kFloor = -1e30f;   // maximum of a row that has seen no key
 constexpr float kGrowth = 8.0f;    // powers of two that P may reach
+constexpr float kFar = 0x1p24f;    // maxima whose rounding shows in P
 constexpr float kLog2 = 0.69314718055994531f;
 
 __device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
@@ -185,6 +189,8 @@ struct Rows {
   bf16x8 q[RT][D / 16];
   f32x16 o[RT][kDT];
   float m[RT], l[RT];
+  float largest[RT];   // the score that m is of, as the product leaves it; 0: none yet
+  bool far[RT];        // some row of the wave has |m| >= kFar
   int lo[RT], hi[RT];  // keys that this lane's row sees
   uint32_t lost[RT][kDT / 2];  // bit 16 (d % 2) + e: element e of o[t][d] is NaN
 
@@ -193,6 +199,8 @@ struct Rows {
     for (int t = 0; t < RT; ++t) {
       m[t] = kFloor;
       l[t] = 0.0f;
+      largest[t] = 0.0f;
+      far[t] = false;
 #pragma unroll
       for (int d = 0; d < kDT; ++d) {
         o[t][d] = f32x16{};
@@ -314,6 +322,7 @@ struct Rows {
         }
   }
 
+  __device__ __forceinline__ bool is_far(int t) const { return largest[t] != 0.0f && fabsf(m[t]) >= kFar; }
   // Scores to probabilities: maximum, sum and O rescaled where it grows.
   __device__ __forceinline__ void softmax(f32x16 (&s)[RT][KB], bf16x8 (&p)[RT][KB][2], float c) {
 #pragma unroll
@@ -323,21 +332,36 @@ struct Rows {
       for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
         for (int e = 0; e < 16; ++e) top = fmaxf(top, s[t][kb][e]);
-      top = swap_max(top) * c;
+      const float score = swap_max(top);
+      top = score * c;
       if (D == 256 || __any(top > m[t] + kGrowth)) {
         // Each row by its own need: what it rounds does not hang on its neighbours.
-        const float now = top > m[t] + kGrowth ? top : m[t], by = __builtin_amdgcn_exp2f(m[t] - now);
+        const bool grows = top > m[t] + kGrowth;
+        const float now = grows ? top : m[t], by = __builtin_amdgcn_exp2f(m[t] - now);
         m[t] = now;
+        if (grows) largest[t] = score;
+        if (D < 256 || __any(grows)) far[t] = __any(is_far(t));
         l[t] *= by;
 #pragma unroll
         for (int d = 0; d < kDT; ++d) o[t][d] *= by;
+      }
+      float minus = m[t];
+      // The branch alone costs wide heads 3 % (8192 tokens of 16 heads of 256: 807 -> 835
+      // us; as 32 subtractions in every tile 832), others nothing.
+      if (__builtin_expect(far[t], false)) {
+        const float from = is_far(t) ? largest[t] : 0.0f;
+        if (is_far(t)) minus = 0.0f;
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[t][kb][e] -= from;
       }
       float sum = 0.0f;  // the tile's, so that long rows add few numbers of unlike size
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          s[t][kb][e] = __builtin_amdgcn_exp2f(fmaf(s[t][kb][e], c, -m[t]));
+          s[t][kb][e] = __builtin_amdgcn_exp2f(fmaf(s[t][kb][e], c, -minus));
           sum += s[t][kb][e];
         }
 #pragma unroll
