@@ -424,8 +424,9 @@ SKGEMM_API int skgemm_rope_append(const void* Q, const void* K, const void* V, c
  * The lengths are read on the device, so a captured call may be replayed with
  * others. It uses the workspace above (skgemm_reserve_ops before a capture).
  * Sums, maxima and O are FP32; the probabilities are rounded to bf16 for the product
- * with V. A row that sees no token (p < 0) has O 0 and lse -inf, and so has one
- * whose scores are all below -1e30. Tokens that a row does not see have no part in
+ * with V. Scores may be as large as FP32 holds: up to 2e38 before and after scale
+ * (past that a row is not right). A row that sees no token (p < 0), or none but with
+ * scores of -inf, has O 0 and lse -inf. Tokens that a row does not see have no part in
  * it, whatever their keys and values hold; an infinity or a NaN in a key that it
  * sees makes the row NaN (a score of -inf: probability 0), in a value that output
  * NaN or infinite. A page id outside 0 .. n_pages - 1 is not read; rows that see its

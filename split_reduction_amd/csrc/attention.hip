@@ -47,7 +47,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 #define SKG_LDS __attribute__((address_space(3)))
 
-constexpr float kFloor = -1e30f;   // maximum of a row that has seen no key
+constexpr float kFloor = -3.402823466e38f;  // maximum of a row that has seen no key: FP32's lowest
 constexpr float kGrowth = 8.0f;    // powers of two that P may reach
 constexpr float kFar = 0x1p24f;    // maxima whose rounding shows in P
 constexpr float kLog2 = 0.69314718055994531f;

@@ -17,7 +17,8 @@ def check_equal_scores(n, L, D, scores, lower):
     power of two with an exponent that is off by less than half a step of s / log 2, and
     the others none (they are s / 16 lower, far below 2^-200). The values
     are small whole numbers: their sums are exact but for the p in front, so O is off by
-    p's rounding, the sums' (L + 64 in FP32), the division (2) and the rounding to bf16.
+    p's rounding, the sums' (L + 64 in FP32), the division (2) and the rounding to bf16. A score of -inf
+    is no key: a row of nothing else has 0 and -inf.
     s is one product of bf16 numbers, times the scale and a factor (3 roundings); lse
     turns it back (2), adding log L (1)."""
     t = torch()
@@ -37,15 +38,19 @@ def check_equal_scores(n, L, D, scores, lower):
     table = t.arange(pages, dtype=t.int32, device=DEV).view(1, -1)
     lens, start = t.tensor([L], dtype=t.int32, device=DEV), t.tensor([0, n], dtype=t.int32, device=DEV)
     for s in scores:
-        x = t.tensor(-s / 2.0**60 * 8).to(t.bfloat16)  # scale 1 / 8
-        s = -float(x) * 2.0**60 / 8
+        x = t.tensor(-s / 2.0**60 * 8 if np.isfinite(s) else 1.0).to(t.bfloat16)  # scale 1 / 8
+        s = -float(x) * 2.0**60 / 8 if np.isfinite(s) else s
         q = t.zeros(n, G, D, dtype=t.bfloat16, device=DEV)
         q[..., 3] = x
+        kc[..., 3] *= float("inf") if np.isinf(s) else 1.0
         o = t.full((n, G, D), 7.0, dtype=t.bfloat16, device=DEV)
         lse = t.full((n, G), 7.0, device=DEV)
         sk.skgemm_paged_attention(q, kc, vc, table, lens, start, o, lse, n, 1, n, G, 1, D, pages, page, pages, 0.125)
         t.cuda.synchronize()
         got, gl = o.double().cpu().numpy(), lse.double().cpu().numpy()
+        if np.isinf(s):
+            assert (got == 0).all() and np.isneginf(gl).all()
+            continue
         for i in range(n):
             seen = values[: L - n + i + 1][top[: L - n + i + 1]]
             ref, size = seen.mean(0), np.abs(seen).mean(0)
@@ -62,3 +67,11 @@ def test_scores_of_any_size(n, L, D, sign):
     scores = [sign * s for s in (1e7, 3.3e9, 4.7e9, 1.1e10, 1.3e13, 2.9e17, 7e20, 1e25, 5.7e29)]
     check_equal_scores(n, L, D, scores, None)
     check_equal_scores(n, L, D, scores, 1 - sign * 2.0**-4)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,L", SIZES)
+def test_scores_near_the_lowest(n, L, D):
+    log(f"attention near the lowest score n={n} L={L} D={D}")
+    check_equal_scores(n, L, D, (-0.5e30, -0.75e30, -0.98e30, -1.02e30, -3e30, -1e36, -3e37, -np.inf), None)
