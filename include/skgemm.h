@@ -382,8 +382,8 @@ SKGEMM_API int skgemm_rope(const void* X, const void* G, const float* inv_freq,
  *   slots int64 [T]: token t goes to page slots[t] / page_size, token slots[t] %
  *   page_size of it. A slot below 0 (padding) or past the cache's n_pages is not
  *   stored. The same slot twice: one of the two, which is not said.
- *   E4M3 codes are of value / k_scale (v_scale), saturated to +-448, to nearest
- *   even; a NaN keeps its code. Outputs must not overlap (SKGEMM_EINVAL where the
+ *   E4M3 codes are of value / k_scale (v_scale), the quotient of FP32 rounded to
+ *   nearest and saturated to +-448, to nearest even; a NaN keeps its code. Outputs must not overlap (SKGEMM_EINVAL where the
  *   strides say so).
  */
 SKGEMM_API int skgemm_rope_append(const void* Q, const void* K, const void* V, const void* Gq,

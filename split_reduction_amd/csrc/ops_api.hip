@@ -137,6 +137,12 @@ int check_cache(const void* K, const void* V, int Hkv, int D, int n_pages, int p
   return SKGEMM_OK;
 }
 
+skg::CodeScale code_scale(float scale) {
+  int e = 0;
+  const float b = 2.0f * frexpf(scale, &e);
+  return {ldexpf(1.0f, 1 - e), b, 1.0f / b, 448.0f * b};
+}
+
 int log2_of(int v) { return __builtin_ctz((unsigned)v); }
 
 }  // namespace
@@ -415,8 +421,8 @@ SKGEMM_API int skgemm_rope_append(const void* Q, const void* K, const void* V, c
   if (Hkv > 0) {
     p.n_slots = (int64_t)n_pages * page_size;
     p.page_shift = log2_of(page_size);
-    p.k_inv = 1.0f / k_scale;
-    p.v_inv = 1.0f / v_scale;
+    p.k_by = code_scale(k_scale);
+    p.v_by = code_scale(v_scale);
   }
   const hipError_t e = skg::launch_rope(p, layout == SKGEMM_ROPE_INTERLEAVED, Hkv > 0 && cache_format == SKGEMM_E4M3, stream);
   return e == hipSuccess ? SKGEMM_OK : skg::hip_fail(e);

@@ -74,6 +74,11 @@ struct LogprobGradParams {
   float scale;
 };
 
+// A cache's scale as the division by it needs it: scale = 2^e b, 1 <= b < 2.
+struct CodeScale {
+  float up, b, inv, most;  // 2^-e, b, 1 / b, 448 b
+};
+
 struct RopeParams {
   const uint8_t *q, *k, *v;  // bf16 rows of heads; k, v null where Hkv is 0
   const uint8_t *gq, *gk;    // bf16 [D] or null: no norm
@@ -85,7 +90,8 @@ struct RopeParams {
   size_t page_stride, slot_stride, head_stride;        // bytes, of both caches
   int64_t n_slots;
   int T, Hq, Hkv, D, rot, page_shift;
-  float eps, amplitude, k_inv, v_inv, by_d;  // by_d: 1 / D
+  float eps, amplitude, by_d;  // by_d: 1 / D
+  CodeScale k_by, v_by;
   int tokens, per;  // tokens of a workgroup; heads of one (blockIdx.y takes the next)
 };
 
