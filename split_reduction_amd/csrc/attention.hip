@@ -558,7 +558,7 @@ __device__ __forceinline__ bool arrive_last(uint32_t* cnt, uint32_t all, uint32_
 // against 567 us; operands read six to nine ahead instead of four: no gain.
 
 constexpr int kRowsKeys = 64;
-constexpr int kFewRows = 32;  // of a sequence's key head, at most, for the other form
+constexpr int kFewRows = 32;  // of a sequence's key head, at most, for the other form: the columns of its products
 
 // The workspace: the few rows' slots and counters first, then these.
 constexpr int kFewCounters = 2 * kChipCUs;
@@ -1201,27 +1201,28 @@ hipError_t launch_format(AttnParams p, hipStream_t s) {
   if (many) {
     // Eight waves of a workgroup share a tile's keys, which halves what comes from the
     // L2; two workgroups of four fill a CU as well, go at their own pace and waste
-    // less on short work. 8192 tokens of 32 heads of 128: 563 against 588 us, 512 over
-    // 32768 cached, keys split: 279 / 300; but heads of 64 360 / 342, a window of 1024
-    // 199 / 183, 4 x 2048 of 16 heads 119 / 105, 500 tokens 24.7 / 19.6.
+    // less on short work and in the last round. A single sequence takes eight where its
+    // keys are split (512 over 32768 cached: 279 us against 300 with four), or where they
+    // are many and its tiles last more than three rounds of the CUs. Eight / four waves (a
+    // pair is of one run) by rounds, 32 heads: 6000 tokens 2.9 329 / 319, 7000 3.4 421 / 428, 8192 4 551 / 568,
+    // 16384 8 2092 / 2189 (just 2 rounds, 4096, would take 154 / 168); by keys, at more than
+    // three rounds: 2048 193 / 191 and 385 / 375, 2500 285 / 277, 3500 260 / 264, 4096 340 / 345,
+    // 6000 695 / 715. Heads of 64 360 / 342, a window of 1024 199 / 183.
+    // A batch stays with four, beside the few kernel; eight would be a launch before it: 16 x 512 tokens of
+    // 64 heads 170 / 153, 64 of up to 300 over up to 1300 139 / 111, 24 of up to 2000 368 / 348,
+    // but 4 x 4096 605 / 620, 16 x 512 over 4000 1027 / 1074; with keys split 12 of up to 64 over
+    // up to 8000 88 / 42, 4 of up to 500 over 30000 405 / 335, but 8 x 64 over 16384 173 / 183,
+    // 2 of up to 1000 over 60000 333 / 360.
     constexpr int kMost = rows_waves<D, F8>();
-    // A batch whose keys are split stays with four: beside the few kernel, not before it,
-    // 12 sequences of up to 64 tokens over up to 8000 cached take 43 us against 88, 4 of up
-    // to 500 over 30000 341 / 411, 37 of up to 301 and heads of 64 32 / 54; but 8 x 64 over
-    // 16384 184 / 171, 2 of up to 1000 over 60000 365 / 332.
-    const bool full = D == 128 && p.window == 0 && tiles_bound(p, 8) * p.Hkv >= 4 * kChipCUs;
-    p.S = rows_splits<D>(p, few && !full ? 4 : kMost, kMost);  // for the waves that are launched, or 1
-    const bool large = kMost == 8 && (full || (p.S > 1 && !few));
-    const int waves = large ? 8 : 4;
-    const unsigned grid = (unsigned)(tiles_bound(p, waves) * p.Hkv * p.S);
+    const bool long_rounds = D == 128 && p.window == 0 && p.max_len >= 3000 && tiles_bound(p, 8) * p.Hkv > 3 * kChipCUs;
+    p.S = rows_splits<D>(p, few ? 4 : kMost, kMost);  // for the waves that are launched, or 1
+    const bool eight = kMost == 8 && !few && (long_rounds || p.S > 1);
+    const unsigned grid = (unsigned)(tiles_bound(p, eight ? 8 : 4) * p.Hkv * p.S);
+    if (few) return launch(attn_mixed_kernel<D, F8>, dim3(few_blocks + grid), dim3(256), 0, s, p, (int)few_blocks);
     if constexpr (kMost == 8) {
-      if (large) {
-        const hipError_t e = launch(attn_rows_kernel<D, F8, 8>, dim3(grid), dim3(512), 0, s, p);
-        if (e != hipSuccess || !few) return e;
-      }
+      if (eight) return launch(attn_rows_kernel<D, F8, 8>, dim3(grid), dim3(512), 0, s, p);
     }
-    if (!large && few) return launch(attn_mixed_kernel<D, F8>, dim3(few_blocks + grid), dim3(256), 0, s, p, (int)few_blocks);
-    if (!large) return launch(attn_rows_kernel<D, F8, 4>, dim3(grid), dim3(256), 0, s, p);
+    return launch(attn_rows_kernel<D, F8, 4>, dim3(grid), dim3(256), 0, s, p);
   }
   return launch(attn_few_kernel<D, F8>, dim3(few_blocks), dim3(64 * kFewWaves), 0, s, p);
 }
