@@ -18,8 +18,9 @@
 // radians.
 //
 // Bound by memory (4 bytes an element of the queries, 6 or 8 of keys and values)
-// and below that by the launch. T=8192 of 64 heads of 128: 48.7 us, 5.5 TB/s (a large
-// copy reaches 5.1), with 8 key heads into E4M3 58 us; T=1 of 16: 3.3 us, the call 7.5.
+// and below that by the launch. Other inputs in every call: T=8192 of 64 heads of 128, half
+// of each turned, 52.7 us, 5.1 TB/s (as a large copy), with 8 key heads into E4M3 61.3; T=1
+// of 16: 3.3 us. Non-temporal loads: between 3 % faster and 5 % slower at 100 MB to 1 GB.
 
 #include "device/pack.h"
 #include "device/wave.h"
@@ -56,9 +57,9 @@ __device__ __forceinline__ float to_code_range(float v, const CodeScale& s) {
   return fmaf(fmaf(-q, s.b, v), s.inv, q);
 }
 
-// STREAM: heads are loaded non-temporally. ONE: a workgroup has heads of one token, so
-// that what goes by the token is the same in all lanes.
-template <int L, bool INTER, bool CODES, bool STREAM, bool ONE>
+// ONE: a workgroup has heads of one token, so that what goes by the token is the same
+// in all lanes.
+template <int L, bool INTER, bool CODES, bool ONE>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p) {
   constexpr int kSlots = kThreads / L;  // heads at once
   extern __shared__ float2 turn[];      // [tokens of the workgroup][rot / 2]: cos, sin
@@ -91,8 +92,8 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p) {
     else
       row = p.v + (size_t)t * p.v_stride + (uint32_t)((it.h - p.Hq - p.Hkv) * p.D * 2);
     const u32x4* const vectors = reinterpret_cast<const u32x4*>(row);
-    it.a = STREAM ? __builtin_nontemporal_load(vectors + va) : vectors[va];
-    it.b = STREAM ? __builtin_nontemporal_load(vectors + vb) : vectors[vb];
+    it.a = vectors[va];
+    it.b = vectors[vb];
     return it;
   };
 
@@ -203,15 +204,15 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p) {
   }
 }
 
-template <int L, bool STREAM, bool ONE>
+template <int L, bool ONE>
 hipError_t launch_kind(const RopeParams& p, bool inter, bool codes, dim3 grid, size_t lds, hipStream_t s) {
   const dim3 block(kThreads);
   if (inter) {
-    if (codes) return launch(rope_kernel<L, true, true, STREAM, ONE>, grid, block, lds, s, p);
-    return launch(rope_kernel<L, true, false, STREAM, ONE>, grid, block, lds, s, p);
+    if (codes) return launch(rope_kernel<L, true, true, ONE>, grid, block, lds, s, p);
+    return launch(rope_kernel<L, true, false, ONE>, grid, block, lds, s, p);
   }
-  if (codes) return launch(rope_kernel<L, false, true, STREAM, ONE>, grid, block, lds, s, p);
-  return launch(rope_kernel<L, false, false, STREAM, ONE>, grid, block, lds, s, p);
+  if (codes) return launch(rope_kernel<L, false, true, ONE>, grid, block, lds, s, p);
+  return launch(rope_kernel<L, false, false, ONE>, grid, block, lds, s, p);
 }
 
 template <int L>
@@ -228,14 +229,9 @@ hipError_t launch_lanes(RopeParams p, bool inter, bool codes, hipStream_t s) {
     gy = (unsigned)((heads + kSlots - 1) / kSlots);
   }
   const size_t lds = (size_t)p.tokens * (size_t)(p.rot / 2) * sizeof(float2);  // at most 16 KB
-  // More than the last cache holds is loaded non-temporally: T=8192 of 64 heads of
-  // 128 51.6 -> 48.7 us; T=4096 of 32 and 8 heads, which it holds, 23.3 -> 26.1.
-  const size_t bytes = (size_t)p.T * p.D * (4 * (size_t)p.Hq + (codes ? 6 : 8) * (size_t)p.Hkv);
   const dim3 grid(gx, gy);
   p.by_d = 1.0f / (float)p.D;
-  if (bytes >= ((size_t)256 << 20))
-    return p.tokens == 1 ? launch_kind<L, true, true>(p, inter, codes, grid, lds, s) : launch_kind<L, true, false>(p, inter, codes, grid, lds, s);
-  return p.tokens == 1 ? launch_kind<L, false, true>(p, inter, codes, grid, lds, s) : launch_kind<L, false, false>(p, inter, codes, grid, lds, s);
+  return p.tokens == 1 ? launch_kind<L, true>(p, inter, codes, grid, lds, s) : launch_kind<L, false>(p, inter, codes, grid, lds, s);
 }
 
 }  // namespace
