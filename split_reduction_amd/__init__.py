@@ -38,7 +38,8 @@ FORMATS = {"bf16": 0, "i8": 1, "e4m3": 2, "f32": 3}
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 
 _lib = None
-_raw_stream = _device = None  # torch's functions, bound by the first call that asks for the stream
+_raw_stream = _device = None  # torch's functions, bound by the first call that asks for the stream or the device
+_gpus = None  # GPUs that this process sees, with them
 _torch_types = {}  # torch's element types that an operator's argument may have, filled by the first call
 
 
@@ -239,17 +240,20 @@ def _batched(L: int, stride: int, one: int) -> int:
     return 0 if L <= 0 or one == 0 else (L - 1) * max(stride, 0) + one
 
 
+def _bind() -> None:
+    global _raw_stream, _device, _gpus
+    import torch
+
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda _: torch.cuda.current_stream().cuda_stream)
+    _gpus = torch.cuda.device_count()
+    _device = torch.cuda.current_device
+
+
 def _current_stream() -> int:
     """torch's current stream on the current device, without the Stream object
     that torch.cuda.current_stream() builds (2.7 us of a call's 11)."""
-    global _raw_stream, _device
     if _device is None:
-        import torch
-
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if _raw_stream is None:
-            return torch.cuda.current_stream().cuda_stream
-        _device = torch.cuda.current_device
+        _bind()
     return _raw_stream(_device())
 
 
@@ -457,10 +461,17 @@ def _layout(name) -> int:
     return int(name)
 
 
-def _here(a, what: str) -> None:
-    """A tensor of another GPU than the current one, where the call is launched."""
-    if a is not None and not isinstance(a, int) and _device is not None and a.is_cuda and a.get_device() != _device():
-        raise SkgemmError(SKGEMM_EINVAL, f"{what}: a tensor on {a.device}, the current device is {_device()}")
+def _here(what: str, *tensors) -> None:
+    """Refuses tensors (in the order of their names) of another GPU than the current
+    one, where the call is launched. With one GPU there is nothing to look at."""
+    if _device is None:
+        _bind()
+    if _gpus < 2:
+        return
+    here = _device()
+    for i, a in enumerate(tensors):
+        if a is not None and not isinstance(a, int) and a.get_device() != here:
+            raise SkgemmError(SKGEMM_EINVAL, f"{what.split()[i]}: a tensor on GPU {a.get_device()}, the current device is {here}")
 
 
 def _pages(K, V, n_pages: int, page_size: int, Hkv: int, D: int, fmt, strides):
@@ -517,7 +528,7 @@ def skgemm_rope(X, G, inv_freq, positions, Y, T: int, H: int, D: int, rot: int, 
     x, xs = _heads(X, T, H, D, x_stride, "X")
     y, ys = _heads(Y, T, H, D, y_stride, "Y")
     st = _stream(stream)
-    _here(X, "X")
+    _here("X G inv_freq positions Y", X, G, inv_freq, positions, Y)
     code = lib().skgemm_rope(x, _ptr(G, 2 * _n(D), "G", ty["bf16"]), _ptr(inv_freq, 2 * _n(rot), "inv_freq", ty["f32"]),
                              _ptr(positions, 8 * _n(T), "positions", ty["i64"]), y, T, H, D, rot, _layout(layout), eps,
                              amplitude, xs, ys, st)
@@ -540,7 +551,7 @@ def skgemm_rope_append(Q, K, V, Gq, Gk, inv_freq, positions, slots, Q_out, K_cac
     o, os_ = _heads(Q_out, T, Hq, D, q_out_stride, "Q_out")
     kc, vc, f, page, slot, head = _pages(K_cache, V_cache, n_pages, page_size, Hkv, D, cache_format, cache_strides)
     st = _stream(stream)
-    _here(K, "K")
+    _here("Q K V Gq Gk inv_freq positions slots Q_out K_cache V_cache", Q, K, V, Gq, Gk, inv_freq, positions, slots, Q_out, K_cache, V_cache)
     code = lib().skgemm_rope_append(q, k, v, _ptr(Gq, 2 * _n(D), "Gq", bf16), _ptr(Gk, 2 * _n(D), "Gk", bf16),
                                     _ptr(inv_freq, 2 * _n(rot), "inv_freq", ty["f32"]),
                                     _ptr(positions, 8 * _n(T), "positions", i64), _ptr(slots, 8 * _n(T), "slots", i64), o, kc,
@@ -563,7 +574,7 @@ def skgemm_paged_attention(Q, K_cache, V_cache, page_table, kv_len, q_start, O, 
     t, ts = _rows(page_table, B, 4 * max_pages, table_stride, "page_table", i32)
     kc, vc, f, page, slot, head = _pages(K_cache, V_cache, n_pages, page_size, Hkv, D, cache_format, cache_strides)
     st = _stream(stream)
-    _here(Q, "Q")
+    _here("Q K_cache V_cache page_table kv_len q_start O lse", Q, K_cache, V_cache, page_table, kv_len, q_start, O, lse)
     code = lib().skgemm_paged_attention(q, kc, vc, t, _ptr(kv_len, 4 * _n(B), "kv_len", i32),
                                         _ptr(q_start, 4 * _n(B + 1), "q_start", i32), o,
                                         _ptr(lse, 4 * _n(T, Hq), "lse", ty["f32"]), T, B, max_q, Hq, Hkv, D, n_pages, page_size,
