@@ -417,10 +417,12 @@ SKGEMM_API int skgemm_rope_append(const void* Q, const void* K, const void* V, c
  *   max_q       at least every n: what the launch is sized for (a sequence's tokens
  *               past it are left out). window 0: none.
  *   D is 64, 128 or 256; Hq % Hkv == 0; max_pages * page_size <= SKGEMM_MAX_LEN; T
- *   * (Hq / Hkv) <= 2^30, B <= 2^20, and B * Hkv * (max_pages * page_size / 64 + 8)
- *   and (T * (Hq / Hkv) / 128 + B) * Hkv below 2^31 (SKGEMM_ESHAPE). 0 < scale <=
- *   SKGEMM_MAX_SCALE, also times k_scale. Q and O are 16-byte aligned with strides
- *   that are multiples of 16; arrays of int32 and float 4.
+ *   * (Hq / Hkv) <= 2^30, B <= 2^20, B * Hkv * (max_pages * page_size / 64 + 8) below
+ *   2^31 and, where max_q * (Hq / Hkv) > 32, so many tiles of 128 rows that (T * (Hq
+ *   / Hkv) / 128 + B) * Hkv, or B * Hkv times those of max_q tokens if that is less,
+ *   stays below 2^24 - 512 (SKGEMM_ESHAPE). 0 < scale <= SKGEMM_MAX_SCALE, and scale
+ *   * k_scale from 1e-37 to that. Q and O are 16-byte aligned with strides that are
+ *   multiples of 16; arrays of int32 and float 4.
  * The lengths are read on the device, so a captured call may be replayed with
  * others. It uses the workspace above (skgemm_reserve_ops before a capture).
  * Sums, maxima and O are FP32; the probabilities are rounded to bf16 for the product

@@ -1155,14 +1155,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_mixed_kernel(AttnP
     rows_body<D, F8, 4>(p, (int)blockIdx.x - few_blocks, lds);
 }
 
-// Tiles of the rows kernel at most: it has a workgroup for each, and those past
+// Tiles of BM rows at most: the rows kernel has a workgroup for each, and those past
 // what the lengths give end at once.
-int64_t tiles_bound(const AttnParams& p, int waves) {
-  const int64_t BM = 32 * waves;
-  const int64_t by_rows = (int64_t)p.T * p.G / BM + p.B;
-  const int64_t by_seq = (int64_t)p.B * (((int64_t)p.max_q * p.G + BM - 1) / BM);
+int64_t most_tiles(int T, int B, int max_q, int G, int BM) {
+  const int64_t by_rows = (int64_t)T * G / BM + B;
+  const int64_t by_seq = (int64_t)B * (((int64_t)max_q * G + BM - 1) / BM);
   return by_rows < by_seq ? by_rows : by_seq;
 }
+int64_t tiles_bound(const AttnParams& p, int waves) { return most_tiles(p.T, p.B, p.max_q, p.G, 32 * waves); }
 
 // Workgroups that split the keys of each tile where the tiles alone leave CUs idle:
 // rounds of one workgroup a CU, S that leaves the fewest idle, the smallest of equal
@@ -1228,6 +1228,10 @@ hipError_t launch_format(AttnParams p, hipStream_t s) {
 }
 
 }  // namespace
+
+int64_t attention_tiles(int T, int B, int max_q, int G) {
+  return (int64_t)max_q * G > kFewRows ? most_tiles(T, B, max_q, G, 128) : 0;
+}
 
 hipError_t launch_attention(const AttnParams& p, int D, bool codes, hipStream_t s) {
   switch (D) {

@@ -447,7 +447,7 @@ SKGEMM_API int skgemm_paged_attention(const void* Q, const void* K_cache, const 
   if (rc != SKGEMM_OK) return rc;
   const int64_t most = (int64_t)1 << 31, G = Hq / Hkv, len = (int64_t)max_pages * page_size;
   if (len > SKGEMM_MAX_LEN || T * G > ((int64_t)1 << 30) || B * (int64_t)Hkv * (len / 64 + 8) >= most ||
-      (T * G / 128 + B) * Hkv >= most)
+      skg::attention_tiles(T, B, max_q < T ? max_q : T, (int)G) * Hkv >= skg::kMostTiles)
     return SKGEMM_ESHAPE;
   const float c = scale * k_scale;
   if (!(c >= 1e-37f) || !(c <= SKGEMM_MAX_SCALE)) return SKGEMM_EINVAL;

@@ -113,6 +113,13 @@ struct AttnParams {
   uint32_t* cnt;     // arrival counters, kOpsCounterStride words apart
 };
 
+// Tiles of 128 rows of a key head in sequences of more than 32, at most.
+int64_t attention_tiles(int T, int B, int max_q, int G);
+// Of all key heads: a launch of a workgroup of 256 threads for each, and of 512 beside
+// them, stays below the 2^32 threads that a grid may have. (Where keys are split there
+// are less workgroups than counters times 64.)
+constexpr int64_t kMostTiles = ((int64_t)1 << 24) - 512;
+
 hipError_t launch_rope(const RopeParams& p, bool inter, bool codes, hipStream_t s);
 hipError_t launch_attention(const AttnParams& p, int D, bool codes, hipStream_t s);
 hipError_t launch_logprobs(const LogprobParams& p, bool f32, hipStream_t s);
