@@ -381,10 +381,11 @@ SKGEMM_API int skgemm_rope(const void* X, const void* G, const float* inv_freq,
  *   (same stride). Hq 0: keys and values alone; Hkv 0: queries alone.
  *   slots int64 [T]: token t goes to page slots[t] / page_size, token slots[t] %
  *   page_size of it. A slot below 0 (padding) or past the cache's n_pages is not
- *   stored. The same slot twice: one of the two, which is not said.
+ *   stored. The same slot twice: every 8 of its values are of one of the tokens,
+ *   which is not said, so a key may be of another one than its value.
  *   E4M3 codes are of value / k_scale (v_scale), the quotient of FP32 rounded to
- *   nearest and saturated to +-448, to nearest even; a NaN keeps its code. Outputs must not overlap (SKGEMM_EINVAL where the
- *   strides say so).
+ *   nearest and saturated to +-448, to nearest even; a NaN keeps its code. Outputs
+ *   must not overlap (SKGEMM_EINVAL where the strides say so).
  */
 SKGEMM_API int skgemm_rope_append(const void* Q, const void* K, const void* V, const void* Gq,
                                   const void* Gk, const float* inv_freq,
@@ -424,7 +425,11 @@ SKGEMM_API int skgemm_rope_append(const void* Q, const void* K, const void* V, c
  *   * k_scale from 1e-37 to that. Q and O are 16-byte aligned with strides that are
  *   multiples of 16; arrays of int32 and float 4.
  * The lengths are read on the device, so a captured call may be replayed with
- * others. It uses the workspace above (skgemm_reserve_ops before a capture).
+ * others. page_table, kv_len and q_start must not change until the call has ended:
+ * its workgroups read them each for itself, so rows would be lost or written outside
+ * their place, and what the call leaves in the workspace would spoil later calls on
+ * the stream until skgemm_release. It uses the workspace above (skgemm_reserve_ops
+ * before a capture).
  * Sums, maxima and O are FP32; the probabilities are rounded to bf16 for the product
  * with V. Scores may be as large as FP32 holds: up to 2e38 before and after scale
  * (past that a row is not right). A row that sees no token (p < 0), or none but with
