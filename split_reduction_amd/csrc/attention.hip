@@ -551,8 +551,8 @@ __device__ __forceinline__ bool arrive_last(uint32_t* cnt, uint32_t all, uint32_
 //
 // Four or eight waves of 32 rows share tiles of 64 keys, two buffers: the next
 // tile is on its way while one is multiplied. The matrix units bound it, with the
-// softmax's vector instructions beside them (about 180 of them and 32 exponentials for 32
-// matrix instructions): 8192 tokens of 32 heads of 128 take 550 us, 1.0 PFLOP/s of visible
+// softmax's vector instructions beside them (about 180, 32 exponentials among them, for 32
+// matrix instructions): 8192 tokens of 32 heads of 128 take 540 to 560 us, 1.0 PFLOP/s of visible
 // pairs, where a large library product reaches 1.22. Two waves of a SIMD in turns,
 // one multiplying while the other has the softmax, with two barriers a tile: 610
 // against 567 us; operands read six to nine ahead instead of four: no gain.
@@ -763,7 +763,7 @@ __device__ __forceinline__ void rows_body(const AttnParams& p, int block, uint8_
 // workspace, in the order of its keys.
 //
 // Bound by the cache's stream: 64 tokens over 213k cached of 8 key heads of 128, 873
-// MB, take 142 us, 6.1 TB/s (a read alone reaches 6.9); below about 30 MB by the chain
+// MB, take 145 us, 6.0 TB/s (a read alone reaches 7.0); below about 30 MB by the chain
 // of loads (lengths, page ids, keys) and one joining, 13 us.
 
 // Buffers of keys and of values of a wave: two, or where 160 KB hold only one.

@@ -19,8 +19,8 @@
 //
 // Bound by memory (4 bytes an element of the queries, 6 or 8 of keys and values)
 // and below that by the launch. Other inputs in every call: T=8192 of 64 heads of 128, half
-// of each turned, 52.7 us, 5.1 TB/s (as a large copy), with 8 key heads into E4M3 61.3; T=1
-// of 16: 3.3 us. Non-temporal loads: between 3 % faster and 5 % slower at 100 MB to 1 GB.
+// of each turned, 52 us, 5.2 TB/s (as a large copy), with 8 key heads into E4M3 60; T=1 of
+// 16: 2.4 us. Non-temporal loads: between 3 % faster and 5 % slower at 100 MB to 1 GB.
 
 #include "device/pack.h"
 #include "device/wave.h"
