@@ -1205,7 +1205,7 @@ hipError_t launch_format(AttnParams p, hipStream_t s) {
   if (many) {
     // Eight waves of a workgroup share a tile's keys, which halves what comes from the
     // L2; two workgroups of four fill a CU as well, go at their own pace and waste
-    // less on short work and in the last round. A single sequence takes eight where its
+    // less on short work and at the end. A single sequence takes eight where its
     // keys are split (512 over 32768 cached: 279 us against 300 with four), or where they
     // are many and its tiles last more than three rounds of the CUs. Eight / four waves (a
     // pair is of one run) by rounds, 32 heads: 6000 tokens 2.9 329 / 319, 7000 3.4 421 / 428, 8192 4 551 / 568,
